@@ -254,6 +254,111 @@ moe_status_t moe_layer_forward_host(const moe_layer_t* L, const uint16_t* x, int
                                     uint16_t* out, void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------------
+ * moe_norm_residual -- the norms on both sides of a block in one pass: the norm after a block (of
+ *   its output y), its gate, the residual sum with the residual scale, and the norm before the next
+ *   block. Per token row:
+ *     u  = y                          when w_post is NULL, else
+ *          y * rsqrt(mean_c(y_c^2) + eps) * (w_offset + w_post)
+ *     r' = residual_scale * residual + gate * u
+ *     x' = r' * rsqrt(mean_c(r'_c^2) + eps) * (w_offset + w_pre)
+ *   in FP32, x' from r' before r' is rounded; residual_out = r' in the residual's type and x_out =
+ *   bf16(x') are each rounded once (nearest even).
+ *   y: bf16 [T][H] or NULL (no gate * u term, w_post and gate NULL too: the norm of the first block);
+ *   residual: [T][H] of residual_dtype or NULL (that term is left out); one of the two is given.
+ *   residual_out and x_out: one of the two may be NULL; w_pre goes with x_out.
+ *   gate: NULL (1), or gate_dtype values, gate[t * gate_ld + c] with gate_per_channel, else
+ *   gate[t * gate_ld]; gate_ld = 0 uses one row for every token.
+ *   ld_*: elements between two rows. H % 8 == 0, 8 <= H <= 8192; every row starts on 16 bytes
+ *   (a gate of one value per token: on its own size); residual_out may be residual and x_out may be
+ *   y (the same address and row stride), no other overlap. An empty batch (T = 0) returns MOE_OK
+ *   after the shape check.
+ * ------------------------------------------------------------------------------------------- */
+enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1 };
+
+typedef struct {
+    int H;
+    const uint16_t* w_post; /* nullable, bf16 [H] */
+    const uint16_t* w_pre;  /* bf16 [H], NULL exactly when x_out is */
+    float eps;              /* >= 0 */
+    float w_offset;         /* 0, or 1 for weights stored around zero */
+    float residual_scale;
+    int residual_dtype;     /* MOE_DTYPE_*: residual and residual_out */
+    const void* gate;       /* nullable */
+    int gate_dtype;         /* MOE_DTYPE_* */
+    int gate_per_channel;   /* 1: a value per channel, 0: a value per row */
+    int64_t gate_ld;        /* elements between two tokens' gates, 0: the same for all */
+} moe_norm_t;
+
+moe_status_t moe_norm_residual(const moe_norm_t* N, const uint16_t* y, int64_t ld_y, const void* residual,
+                               int64_t ld_residual, int T, void* residual_out, int64_t ld_residual_out,
+                               uint16_t* x_out, int64_t ld_x, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * moe_select_experts -- routing of given logits by scores: the choice of k experts per token and
+ *   their weights, for routers other than moe_route_topk's softmax top-k. Per token:
+ *     s_e = softmax(logits)_e or sigmoid(logits_e);   c_e = s_e + bias_e  (the choice value)
+ *     groups (n_group > 1): expert e is in group e / (E / n_group); a group's value is its largest c
+ *        (MOE_GROUP_MAX) or the sum of its two largest (MOE_GROUP_TOP2; of one where it has one);
+ *        the topk_group groups of largest value stay, lowest group first on equal values
+ *     ids = the k experts of largest c in those groups, c non-increasing, lowest id first on equal c
+ *     w   = scale * s_ids  (renormalize: / the sum of the k scores; 0 where that sum is 0)
+ *   The bias moves the choice alone, never the weights. An expert whose logit is -inf or NaN has
+ *   score 0 and takes no part in the softmax; logits of +inf share the softmax equally. An expert
+ *   with such a logit, or whose c is -inf or NaN, is masked: it adds nothing to its group's value
+ *   (a group of masked experts alone comes last) and is chosen only after all others of the groups
+ *   that stay (lowest id first), with weight 0.
+ *   ids are those of exact arithmetic: values are compared in FP32 with a bound on their error, and
+ *   a token with two values nearer than that is decided again in FP64.
+ *   logits: logits_dtype (MOE_DTYPE_*) [T][E], rows ld >= E elements apart, naturally aligned;
+ *   topk_ids: int32 [T][k]; topk_w: FP32 [T][k]. 1 <= E <= 1024, 1 <= k <= 32, 1 <= n_group <= 32
+ *   dividing E, 1 <= topk_group <= n_group, k <= topk_group * (E / n_group). T = 0 returns MOE_OK
+ *   after the shape check.
+ * ------------------------------------------------------------------------------------------- */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 };
+
+typedef struct {
+    int E, k;
+    int score;              /* MOE_SCORE_* */
+    int n_group, topk_group;/* 1, 1: no groups */
+    int group_score;        /* MOE_GROUP_* */
+    int renormalize;        /* 1: the k weights are divided by their sum */
+    float scale;
+    const float* bias;      /* nullable, FP32 [E] */
+} moe_routing_t;
+
+moe_status_t moe_select_experts(const moe_routing_t* R, const void* logits, int logits_dtype, int64_t ld, int T,
+                                int32_t* topk_ids, float* topk_w, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * moe_adapter_add -- low-rank adapters of many requests at once beside a projection they share (for
+ *   example a whole MoE layer of NVFP4 weights, which stay as they are):
+ *     out[t] = bf16( y[t] + scale[a] * B_a (A_a x[t]) )     a = the adapter of t's request
+ *     out[t] = y[t]                                         a = -1: no adapter
+ *   The T rows are the requests' tokens one request after the other: request s has the rows
+ *   [seg_offsets[s], seg_offsets[s+1]) (lengths of 0 and 1 included) and the adapter
+ *   seg_adapter[s] in [-1, n). seg_offsets[0] = 0 and seg_offsets[S] = T, non-decreasing. What
+ *   breaks these rules is skipped (those rows of out are not written) and reported by
+ *   moe_read_device_status as MOE_ERR_INVALID_ARG.
+ *   x: bf16 [T][K]; y, out: bf16 [T][N]; ld_*: elements between two rows, every row on 16 bytes.
+ *   K and N multiples of 8 in [8, 16384]; rank r a multiple of 8 in [8, 128]; adapters of smaller
+ *   rank are padded with zeros. Sums are FP32; A_a x is held in 16 significant bits or more between
+ *   the two products. out may be y (the same address and row stride), no other overlap.
+ *   ws: >= 256 bytes. T = 0 returns MOE_OK after the shape check.
+ * ------------------------------------------------------------------------------------------- */
+typedef struct {
+    int n, r, K, N;
+    const uint16_t* a;      /* bf16 [n][r][K] */
+    const uint16_t* b;      /* bf16 [n][N][r] */
+    const float* scale;     /* FP32 [n] */
+} moe_adapters_t;
+
+moe_status_t moe_adapter_add(const moe_adapters_t* A, const uint16_t* x, int64_t ld_x, int T,
+                             const int32_t* seg_offsets, const int32_t* seg_adapter, int S, const uint16_t* y,
+                             int64_t ld_y, uint16_t* out, int64_t ld_out, void* ws, size_t ws_bytes,
+                             moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
  * moe_route_topk_noalloc -- moe_route_topk for callers that cannot give the library scratch
  *   memory: an application whose device memory is owned by another allocator and may not grow
  *   by extra cudaMalloc calls, or a decode loop that cannot afford cudaMalloc's implicit device

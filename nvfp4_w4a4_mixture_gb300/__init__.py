@@ -15,13 +15,16 @@ LIB_PATH = os.path.join(_HERE, "_lib", "libmoe_nvfp4.so")
 EPI_F32, EPI_BF16, EPI_SWIGLU_NVFP4 = 0, 1, 2
 SCHED_AUTO, SCHED_ACT_ON_M, SCHED_WEIGHTS_ON_M, SCHED_WIDE, SCHED_WIDE_ROWS = 0, 0x100, 0x200, 0x400, 0x800
 SCHED_WEIGHTS_RESIDENT = 0x1000
+DTYPE_BF16, DTYPE_F32 = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+GROUP_MAX, GROUP_TOP2 = 0, 1
 
 ENTRY_POINTS = (
     "moe_quantize_nvfp4", "moe_quantize_nvfp4_f32", "moe_route_topk", "moe_permute", "moe_prepack_nvfp4",
     "moe_grouped_gemm_nvfp4", "moe_combine", "moe_layer_forward", "moe_layer_forward_profiled", "moe_workspace_bytes",
     "moe_read_device_status", "moe_status_string", "moe_last_error_detail", "moe_route_topk_noalloc",
     "moe_layer_forward_host", "moe_workspace_bytes_host", "moe_layer_workspace_view",
-    "moe_set_wait_test_hook",
+    "moe_set_wait_test_hook", "moe_norm_residual", "moe_select_experts", "moe_adapter_add",
 )
 
 
@@ -46,6 +49,24 @@ class LayerView(ctypes.Structure):
         "bytes", "x_scale", "x_codes", "x_sf", "logits", "logits_ld", "topk_ids", "topk_w", "shared_g",
         "permutation_in_workspace", "expert_offsets", "perm_src", "src_perm", "row_token", "h_codes", "h_sf",
         "h_block_rows", "y", "route_first")]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("H", ctypes.c_int), ("w_post", ctypes.c_void_p), ("w_pre", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("w_offset", ctypes.c_float), ("residual_scale", ctypes.c_float), ("residual_dtype", ctypes.c_int),
+                ("gate", ctypes.c_void_p), ("gate_dtype", ctypes.c_int), ("gate_per_channel", ctypes.c_int),
+                ("gate_ld", ctypes.c_int64)]
+
+
+class RoutingDesc(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int), ("k", ctypes.c_int), ("score", ctypes.c_int), ("n_group", ctypes.c_int),
+                ("topk_group", ctypes.c_int), ("group_score", ctypes.c_int), ("renormalize", ctypes.c_int),
+                ("scale", ctypes.c_float), ("bias", ctypes.c_void_p)]
+
+
+class AdaptersDesc(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int), ("r", ctypes.c_int), ("K", ctypes.c_int), ("N", ctypes.c_int),
+                ("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
 
 
 _lib = None
@@ -97,6 +118,12 @@ def lib():
         L.moe_layer_forward_profiled.restype = i32
         L.moe_layer_forward_profiled.argtypes = [ctypes.POINTER(LayerDesc), vp, i32, vp, vp, vp, sz, vp,
                                                  ctypes.POINTER(vp), i32]
+        L.moe_norm_residual.restype = i32
+        L.moe_norm_residual.argtypes = [ctypes.POINTER(NormDesc), vp, i64, vp, i64, i32, vp, i64, vp, i64, vp]
+        L.moe_select_experts.restype = i32
+        L.moe_select_experts.argtypes = [ctypes.POINTER(RoutingDesc), vp, i32, i64, i32, vp, vp, vp]
+        L.moe_adapter_add.restype = i32
+        L.moe_adapter_add.argtypes = [ctypes.POINTER(AdaptersDesc), vp, i64, i32, vp, vp, i32, vp, i64, vp, i64, vp, sz, vp]
         _lib = L
     return _lib
 
@@ -376,4 +403,94 @@ def moe_layer_forward_profiled(layer, x, events, residual=None, out=None, ws=Non
     handles = (ctypes.c_void_p * len(events))(*[ctypes.c_void_p(e.cuda_event) for e in events])
     _check(lib().moe_layer_forward_profiled(ctypes.byref(layer.desc), _p(_bf16_bits(x)), T, _p(residual), _p(out),
                                             ws.ptr, ws.nbytes, _stream(), handles, len(events)))
+    return out
+
+
+def _cuda(t, name, dtype, *shape):
+    """t's data pointer, checked: a CUDA tensor of `dtype` and `shape` whose last dimension is contiguous."""
+    if t.dtype != dtype or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor of %s, got %s on %s" % (name, dtype, t.dtype, t.device))
+    if tuple(t.shape) != shape or (shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError("%s must have shape %s and a contiguous last dimension, got %s with strides %s"
+                         % (name, shape, tuple(t.shape), t.stride()))
+    return t.data_ptr()
+
+
+def moe_norm_residual(y, residual, w_post=None, w_pre=None, gate=None, residual_scale=1.0, eps=1e-6, w_offset=0.0,
+                      out=None):
+    """The norm after a block (of its output y, with w_post), its gate, the residual sum and the norm
+    before the next block (with w_pre): returns (residual_out, x_out), x_out None without w_pre.
+
+    y: bf16 [T, H] or None; residual: bf16 or fp32 [T, H] or None. gate: bf16 or fp32, [H] (per channel),
+    [T, 1] (per token), [T, H] or [1, 1]. out: optional (residual_out, x_out) to write into; an entry of
+    None is left out (x_out) or allocated (residual_out). Rows may be strided."""
+    like = y if y is not None else residual
+    if like is None:
+        raise ValueError("y and residual are both None")
+    T, H = like.shape
+    bf = torch.bfloat16
+    rt = residual.dtype if residual is not None else bf
+    if rt not in (bf, torch.float32):
+        raise TypeError("residual must be bf16 or fp32, got %s" % rt)
+    r_out, x_out = out if out is not None else (None, None)
+    if r_out is None:
+        r_out = torch.empty(T, H, dtype=rt, device=like.device)
+    if x_out is None and w_pre is not None:
+        x_out = torch.empty(T, H, dtype=bf, device=like.device)
+    g_ptr, g_type, g_channel, g_ld = None, 0, 0, 0
+    if gate is not None:
+        if gate.dim() == 1:
+            gate = gate.unsqueeze(0)
+        g_type = DTYPE_F32 if gate.dtype == torch.float32 else DTYPE_BF16
+        g_channel = int(gate.shape[1] != 1)
+        g_ptr = _cuda(gate, "gate", torch.float32 if g_type else bf, 1 if gate.shape[0] == 1 else T, H if g_channel else 1)
+        g_ld = gate.stride(0) if gate.shape[0] > 1 else 0
+    d = NormDesc(H, None if w_post is None else _cuda(w_post, "w_post", bf, H),
+                 None if w_pre is None else _cuda(w_pre, "w_pre", bf, H), eps, w_offset, residual_scale,
+                 int(rt == torch.float32), g_ptr, g_type, g_channel, g_ld)
+    y_ptr, y_ld = (None, 0) if y is None else (_cuda(y, "y", bf, T, H), y.stride(0))
+    r_ptr, r_ld = (None, 0) if residual is None else (_cuda(residual, "residual", rt, T, H), residual.stride(0))
+    x_ptr, x_ld = (None, 0) if x_out is None else (_cuda(x_out, "x_out", bf, T, H), x_out.stride(0))
+    _check(lib().moe_norm_residual(ctypes.byref(d), y_ptr, y_ld, r_ptr, r_ld, T, _cuda(r_out, "residual_out", rt, T, H),
+                                   r_out.stride(0), x_ptr, x_ld, _stream()))
+    return r_out, x_out
+
+
+def moe_select_experts(logits, k, bias=None, score=SCORE_SOFTMAX, n_group=1, topk_group=1, group_score=GROUP_MAX,
+                       renormalize=True, scale=1.0, out=None):
+    """The k experts of each token and their weights from logits [T, E] (bf16 or fp32, rows may be strided):
+    (ids int32 [T, k], weights fp32 [T, k]). bias: fp32 [E], for the choice alone. out: optional (ids, weights)."""
+    T, E = logits.shape
+    lt = DTYPE_F32 if logits.dtype == torch.float32 else DTYPE_BF16
+    ids, w = out if out is not None else (torch.empty(T, k, dtype=torch.int32, device=logits.device),
+                                          torch.empty(T, k, dtype=torch.float32, device=logits.device))
+    i_ptr, w_ptr = _cuda(ids, "ids", torch.int32, T, k), _cuda(w, "weights", torch.float32, T, k)
+    if not (ids.is_contiguous() and w.is_contiguous()):
+        raise ValueError("ids and weights must be contiguous")
+    d = RoutingDesc(E, k, score, n_group, topk_group, group_score, int(renormalize), scale,
+                    None if bias is None else _cuda(bias, "bias", torch.float32, E))
+    _check(lib().moe_select_experts(ctypes.byref(d), _cuda(logits, "logits", torch.float32 if lt else torch.bfloat16, T, E),
+                                    lt, logits.stride(0), T, i_ptr, w_ptr, _stream()))
+    return ids, w
+
+
+def moe_adapter_add(x, y, a, b, scale, seg_offsets, seg_adapter, out=None, ws=None):
+    """y + scale[i] * (x A_i^T) B_i^T per request, i its adapter (-1: y alone). x bf16 [T, K]; y bf16 [T, N];
+    a bf16 [n, r, K]; b bf16 [n, N, r]; scale fp32 [n]; request s has the rows seg_offsets[s] ..
+    seg_offsets[s + 1] (int32 [S + 1]) and the adapter seg_adapter[s] (int32 [S]). out: optional, may be y."""
+    T, K = x.shape
+    n, r, _ = a.shape
+    N = y.shape[1]
+    S = seg_adapter.shape[0]
+    bf, i32 = torch.bfloat16, torch.int32
+    if out is None:
+        out = torch.empty(T, N, dtype=bf, device=y.device)
+    if not (a.is_contiguous() and b.is_contiguous()):
+        raise ValueError("a and b must be contiguous")
+    ws = ws or _ws(4096)
+    d = AdaptersDesc(n, r, K, N, _cuda(a, "a", bf, n, r, K), _cuda(b, "b", bf, n, N, r), _cuda(scale, "scale", torch.float32, n))
+    _check(lib().moe_adapter_add(ctypes.byref(d), _cuda(x, "x", bf, T, K), x.stride(0), T,
+                                 _cuda(seg_offsets, "seg_offsets", i32, S + 1), _cuda(seg_adapter, "seg_adapter", i32, S), S,
+                                 _cuda(y, "y", bf, T, N), y.stride(0), _cuda(out, "out", bf, T, N), out.stride(0), ws.ptr,
+                                 ws.nbytes, _stream()))
     return out

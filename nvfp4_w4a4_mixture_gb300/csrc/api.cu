@@ -12,6 +12,7 @@
 
 #include "../../include/moe_nvfp4.h"
 
+#include "block.cuh"
 #include "kernels.cuh"
 
 namespace moe {
@@ -296,6 +297,9 @@ moe_status_t moe_read_device_status(void* ws, moe_stream_t stream)
     if (status & kDevTimeoutGemm) return fail(MOE_ERR_DEVICE_TIMEOUT, "device status 0x%x: grouped GEMM wait timed out", status);
     if (status & kDevTimeoutRouter) return fail(MOE_ERR_DEVICE_TIMEOUT, "device status 0x%x: router wait timed out", status);
     if (status & kDevTimeoutCombine) return fail(MOE_ERR_DEVICE_TIMEOUT, "device status 0x%x: combine wait timed out", status);
+    if (status & kDevTimeoutAdapter) return fail(MOE_ERR_DEVICE_TIMEOUT, "device status 0x%x: adapter wait timed out", status);
+    if (status & kDevBadSegment)
+        return fail(MOE_ERR_INVALID_ARG, "device status 0x%x: seg_offsets or seg_adapter outside its range", status);
     if (status & kDevBadExpertId) return fail(MOE_ERR_INVALID_ARG, "device status 0x%x: expert id outside [0, E)", status);
     return MOE_OK;
 }
@@ -530,6 +534,195 @@ moe_status_t moe_combine(const uint16_t* y, const float* topk_w, const float* sh
     MOE_TRY(check_device());
     MOE_CUDA(launch_combine(y, topk_w, shared_g, src_perm, T, k, H, residual, out, nullptr, static_cast<cudaStream_t>(stream)),
              "combine launch");
+    return MOE_OK;
+}
+
+// Whether the rows [T][width bytes] at a (stride ld bytes) and at b overlap in memory.
+static bool rows_overlap(const void* a, int64_t ld_a, int64_t width_a, const void* b, int64_t ld_b, int64_t width_b, int T)
+{
+    if (!a || !b || T <= 0) return false;
+    const char *a0 = static_cast<const char*>(a), *b0 = static_cast<const char*>(b);
+    return a0 < b0 + (T - 1) * ld_b + width_b && b0 < a0 + (T - 1) * ld_a + width_a;
+}
+
+// One tensor of rows: base and row stride on 16 bytes, the stride at least a row (T > 1).
+static moe_status_t check_rows(const char* name, const void* p, int64_t ld, int64_t width, int elem, int T)
+{
+    if (T > 1 && ld < width) return fail(MOE_ERR_INVALID_ARG, "%s: row stride %lld < row length %lld", name, (long long)ld, (long long)width);
+    if (!aligned(p, 16) || (T > 1 && ld * elem % 16))
+        return fail(MOE_ERR_MISALIGNED, "%s %p with row stride %lld: every row must start on 16 bytes", name, p, (long long)ld);
+    return MOE_OK;
+}
+
+moe_status_t moe_norm_residual(const moe_norm_t* N, const uint16_t* y, int64_t ld_y, const void* residual,
+                               int64_t ld_residual, int T, void* residual_out, int64_t ld_residual_out,
+                               uint16_t* x_out, int64_t ld_x, moe_stream_t stream)
+{
+    if (!N) return fail(MOE_ERR_INVALID_ARG, "norm is NULL");
+    const int H = N->H;
+    if (H < 8 || H > 8192 || H % 8) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "H=%d not a multiple of 8 in [8, 8192]", H);
+    if (T < 0) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "T=%d < 0", T);
+    if (N->residual_dtype != MOE_DTYPE_BF16 && N->residual_dtype != MOE_DTYPE_F32)
+        return fail(MOE_ERR_INVALID_ARG, "residual_dtype=%d", N->residual_dtype);
+    if (N->gate && N->gate_dtype != MOE_DTYPE_BF16 && N->gate_dtype != MOE_DTYPE_F32)
+        return fail(MOE_ERR_INVALID_ARG, "gate_dtype=%d", N->gate_dtype);
+    if (!(N->eps >= 0.0f)) return fail(MOE_ERR_INVALID_ARG, "eps=%g: must be >= 0", static_cast<double>(N->eps));
+    if (T == 0) return MOE_OK;  // an empty batch: nothing is read or written, the pointers may be NULL
+    if (!y && !residual) return fail(MOE_ERR_INVALID_ARG, "y and residual are both NULL");
+    if (!y && (N->w_post || N->gate)) return fail(MOE_ERR_INVALID_ARG, "w_post and gate need y");
+    if (!residual_out && !x_out) return fail(MOE_ERR_INVALID_ARG, "residual_out and x_out are both NULL");
+    if ((x_out != nullptr) != (N->w_pre != nullptr)) return fail(MOE_ERR_INVALID_ARG, "x_out and w_pre go together");
+    const int rs = N->residual_dtype == MOE_DTYPE_F32 ? 4 : 2, gs = N->gate_dtype == MOE_DTYPE_F32 ? 4 : 2;
+    if (y) MOE_TRY(check_rows("y", y, ld_y, H, 2, T));
+    if (residual) MOE_TRY(check_rows("residual", residual, ld_residual, H, rs, T));
+    if (residual_out) MOE_TRY(check_rows("residual_out", residual_out, ld_residual_out, H, rs, T));
+    if (x_out) MOE_TRY(check_rows("x_out", x_out, ld_x, H, 2, T));
+    if ((N->w_post && !aligned(N->w_post, 16)) || (N->w_pre && !aligned(N->w_pre, 16)))
+        return fail(MOE_ERR_MISALIGNED, "w_post and w_pre must be 16-byte aligned");
+    if (N->gate) {
+        if (N->gate_ld < 0) return fail(MOE_ERR_INVALID_ARG, "gate_ld=%lld < 0", (long long)N->gate_ld);
+        const int need = N->gate_per_channel ? 16 : gs;
+        if (!aligned(N->gate, need) || (T > 1 && N->gate_ld * gs % need))
+            return fail(MOE_ERR_MISALIGNED, "gate %p with row stride %lld: every row must start on %d bytes", N->gate,
+                        (long long)N->gate_ld, need);
+    }
+    const bool same_r = residual_out == residual && (T == 1 || ld_residual_out == ld_residual);
+    const bool same_y = static_cast<const void*>(x_out) == static_cast<const void*>(y) && (T == 1 || ld_x == ld_y);
+    const int64_t gw = N->gate_per_channel ? H : 1;
+    struct {
+        const void* p;
+        int64_t ld, width;
+    } const outs[2] = {{residual_out, ld_residual_out * rs, static_cast<int64_t>(H) * rs}, {x_out, ld_x * 2, static_cast<int64_t>(H) * 2}},
+            ins[5] = {{residual, ld_residual * rs, static_cast<int64_t>(H) * rs}, {y, ld_y * 2, static_cast<int64_t>(H) * 2},
+                      {N->gate, N->gate_ld * gs, gw * gs}, {N->w_post, 0, static_cast<int64_t>(H) * 2}, {N->w_pre, 0, static_cast<int64_t>(H) * 2}};
+    for (int o = 0; o < 2; ++o)
+        for (int i = 0; i < 5; ++i) {
+            if ((o == 0 && i == 0 && same_r) || (o == 1 && i == 1 && same_y)) continue;
+            if (rows_overlap(outs[o].p, outs[o].ld, outs[o].width, ins[i].p, ins[i].ld, ins[i].width, T))
+                return fail(MOE_ERR_INVALID_ARG, "%s overlaps an input", o ? "x_out" : "residual_out");
+        }
+    if (rows_overlap(outs[0].p, outs[0].ld, outs[0].width, outs[1].p, outs[1].ld, outs[1].width, T))
+        return fail(MOE_ERR_INVALID_ARG, "x_out overlaps residual_out");
+    MOE_TRY(check_device());
+    NormArgs a{};
+    a.T = T;
+    a.H = H;
+    a.y = y;
+    a.ld_y = T > 1 ? ld_y : H;
+    a.res = residual;
+    a.ld_res = T > 1 ? ld_residual : H;
+    a.res_f32 = rs == 4;
+    a.w_post = N->w_post;
+    a.w_pre = N->w_pre;
+    a.eps = N->eps;
+    a.w_offset = N->w_offset;
+    a.res_scale = N->residual_scale;
+    a.gate = N->gate;
+    a.gate_f32 = gs == 4;
+    a.gate_per_channel = N->gate_per_channel != 0;
+    a.gate_ld = T > 1 ? N->gate_ld : 0;
+    a.res_out = residual_out;
+    a.ld_res_out = T > 1 ? ld_residual_out : H;
+    a.x_out = x_out;
+    a.ld_x = T > 1 ? ld_x : H;
+    MOE_CUDA(launch_norm_residual(a, static_cast<cudaStream_t>(stream)), "norm launch");
+    return MOE_OK;
+}
+
+moe_status_t moe_select_experts(const moe_routing_t* R, const void* logits, int logits_dtype, int64_t ld, int T,
+                                int32_t* topk_ids, float* topk_w, moe_stream_t stream)
+{
+    if (!R) return fail(MOE_ERR_INVALID_ARG, "routing is NULL");
+    const int E = R->E, k = R->k, G = R->n_group;
+    if (E < 1 || E > 1024) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "E=%d outside [1, 1024]", E);
+    if (k < 1 || k > 32 || k > E) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "k=%d outside [1, min(E=%d, 32)]", k, E);
+    if (G < 1 || G > 32 || E % G) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "n_group=%d outside [1, 32] or no divisor of E=%d", G, E);
+    if (R->topk_group < 1 || R->topk_group > G) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "topk_group=%d outside [1, n_group=%d]", R->topk_group, G);
+    if (k > R->topk_group * (E / G))
+        return fail(MOE_ERR_UNSUPPORTED_SHAPE, "k=%d > %d experts in topk_group=%d groups", k, R->topk_group * (E / G), R->topk_group);
+    if (T < 0) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "T=%d < 0", T);
+    if (R->score != MOE_SCORE_SOFTMAX && R->score != MOE_SCORE_SIGMOID) return fail(MOE_ERR_INVALID_ARG, "score=%d", R->score);
+    if (R->group_score != MOE_GROUP_MAX && R->group_score != MOE_GROUP_TOP2)
+        return fail(MOE_ERR_INVALID_ARG, "group_score=%d", R->group_score);
+    if (logits_dtype != MOE_DTYPE_BF16 && logits_dtype != MOE_DTYPE_F32) return fail(MOE_ERR_INVALID_ARG, "logits_dtype=%d", logits_dtype);
+    if (T == 0) return MOE_OK;  // an empty batch: nothing is read or written, the pointers may be NULL
+    if (!logits || !topk_ids || !topk_w) return fail(MOE_ERR_INVALID_ARG, "NULL tensor pointer");
+    if (T > 1 && ld < E) return fail(MOE_ERR_INVALID_ARG, "logits: row stride %lld < E=%d", (long long)ld, E);
+    if (!aligned(logits, logits_dtype == MOE_DTYPE_F32 ? 4 : 2) || !aligned(topk_ids, 4) || !aligned(topk_w, 4) ||
+        (R->bias && !aligned(R->bias, 4)))
+        return fail(MOE_ERR_MISALIGNED, "logits, bias, topk_ids and topk_w must be aligned to their elements");
+    const int64_t es = logits_dtype == MOE_DTYPE_F32 ? 4 : 2, ob = static_cast<int64_t>(k) * 4;
+    if (rows_overlap(topk_ids, ob, ob, logits, ld * es, E * es, T) || rows_overlap(topk_w, ob, ob, logits, ld * es, E * es, T) ||
+        rows_overlap(topk_ids, ob, ob, topk_w, ob, ob, T))
+        return fail(MOE_ERR_INVALID_ARG, "topk_ids, topk_w and logits overlap");
+    MOE_TRY(check_device());
+    SelectArgs a{};
+    a.T = T;
+    a.E = E;
+    a.k = k;
+    a.sigmoid = R->score == MOE_SCORE_SIGMOID;
+    a.n_group = G;
+    a.topk_group = R->topk_group;
+    a.group_top2 = R->group_score == MOE_GROUP_TOP2;
+    a.renormalize = R->renormalize != 0;
+    a.scale = R->scale;
+    a.bias = R->bias;
+    a.logits = logits;
+    a.logits_f32 = es == 4;
+    a.ld = T > 1 ? ld : E;
+    a.ids = topk_ids;
+    a.w = topk_w;
+    MOE_CUDA(launch_select_experts(a, static_cast<cudaStream_t>(stream)), "expert selection launch");
+    return MOE_OK;
+}
+
+moe_status_t moe_adapter_add(const moe_adapters_t* A, const uint16_t* x, int64_t ld_x, int T,
+                             const int32_t* seg_offsets, const int32_t* seg_adapter, int S, const uint16_t* y,
+                             int64_t ld_y, uint16_t* out, int64_t ld_out, void* ws, size_t ws_bytes,
+                             moe_stream_t stream)
+{
+    if (!A) return fail(MOE_ERR_INVALID_ARG, "adapters is NULL");
+    const int n = A->n, r = A->r, K = A->K, N = A->N;
+    if (n < 1) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "n=%d < 1", n);
+    if (r < 8 || r > kAdapterMaxRank || r % 8) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "r=%d not a multiple of 8 in [8, %d]", r, kAdapterMaxRank);
+    if (K < 8 || K > 16384 || K % 8 || N < 8 || N > 16384 || N % 8)
+        return fail(MOE_ERR_UNSUPPORTED_SHAPE, "K=%d N=%d: multiples of 8 in [8, 16384]", K, N);
+    if (T < 0 || S < 0) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "T=%d S=%d: negative", T, S);
+    if (T == 0) return MOE_OK;  // an empty batch: nothing is read or written, the pointers may be NULL
+    if (S < 1) return fail(MOE_ERR_INVALID_ARG, "S=%d: no request holds the T=%d rows", S, T);
+    if (!A->a || !A->b || !A->scale || !x || !seg_offsets || !seg_adapter || !y || !out)
+        return fail(MOE_ERR_INVALID_ARG, "NULL tensor pointer");
+    MOE_TRY(check_rows("x", x, ld_x, K, 2, T));
+    MOE_TRY(check_rows("y", y, ld_y, N, 2, T));
+    MOE_TRY(check_rows("out", out, ld_out, N, 2, T));
+    if (!aligned(A->a, 16) || !aligned(A->b, 16) || !aligned(A->scale, 4) || !aligned(seg_offsets, 4) || !aligned(seg_adapter, 4))
+        return fail(MOE_ERR_MISALIGNED, "a and b must be 16-byte, scale, seg_offsets and seg_adapter 4-byte aligned");
+    const int64_t kb = static_cast<int64_t>(K) * 2, nb = static_cast<int64_t>(N) * 2;
+    if (rows_overlap(out, ld_out * 2, nb, x, ld_x * 2, kb, T)) return fail(MOE_ERR_INVALID_ARG, "out overlaps x");
+    if (!(out == y && (T == 1 || ld_out == ld_y)) && rows_overlap(out, ld_out * 2, nb, y, ld_y * 2, nb, T))
+        return fail(MOE_ERR_INVALID_ARG, "out overlaps y without being y");
+    MOE_TRY(check_ws(ws, ws_bytes, sizeof(WsHeader)));
+    MOE_TRY(check_device());
+    AdapterArgs a{};
+    a.T = T;
+    a.S = S;
+    a.n = n;
+    a.r = r;
+    a.K = K;
+    a.N = N;
+    a.a = A->a;
+    a.b = A->b;
+    a.scale = A->scale;
+    a.x = x;
+    a.ld_x = T > 1 ? ld_x : K;
+    a.seg_offsets = seg_offsets;
+    a.seg_adapter = seg_adapter;
+    a.y = y;
+    a.ld_y = T > 1 ? ld_y : N;
+    a.out = out;
+    a.ld_out = T > 1 ? ld_out : N;
+    a.status = &static_cast<WsHeader*>(ws)->status;
+    MOE_CUDA(launch_adapter_add(a, device_sm_count(), static_cast<cudaStream_t>(stream)), "adapter launch");
     return MOE_OK;
 }
 
