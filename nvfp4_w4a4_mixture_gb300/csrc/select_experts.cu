@@ -1,65 +1,189 @@
 // select_experts.cu -- the choice of k experts per token from given logits: softmax or sigmoid
 // scores, a bias for the choice alone, groups, top-k, weights.
-// One warp per token, every value in FP64: scores and choice values in shared memory, the groups'
-// values by one lane per group, then k rounds of a warp arg-max (lowest id first on equal values).
+//
+// One warp per token, the E choice values c in registers (kNper a lane). Without a bias c is the
+// logit itself (a larger logit is a larger score), so the order is exact; with one, c = score + bias
+// in FP32 with an error of at most eps.
+//   groups   c goes to shared memory, 32 / n_group lanes (a power of two) take a group's two largest
+//            values, a warp-wide rank count keeps topk_group groups, the others' c become -inf
+//   choice   the 32 lane maxima are sorted across the lanes; the (k + 1)-th is a lower bound of the
+//            (k + 1)-th largest value, and the few values that reach it are compacted into a list
+//            and ranked by (c descending, id ascending)
+//   exact    where two neighbours of the ranking, or the last group that stays and the first that
+//            goes, are nearer than their errors, the candidates are ranked again in FP64
+//            (exact_ranking, exact_groups). FP64 runs at 1/64 of the FP32 rate, so only the values
+//            that can matter are computed again
+//   others   rows with fewer unmasked experts than k, more than kMaxCand candidates (many equal
+//            logits) or logits of +inf (whole_row)
+// The weights are computed from the chosen logits alone.
 #include "block.cuh"
 
 namespace moe {
 
 namespace {
 
-constexpr int kWarps = 4, kMaxE = 1024;
+constexpr int kWarps = 4;
 constexpr unsigned kFull = 0xFFFFFFFFu;
+constexpr int kMaxCand = 128;  // of E <= 1024 values; ranked in FP64 in the same scratch
+
+// Bounds of a score's error relative to the row's largest possible score (1; softmax: the row's
+// largest). Exponential 2^(x log2 e): ex2.approx is off by 2^-22, its argument by 1.5 * 2^-24 |x|
+// (the softmax's x = l - m by 2^-24 |x| more). Sigmoid: that error counts s (1 - s) times (at most
+// 8e-8 in all), the sum and rcp.approx add 2^-24 and 2^-23: 2.6e-7, taken as 6e-7. Softmax: a term's
+// own error is at most 2.6e-7 of the largest; the sum of up to 1024 terms, 37 roundings deep, is off
+// by 3.3e-6, a factor that all scores of the row share: two of them compare within 3.8e-6, two pairs
+// within 7.6e-6, taken as 2 and 4 times 2.5e-6.
+constexpr float kEpsSigmoid = 6e-7f, kEpsSoftmax = 2.5e-6f, kEpsAdd = 6e-8f;
 
 __device__ __forceinline__ bool ahead(double c, int e, double d, int f) { return c > d || (c == d && e < f); }
 
+template <bool F32>
 __device__ __forceinline__ float load_logit(const SelectArgs& a, int64_t t, int e)
 {
-    return a.logits_f32 ? static_cast<const float*>(a.logits)[t * a.ld + e]
-                        : bf16_to_f32(static_cast<const uint16_t*>(a.logits)[t * a.ld + e]);
+    return F32 ? static_cast<const float*>(a.logits)[t * a.ld + e]
+               : bf16_to_f32(static_cast<const uint16_t*>(a.logits)[t * a.ld + e]);
 }
 
-__global__ void __launch_bounds__(kWarps * 32) k_select_experts(const SelectArgs a)
+__device__ __forceinline__ float fast_exp(float x)
 {
-    __shared__ double c_s[kWarps][kMaxE];
-    ptx::griddep_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-    if (t >= a.T) return;
-    double* c = c_s[warp];
-    const double ninf = -INFINITY, nan = NAN;
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+    return r;
+}
 
-    float m = -INFINITY;
-    double sum = 0.0;
-    if (!a.sigmoid) {
-        for (int e = lane; e < a.E; e += 32) m = fmaxf(m, load_logit(a, t, e));
+__device__ __forceinline__ float fast_rcp(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ float warp_max(float v)
+{
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-        for (int e = lane; e < a.E; e += 32) {
-            const float l = load_logit(a, t, e);
-            if (l > -INFINITY) sum += l == m ? 1.0 : exp(static_cast<double>(l) - static_cast<double>(m));
-        }
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+    return v;
+}
+
+__device__ __forceinline__ float warp_sum(float v)
+{
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-    }
-    auto score = [&](float l) {
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+
+// Scores in FP64. m: the row's largest logit (softmax); sum: its softmax sum, or 1 where only the
+// order or ratios of scores are asked for.
+struct Exact {
+    bool sigmoid;
+    double m, sum;
+    __device__ __forceinline__ double operator()(float l) const
+    {
         if (!(l > -INFINITY)) return 0.0;
-        if (a.sigmoid) return 1.0 / (1.0 + exp(-static_cast<double>(l)));
-        return (l == m ? 1.0 : exp(static_cast<double>(l) - static_cast<double>(m))) / sum;
-    };
+        if (sigmoid) return 1.0 / (1.0 + exp(-static_cast<double>(l)));
+        return (l == m ? 1.0 : exp(static_cast<double>(l) - m)) / sum;
+    }
+};
+
+template <bool F32>
+__device__ __noinline__ Exact exact_scores(const SelectArgs& a, int64_t t, bool need_sum)
+{
+    const int lane = threadIdx.x & 31;
+    Exact x{a.sigmoid, 0.0, 1.0};
+    if (a.sigmoid) return x;
+    float m = -INFINITY;
+    for (int e = lane; e < a.E; e += 32) m = fmaxf(m, load_logit<F32>(a, t, e));
+    x.m = warp_max(m);
+    if (!need_sum) return x;
+    double sum = 0.0;
+    for (int e = lane; e < a.E; e += 32) sum += x(load_logit<F32>(a, t, e));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    x.sum = sum;
+    return x;
+}
+
+// The groups that stay (bit of a group's first lane), from FP64 values; the FP32 choice values are in
+// c_s. Only what lies within the error of a group's second largest can be one of its two largest.
+template <bool F32>
+__device__ __noinline__ unsigned exact_groups(const SelectArgs& a, int64_t t, const float* c_s, float v2, float margin)
+{
+    const Exact score = exact_scores<F32>(a, t, a.bias != nullptr);
+    const int lane = threadIdx.x & 31, size = a.E / a.n_group;
+    const int lg = 31 - __clz(32 / a.n_group), per = 1 << lg, g = lane >> lg, j = lane & (per - 1);
+    const bool real = g < a.n_group;
+    const float thr = v2 < INFINITY ? v2 - margin : v2;  // -inf where the group has one unmasked expert or none
+    uint64_t hits = 0;              // this lane's values: j, j + per, ... (at most 43 of them)
+    if (real)
+        for (int i = 0; (i << lg) + j < size; ++i) {
+            const float v = c_s[g * size + (i << lg) + j];
+            hits |= static_cast<uint64_t>(v >= thr && v > -INFINITY) << i;
+        }
+    double v1 = -INFINITY, w2 = -INFINITY;
+    while (__any_sync(kFull, hits != 0)) {
+        if (hits) {
+            const int e = g * size + ((__ffsll(static_cast<long long>(hits)) - 1) << lg) + j;
+            hits &= hits - 1;
+            const double v = score(load_logit<F32>(a, t, e)) + (a.bias ? static_cast<double>(a.bias[e]) : 0.0);
+            w2 = fmax(w2, fmin(v1, v));
+            v1 = fmax(v1, v);
+        }
+    }
+    for (int o = per >> 1; o > 0; o >>= 1) {
+        const double o1 = __shfl_xor_sync(kFull, v1, o), o2 = __shfl_xor_sync(kFull, w2, o);
+        w2 = fmax(fmin(v1, o1), fmax(w2, o2));
+        v1 = fmax(v1, o1);
+    }
+    const double gv = a.group_top2 && w2 > -INFINITY ? v1 + w2 : v1;
+    int rank = 0;
+    for (int o = 0; o < a.n_group; ++o) {
+        const double ov = __shfl_sync(kFull, gv, o << lg);
+        rank += ov > gv || (ov == gv && o < g);
+    }
+    return __ballot_sync(kFull, real && j == 0 && rank < a.topk_group);
+}
+
+// The first k + 1 of the C candidates in sel, ordered by FP64 values (c64: scratch for C of them).
+template <bool F32>
+__device__ __noinline__ void exact_ranking(const SelectArgs& a, int64_t t, const float2* cand, int C, double* c64, float2* sel)
+{
+    const Exact score = exact_scores<F32>(a, t, true);
+    const int lane = threadIdx.x & 31;
+    for (int q = lane; q < C; q += 32) {
+        const int e = __float_as_int(cand[q].y);
+        c64[q] = score(load_logit<F32>(a, t, e)) + static_cast<double>(a.bias[e]);
+    }
+    __syncwarp();
+    for (int q = lane; q < C; q += 32) {
+        const double me = c64[q];
+        const int id = __float_as_int(cand[q].y);
+        int r = 0;
+        for (int o = 0; o < C; ++o) r += ahead(c64[o], __float_as_int(cand[o].y), me, id);
+        if (r <= a.k) sel[r] = cand[q];
+    }
+    __syncwarp();
+}
+
+// One token by plain rounds of a warp arg-max over c[E] (lowest id first on equal values): rows that
+// the ranking below does not hold. V: double with a bias; float without, where c is the logit.
+template <bool F32, typename V>
+__device__ __noinline__ void whole_row(const SelectArgs& a, int64_t t, V* c)
+{
+    const int lane = threadIdx.x & 31;
+    const V ninf = -INFINITY, nan = NAN;
+    const Exact score = exact_scores<F32>(a, t, a.bias || !a.renormalize);
     for (int e = lane; e < a.E; e += 32) {
-        const float l = load_logit(a, t, e);
-        // without a bias the logits themselves give the order, also where two scores round to one number
-        const double v = a.bias ? score(l) + static_cast<double>(a.bias[e]) : static_cast<double>(l);
+        const float l = load_logit<F32>(a, t, e);
+        const V v = a.bias ? static_cast<V>(score(l) + static_cast<double>(a.bias[e])) : static_cast<V>(l);
         c[e] = l > -INFINITY && v > ninf ? v : ninf;
     }
     __syncwarp();
     if (a.n_group > 1) {
         const int size = a.E / a.n_group;
-        double v1 = ninf, v2 = ninf;
+        V v1 = ninf, v2 = ninf;
         if (lane < a.n_group)
             for (int i = 0; i < size; ++i) {
-                const double v = c[lane * size + i];
+                const V v = c[lane * size + i];
                 if (v > v1) {
                     v2 = v1;
                     v1 = v;
@@ -68,8 +192,8 @@ __global__ void __launch_bounds__(kWarps * 32) k_select_experts(const SelectArgs
             }
         double gv = v1;
         if (a.group_top2 && v1 > ninf) {
-            const double s1 = a.bias ? v1 : score(static_cast<float>(v1));
-            gv = v2 > ninf ? s1 + (a.bias ? v2 : score(static_cast<float>(v2))) : s1;
+            const double s1 = a.bias ? static_cast<double>(v1) : score(static_cast<float>(v1));
+            gv = v2 > ninf ? s1 + (a.bias ? static_cast<double>(v2) : score(static_cast<float>(v2))) : s1;
         }
         int rank = 0;
         for (int g = 0; g < a.n_group; ++g) {
@@ -82,39 +206,299 @@ __global__ void __launch_bounds__(kWarps * 32) k_select_experts(const SelectArgs
         __syncwarp();
     }
     int my_id = 0;
-    double my_s = 0.0, total = 0.0;
+    bool masked = true;
     for (int j = 0; j < a.k; ++j) {
-        double best = nan;
-        int at = kMaxE;
+        V best = nan;
+        int at = 1 << 30;
         for (int e = lane; e < a.E; e += 32)
-            if (c[e] == c[e] && (at == kMaxE || c[e] > best)) {
+            if (c[e] == c[e] && (at == 1 << 30 || c[e] > best)) {
                 best = c[e];
                 at = e;
             }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
-            const double ob = __shfl_xor_sync(kFull, best, o);
+            const V ob = __shfl_xor_sync(kFull, best, o);
             const int oa = __shfl_xor_sync(kFull, at, o);
-            if (oa < kMaxE && (at == kMaxE || ahead(ob, oa, best, at))) {
+            if (oa < 1 << 30 && (at == 1 << 30 || ob > best || (ob == best && oa < at))) {
                 best = ob;
                 at = oa;
             }
         }
-        const double s = best > ninf ? score(load_logit(a, t, at)) : 0.0;
-        total += s;
         if (lane == j) {
             my_id = at;
-            my_s = s;
+            masked = !(best > ninf);
         }
         __syncwarp();
         if (lane == (at & 31)) c[at] = nan;
         __syncwarp();
     }
-    if (lane < a.k) {
-        if (a.renormalize) my_s = total > 0.0 ? my_s / total : 0.0;
-        a.ids[t * a.k + lane] = my_id;
-        a.w[t * a.k + lane] = static_cast<float>(my_s * a.scale);
+    double s = lane < a.k && !masked ? score(load_logit<F32>(a, t, my_id)) : 0.0;
+    if (a.renormalize) {
+        double total = s;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kFull, total, o);
+        s = total > 0.0 ? s / total : 0.0;
     }
+    if (lane < a.k) {
+        a.ids[t * a.k + lane] = my_id;
+        a.w[t * a.k + lane] = static_cast<float>(s * a.scale);
+    }
+}
+
+template <bool F32>
+__device__ __forceinline__ void whole_row(const SelectArgs& a, int64_t t, double* scratch)
+{
+    if (a.bias) whole_row<F32, double>(a, t, scratch);
+    else whole_row<F32, float>(a, t, reinterpret_cast<float*>(scratch));
+}
+
+// Expert held in slot i of a lane: 4 neighbours a 16-byte (bf16: 8-byte) load, or one.
+template <bool VEC>
+__device__ __forceinline__ int expert_of(int i, int lane)
+{
+    return VEC ? ((i >> 2) * 32 + lane) * 4 + (i & 3) : i * 32 + lane;
+}
+
+template <int kNper, bool F32, bool VEC>
+__global__ void __launch_bounds__(kWarps * 32, kNper <= 16 ? 10 : 5) k_select_experts(const SelectArgs a)
+{
+    constexpr int kE = kNper * 32;
+    __shared__ double scratch_s[kWarps][kE < kMaxCand ? kMaxCand : kE];
+    __shared__ float2 cand_s[kWarps][kMaxCand];
+    __shared__ float2 sel_s[kWarps][33];
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    if (t >= a.T) return;
+    float* c_s = reinterpret_cast<float*>(scratch_s[warp]);
+    float2* cand = cand_s[warp];
+    float2* sel = sel_s[warp];
+    const int E = a.E, k = a.k;
+
+    // logits; what is masked (NaN included) or no expert is -inf
+    float c[kNper];
+    if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < kNper; i += 4) {
+            const int e = expert_of<true>(i, lane);
+            c[i] = c[i + 1] = c[i + 2] = c[i + 3] = -INFINITY;
+            if (e < E) {
+                if constexpr (F32) {
+                    const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + t * a.ld + e));
+                    c[i] = v.x, c[i + 1] = v.y, c[i + 2] = v.z, c[i + 3] = v.w;
+                } else {
+                    const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.logits) + t * a.ld + e));
+                    c[i] = bf16_to_f32(v.x & 0xFFFFu), c[i + 1] = bf16_to_f32(v.x >> 16);
+                    c[i + 2] = bf16_to_f32(v.y & 0xFFFFu), c[i + 3] = bf16_to_f32(v.y >> 16);
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kNper; ++i) {
+            const int e = expert_of<false>(i, lane);
+            c[i] = e < E ? load_logit<F32>(a, t, e) : -INFINITY;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kNper; ++i) c[i] = fmaxf(c[i], -INFINITY);
+
+    // the row's maximum and the softmax's sum, where anything needs them
+    const bool groups = a.n_group > 1 && a.topk_group < a.n_group;
+    const bool need_sum = !a.sigmoid && (a.bias || !a.renormalize);
+    float m = 0.0f, inv_sum = 1.0f, smax = 1.0f;
+    const bool have_m = !a.sigmoid && (need_sum || groups);
+    if (have_m) {
+        m = c[0];
+#pragma unroll
+        for (int i = 1; i < kNper; ++i) m = fmaxf(m, c[i]);
+        m = warp_max(m);
+        if (need_sum) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kNper; ++i) sum += fast_exp(c[i] - m);
+            inv_sum = 1.0f / warp_sum(sum);
+            smax = inv_sum;
+        }
+        if (!(fabsf(m) < INFINITY)) {  // nothing but masked experts, or logits of +inf
+            whole_row<F32>(a, t, scratch_s[warp]);
+            return;
+        }
+    }
+    auto score = [&](float l) { return a.sigmoid ? fast_rcp(1.0f + fast_exp(-l)) : fast_exp(l - m) * inv_sum; };
+    if (a.bias) {
+#pragma unroll
+        for (int i = 0; i < kNper; ++i) {
+            const int e = expert_of<VEC>(i, lane);
+            // a masked logit stays -inf; a NaN of the bias becomes -inf
+            const float b = e < E ? __ldg(a.bias + e) : -INFINITY;
+            c[i] = c[i] > -INFINITY ? fmaxf(score(c[i]) + b, -INFINITY) : -INFINITY;
+        }
+    }
+    const float eps_score = (a.sigmoid ? kEpsSigmoid : kEpsSoftmax) * smax;
+
+    if (groups) {
+#pragma unroll
+        for (int i = 0; i < kNper; ++i) {
+            const int e = expert_of<VEC>(i, lane);
+            if (!VEC && e < E) c_s[e] = c[i];
+            if (VEC && i % 4 == 0 && e < E)
+                *reinterpret_cast<float4*>(c_s + e) = make_float4(c[i], c[(i + 1) % kNper], c[(i + 2) % kNper], c[(i + 3) % kNper]);
+        }
+        __syncwarp();
+        const int size = E / a.n_group;
+        const int lg = 31 - __clz(32 / a.n_group), per = 1 << lg;  // lanes a group
+        const int g = lane >> lg, j = lane & (per - 1);
+        float v1 = -INFINITY, v2 = -INFINITY;
+        if (g < a.n_group) {
+            // the groups start at different places, so that their lanes read different banks
+            const int n = (size - j + per - 1) >> lg;  // this lane's values: j, j + per, ...
+            int i = n > 0 ? g % n : 0;
+            for (int q = 0; q < n; ++q) {
+                const float v = c_s[g * size + (i << lg) + j];
+                v2 = fmaxf(v2, fminf(v1, v));
+                v1 = fmaxf(v1, v);
+                if (++i == n) i = 0;
+            }
+        }
+        for (int o = per >> 1; o > 0; o >>= 1) {
+            const float o1 = __shfl_xor_sync(kFull, v1, o), o2 = __shfl_xor_sync(kFull, v2, o);
+            v2 = fmaxf(fminf(v1, o1), fmaxf(v2, o2));
+            v1 = fmaxf(v1, o1);
+        }
+        float gv = v1;
+        if (a.group_top2 && v1 > -INFINITY) {
+            const float s1 = a.bias ? v1 : score(v1);
+            gv = v2 > -INFINITY ? s1 + (a.bias ? v2 : score(v2)) : s1;
+        }
+        int rank = 0;
+        for (int o = 0; o < a.n_group; ++o) {
+            const float ov = __shfl_sync(kFull, gv, o << lg);
+            rank += ov > gv || (ov == gv && o < g);
+        }
+        const bool real = g < a.n_group, stays = real && rank < a.topk_group;
+        unsigned keep = __ballot_sync(kFull, stays && j == 0);
+        if (a.bias || a.group_top2) {
+            const float lo = -warp_max(stays ? -gv : -INFINITY), hi = warp_max(real && !stays ? gv : -INFINITY);
+            if (hi > -INFINITY && lo - hi <= 4.0f * eps_score + 2.0f * kEpsAdd * (fabsf(lo) + fabsf(hi)))
+                keep = exact_groups<F32>(a, t, c_s, a.group_top2 ? v2 : v1,
+                                         a.bias ? 2.0f * (eps_score + kEpsAdd * fabsf(v1)) : 0.0f);
+        }
+        // e / size for e < 1024: exact, since 1023 * size <= 2^20 < 2^21
+        const unsigned mul = ((1u << 21) + size - 1) / size;
+#pragma unroll
+        for (int i = 0; i < kNper; ++i) {
+            const unsigned ge = (static_cast<unsigned>(expert_of<VEC>(i, lane)) * mul) >> 21;
+            if (!((keep >> ((ge << lg) & 31u)) & 1u)) c[i] = -INFINITY;
+        }
+    }
+
+    // the (k + 1)-th largest lane maximum (k = 32: the smallest), by a bitonic sort across the lanes
+    float tau = c[0];
+#pragma unroll
+    for (int i = 1; i < kNper; ++i) tau = fmaxf(tau, c[i]);
+#pragma unroll
+    for (int s = 2; s <= 32; s <<= 1)
+#pragma unroll
+        for (int o = s >> 1; o > 0; o >>= 1) {
+            const float v = __shfl_xor_sync(kFull, tau, o);
+            const bool larger = ((lane & o) == 0) == ((lane & s) == 0);  // descending runs where bit s is clear
+            tau = larger ? fmaxf(tau, v) : fminf(tau, v);
+        }
+    tau = __shfl_sync(kFull, tau, k < 32 ? k : 31);
+    // what can be among the k largest in exact arithmetic has a value of at least tau less two errors
+    if (a.bias) tau -= 2.0f * (eps_score + kEpsAdd * fabsf(tau));
+
+    // the values that reach it
+    unsigned mine = 0;
+#pragma unroll
+    for (int i = 0; i < kNper; ++i) mine |= (c[i] >= tau && c[i] > -INFINITY ? 1u : 0u) << i;
+    const int cnt = __popc(mine);
+    int pos = cnt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(kFull, pos, o);
+        if (lane >= o) pos += v;
+    }
+    const int C = __shfl_sync(kFull, pos, 31);
+    pos -= cnt;
+    if (C < k || C > kMaxCand) {
+        __syncwarp();
+        whole_row<F32>(a, t, scratch_s[warp]);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < kNper; ++i)
+        if ((mine >> i) & 1u) cand[pos++] = make_float2(c[i], __int_as_float(expert_of<VEC>(i, lane)));
+    __syncwarp();
+    for (int q = lane; q < C; q += 32) {
+        const float2 me = cand[q];
+        const int id = __float_as_int(me.y);
+        int r = 0;
+        for (int o = 0; o < C; ++o) {
+            const float2 v = cand[o];
+            r += v.x > me.x || (v.x == me.x && __float_as_int(v.y) < id);
+        }
+        if (r <= k) sel[r] = me;
+    }
+    __syncwarp();
+    float2 me = sel[lane < k ? lane : 0];
+    if (a.bias) {
+        const float next = lane < k && lane + 1 < C ? sel[lane + 1].x : -INFINITY;
+        const bool near = next > -INFINITY && me.x - next <= 2.0f * eps_score + kEpsAdd * (fabsf(me.x) + fabsf(next));
+        if (__any_sync(kFull, near)) {
+            __syncwarp();
+            exact_ranking<F32>(a, t, cand, C, scratch_s[warp], sel);
+            me = sel[lane < k ? lane : 0];
+        }
+    }
+    const int id = __float_as_int(me.y);
+    const float l = a.bias ? load_logit<F32>(a, t, id) : me.x;
+    float s;
+    if (a.renormalize) {
+        // the scores divided by exp(largest chosen logit), or for sigmoid by no less than that: a factor
+        // that the sum divides out, so that small scores keep their ratios
+        const float top = warp_max(lane < k ? l : -INFINITY);
+        if ((a.sigmoid ? top : have_m ? top - m : 0.0f) < -80.0f) {  // scores that underflow here: in FP64
+            whole_row<F32>(a, t, scratch_s[warp]);
+            return;
+        }
+        const float f = a.sigmoid ? fminf(top, 0.0f) : top;
+        s = l == f ? 1.0f : expf(l - f);
+        if (a.sigmoid) s = l < 0.0f ? s / (1.0f + expf(l)) : 1.0f / (1.0f + expf(-l));  // f is 0 there
+        s /= warp_sum(lane < k ? s : 0.0f);
+    } else {
+        s = a.sigmoid ? 1.0f / (1.0f + expf(-l)) : expf(l - m) * inv_sum;
+    }
+    if (lane < k) {
+        a.ids[t * k + lane] = id;
+        a.w[t * k + lane] = s * a.scale;
+    }
+}
+
+template <int kNper, bool F32>
+cudaError_t launch(const SelectArgs& a, bool vec, cudaStream_t stream)
+{
+    const dim3 grid((a.T + kWarps - 1) / kWarps), block(kWarps * 32);
+    if constexpr (kNper >= 4) {
+        if (vec) return launch_pdl(k_select_experts<kNper, F32, true>, grid, block, 0, stream, a);
+    }
+    return launch_pdl(k_select_experts<kNper, F32, false>, grid, block, 0, stream, a);
+}
+
+template <bool F32>
+cudaError_t launch_type(const SelectArgs& a, cudaStream_t stream)
+{
+    // four experts a load where every row allows it and there are enough for all lanes
+    constexpr int bytes = F32 ? 4 : 2;
+    const bool vec = a.E % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % (4 * bytes) == 0 && (a.ld % 4 == 0 || a.T == 1);
+    if (a.E <= 32) return launch<1, F32>(a, vec, stream);
+    if (a.E <= 64) return launch<2, F32>(a, vec, stream);
+    if (a.E <= 128) return launch<4, F32>(a, vec && a.E > 64, stream);
+    if (a.E <= 256) return launch<8, F32>(a, vec, stream);
+    if (a.E <= 512) return launch<16, F32>(a, vec, stream);
+    return launch<32, F32>(a, vec, stream);
 }
 
 }  // namespace
@@ -122,7 +506,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_select_experts(const SelectArgs
 cudaError_t launch_select_experts(const SelectArgs& a, cudaStream_t stream)
 {
     if (a.T <= 0) return cudaSuccess;
-    return launch_pdl(k_select_experts, dim3((a.T + kWarps - 1) / kWarps), dim3(kWarps * 32), 0, stream, a);
+    return a.logits_f32 ? launch_type<true>(a, stream) : launch_type<false>(a, stream);
 }
 
 }  // namespace moe
