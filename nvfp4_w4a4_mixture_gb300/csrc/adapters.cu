@@ -13,6 +13,8 @@
 // lane quarter each), add y in the ring's buffer and store rows of 128 bytes.
 // Rows of a tile beyond its request's end hold whatever the buffers held; rows do not mix, and those
 // are not stored. The zero fill of TMA pads K, N and the rank.
+#include <cstdlib>
+
 #include "block.cuh"
 #include "ptx_cluster.cuh"
 
@@ -20,33 +22,46 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 192, kTileM = 128;
-constexpr int kXBytes = kTileM * 128;  // 128 rows x 64 bf16
-constexpr uint32_t kD2Col = 128;       // TMEM columns: h at 0..127, two phase-2 accumulators behind it
+constexpr int kTileM = 128;            // rows of an MMA
+constexpr int kGroups = 2;             // epilogue groups of four warps; they take phase 2's slices in turn
+constexpr int kEpiWarps = 4 * kGroups, kThreads = 64 + 32 * kEpiWarps;
+constexpr int kBufs = 2 * kGroups;     // phase-2 accumulators
+constexpr uint32_t kD2Col = 128;       // TMEM columns: h at 0..127, the phase-2 accumulators behind it
+constexpr uint32_t kTmemCols = 512;
+constexpr int kSmemMax = 227 * 1024;
 
-// kR: the rank, padded (16, 32, 64 or 128)
-template <int kR>
+// kR: the rank, padded (16, 32, 64 or 128); kRows: rows that a tile's buffers hold (32 or 128). With 32
+// the MMAs read 96 rows more: what lies behind the buffers, inside this CTA's shared memory.
+template <int kR, int kRows>
 struct Shape {
     static constexpr int kBlocks = (kR + 63) / 64;        // 64-column blocks of the rank
+    static constexpr int kX = kRows * 128;                // x or y slice: 64 bf16 a row
     static constexpr int kW = kBlocks * 64 * 128;         // bytes of a B slice (64 rows), >= the A slice (kR rows of 128)
     static_assert(kW >= kR * 128, "an A slice fits");
-    static constexpr int kStage = kXBytes + kW;
-    static constexpr int kH = kBlocks * kXBytes;          // hi (or lo)
-    static constexpr int kStages = kR > 64 ? 4 : 7;
+    static constexpr int kStage = kX + kW;
+    static constexpr int kH = kBlocks * kX;               // hi (or lo)
+    static constexpr int kOutStage = kEpiWarps * 4096;    // 32 rows x 128 bytes a warp
+    static constexpr int kPart = kRows * kR * 4;          // a cluster's partial h, before the stores need their buffers
+    static constexpr int kOut = kPart > kOutStage ? kPart : kOutStage;
+    static constexpr int kStages = (kSmemMax - 2048 - 2 * kH - kOut) / kStage;
+    static_assert(kStages >= 3 && 2 * kH + kOut >= (kBlocks + 1) * kX * 1 + kTileM * 128, "buffers");
 };
 
 template <int kStages>
 struct Tail {
     uint64_t full[kStages], empty[kStages];
-    uint64_t d1_full, h_ready, d2_full[2], d2_empty[2], p_ready, p_done, drain;
+    uint64_t d1_full, h_ready, d2_full[kBufs], d2_empty[kBufs], p_ready, p_done, idle, drain;
     uint32_t tmem;
     int abort;
 };
 
-template <int kR>
+template <int kR, int kRows>
 constexpr size_t smem_bytes()
 {
-    return 1024 + static_cast<size_t>(Shape<kR>::kStages) * Shape<kR>::kStage + 2 * Shape<kR>::kH + sizeof(Tail<Shape<kR>::kStages>);
+    using S = Shape<kR, kRows>;
+    constexpr size_t n = 1024 + static_cast<size_t>(S::kStages) * S::kStage + 2 * S::kH + S::kOut + sizeof(Tail<S::kStages>);
+    static_assert(n <= kSmemMax, "shared memory");
+    return n;
 }
 
 struct Tile {
@@ -108,19 +123,31 @@ __device__ __forceinline__ void load_rows(uint8_t* dst, const CUtensorMap* m8, c
 // 16-byte piece j of row r in the 128-byte-swizzled layout
 __device__ __forceinline__ uint32_t piece(int r, int j) { return r * 128 + ((j ^ (r & 7)) << 4); }
 
-template <int kR>
+// Two FP32 values (or zeros) as hi + lo, each two bf16: hi the nearest, lo the nearest to what is left.
+__device__ __forceinline__ void split(bool in, float u, float v, uint32_t& hi, uint32_t& lo)
+{
+    if (!in) u = v = 0.0f;  // a padded column stays zero where x is not finite, too
+    hi = pack_bf16x2(u, v);
+    const float uh = bf16_to_f32(hi & 0xFFFFu), vh = bf16_to_f32(hi >> 16);
+    // an infinity has no remainder
+    lo = pack_bf16x2(fabsf(uh) < INFINITY ? u - uh : 0.0f, fabsf(vh) < INFINITY ? v - vh : 0.0f);
+}
+
+template <int kR, int kRows>
 __global__ void __launch_bounds__(kThreads, 1)
     k_adapter_add(const __grid_constant__ AdapterArgs p, int tile_rows, const __grid_constant__ CUtensorMap map_x8,
                   const __grid_constant__ CUtensorMap map_x32, const __grid_constant__ CUtensorMap map_y8,
                   const __grid_constant__ CUtensorMap map_y32, const __grid_constant__ CUtensorMap map_a,
                   const __grid_constant__ CUtensorMap map_b)
 {
-    using S = Shape<kR>;
+    using S = Shape<kR, kRows>;
+    constexpr int kXBytes = S::kX;
     constexpr int kStages = S::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* hbuf = smem + kStages * S::kStage;  // hi, lo; before them the partial sums [kR][128] of a cluster
-    Tail<kStages>& st = *reinterpret_cast<Tail<kStages>*>(hbuf + 2 * S::kH);
+    uint8_t* hbuf = smem + kStages * S::kStage;  // hi, lo
+    uint8_t* obuf = hbuf + 2 * S::kH;            // rows to store, 4 KB a warp; before that a cluster's partial h
+    Tail<kStages>& st = *reinterpret_cast<Tail<kStages>*>(obuf + S::kOut);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int cs = static_cast<int>(ptx::cluster_size()), rank = static_cast<int>(ptx::cluster_rank());
     const int cluster = blockIdx.x / cs, n_clusters = gridDim.x / cs;
@@ -130,24 +157,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
             ptx::mbar_init(&st.full[s], 1);
-            ptx::mbar_init(&st.empty[s], 5);  // the MMA thread and four epilogue warps
+            ptx::mbar_init(&st.empty[s], 5);  // the MMA thread and the four warps of an epilogue group
         }
         ptx::mbar_init(&st.d1_full, 1);
         ptx::mbar_init(&st.drain, 1);
-        ptx::mbar_init(&st.h_ready, 4);
-        for (int b = 0; b < 2; ++b) {
+        ptx::mbar_init(&st.h_ready, kEpiWarps);
+        ptx::mbar_init(&st.idle, kEpiWarps);
+        for (int b = 0; b < kBufs; ++b) {
             ptx::mbar_init(&st.d2_full[b], 1);
             ptx::mbar_init(&st.d2_empty[b], 4);
         }
-        ptx::mbar_init(&st.p_ready, 4 * cs);
-        ptx::mbar_init(&st.p_done, 4 * cs);
+        ptx::mbar_init(&st.p_ready, kEpiWarps * cs);
+        ptx::mbar_init(&st.p_done, kEpiWarps * cs);
         st.abort = 0;
         ptx::fence_mbar_init();
         ptx::prefetch_tmap(&map_a);
         ptx::prefetch_tmap(&map_b);
     }
     if (warp == 1) {
-        ptx::tmem_alloc(&st.tmem, 256);
+        ptx::tmem_alloc(&st.tmem, kTmemCols);
         ptx::tmem_relinquish();
     }
     ptx::griddep_wait();
@@ -226,14 +254,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++it;
                     ptx::tc_fence_after();
                 }
-                for (int nc = n0; ok && nc < n1; ++nc) {
-                    ok = ptx::mbar_wait(&st.full[s], ph);
+                for (int nc = n0; ok && nc < n1; ++nc, ++cc) {
+                    const uint32_t buf = cc % kBufs;
+                    ok = ptx::mbar_wait(&st.full[s], ph) && ptx::mbar_wait(&st.d2_empty[buf], ((cc / kBufs) & 1) ^ 1);
                     if (!ok) break;
                     if (t.adapter >= 0) {
-                        const uint32_t buf = cc & 1;
-                        ok = ptx::mbar_wait(&st.d2_empty[buf], ((cc >> 1) & 1) ^ 1);
-                        if (!ok) break;
-                        ++cc;
                         ptx::tc_fence_after();
                         const uint64_t so = static_cast<uint64_t>(s) * (S::kStage >> 4);
                         const uint32_t d = tmem + kD2Col + buf * 64;
@@ -244,8 +269,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         ptx::tc_commit(&st.empty[s]);
                         ptx::tc_commit(&st.d2_full[buf]);
-                    } else {
+                    } else {  // a tile to copy takes the same turns, without a product
                         ptx::mbar_arrive(&st.empty[s]);
+                        ptx::mbar_arrive(&st.d2_full[buf]);
                     }
                     if (++s == kStages) { s = 0; ph ^= 1; }
                 }
@@ -258,14 +284,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
         }
     } else {
-        const int q = warp & 3, row = q * 32 + lane;  // TMEM lane quarter, row of the tile
+        // group g: half of h's columns, every kGroups-th slice of phase 2; q: TMEM lane quarter
+        const int ew = warp - 2, g = ew / 4, q = warp & 3, row = q * 32 + lane;
         const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16);
+        uint8_t* ob = obuf + ew * 4096;
         int s = 0;
-        uint32_t ph = 0, it = 0, cc = 0;
+        uint32_t ph = 0, it = 0, cc = 0, tiles = 0;
         bool ok = true;
         // one lane's wait result may differ from another's only in time: the warp agrees on it
         auto all = [&](bool got) { return __all_sync(0xFFFFFFFFu, got) != 0; };
-        if (cluster == 0 && rank == 0 && warp == 2) {
+        if (cluster == 0 && rank == 0 && ew == 0) {
             bool bad = __ldg(p.seg_offsets) != 0 || __ldg(p.seg_offsets + p.S) != p.T;
             for (int i = lane; i < p.S; i += 32) {
                 const int beg = __ldg(p.seg_offsets + i), end = __ldg(p.seg_offsets + i + 1), ad = __ldg(p.seg_adapter + i);
@@ -273,69 +301,85 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (bad) record_status(p.status, kDevBadSegment);
         }
-        for (int number = cluster; ok && walk.find(p, tile_rows, number, t); number += n_clusters) {
+        for (int number = cluster; ok && walk.find(p, tile_rows, number, t); number += n_clusters, ++tiles) {
             const bool live = q * 32 < t.rows;  // this warp has rows of the tile
+            // a cluster: no warp is a tile ahead of another (their buffers are about to hold partial sums)
+            if (cs > 1 && tiles > 0) ok = all(ptx::mbar_wait(&st.idle, (tiles - 1) & 1));
+            if (!ok) break;
             if (t.adapter >= 0) {
                 for (s += k1 - k0; s >= kStages; s -= kStages) ph ^= 1;  // phase 1's stages are not its own
-                float h[kR];
+                constexpr int kHalf = kR / kGroups;
+                const int c0 = g * kHalf;
+                const float f = __ldg(p.scale + t.adapter);
                 ok = all(ptx::mbar_wait(&st.d1_full, it & 1));
                 if (!ok) break;
                 ptx::tc_fence_after();
-                if (live && k0 < k1) {
+                if (cs == 1) {
+                    if (live) {
+                        uint32_t v[kHalf];
 #pragma unroll
-                    for (int c = 0; c < kR; c += 16) {
-                        uint32_t v[16];
-                        ptx::tmem_ld16(tq + c, v);
+                        for (int c = 0; c < kHalf; c += 8) ptx::tmem_ld8(tq + c0 + c, v + c);
                         ptx::tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) h[c + i] = __uint_as_float(v[i]);
+                        for (int c = 0; c < kHalf; c += 8) {
+                            uint32_t hi[4], lo[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                split(c0 + c + 2 * i < p.r, __uint_as_float(v[c + 2 * i]) * f, __uint_as_float(v[c + 2 * i + 1]) * f,
+                                      hi[i], lo[i]);
+                            uint8_t* d = hbuf + ((c0 + c) / 64) * kXBytes + piece(row, ((c0 + c) % 64) / 8);
+                            *reinterpret_cast<uint4*>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                            *reinterpret_cast<uint4*>(d + S::kH) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        }
                     }
+                    ptx::tc_fence_before();
                 } else {
+                    // each CTA's partial h, pieces of four columns; then CTA `rank` adds every cs-th row and
+                    // writes it to all of the cluster
+                    constexpr int kQuads = kR / 4, kMask = kQuads < 8 ? kQuads - 1 : 7;
+                    if (live) {
+                        uint32_t v[kHalf];
+                        if (k0 < k1) {
 #pragma unroll
-                    for (int c = 0; c < kR; ++c) h[c] = 0.0f;
-                }
-                ptx::tc_fence_before();
-                if (cs > 1) {
-                    float* part = reinterpret_cast<float*>(hbuf);  // [kR][128]
-                    if (live)
+                            for (int c = 0; c < kHalf; c += 8) ptx::tmem_ld8(tq + c0 + c, v + c);
+                            ptx::tmem_ld_wait();
+                        } else {
 #pragma unroll
-                        for (int c = 0; c < kR; ++c) part[c * kTileM + row] = h[c];
+                            for (int c = 0; c < kHalf; ++c) v[c] = 0u;
+                        }
+#pragma unroll
+                        for (int c = 0; c < kHalf; c += 4)
+                            *reinterpret_cast<uint4*>(obuf + (row * kQuads + (((c0 + c) / 4) ^ (row & kMask))) * 16) =
+                                make_uint4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+                    }
+                    ptx::tc_fence_before();
                     __syncwarp();
                     if (lane < cs) ptx::cluster_arrive(ptx::cluster_addr(&st.p_ready, lane));
                     ok = all(ptx::mbar_wait_cluster(&st.p_ready, it & 1));
                     if (!ok) break;
-                    if (live) {
-#pragma unroll
-                        for (int c = 0; c < kR; ++c) h[c] = 0.0f;
+                    const int n = t.rows > rank ? (t.rows - rank + cs - 1) / cs * kQuads : 0;
+                    for (int u = ew * 32 + lane; u < n; u += kEpiWarps * 32) {
+                        const int r = rank + u / kQuads * cs, c = u % kQuads * 4;
+                        const uint8_t* at = obuf + (r * kQuads + ((c / 4) ^ (r & kMask))) * 16;
+                        float4 h = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                         for (int o = 0; o < cs; ++o) {
-                            const uint32_t at = ptx::cluster_addr(part + row, o);
-#pragma unroll
-                            for (int c = 0; c < kR; ++c) h[c] += ptx::cluster_load(at + c * kTileM * 4);
+                            const float4 v = ptx::cluster_load4(ptx::cluster_addr(at, o));
+                            h.x += v.x, h.y += v.y, h.z += v.z, h.w += v.w;
+                        }
+                        uint32_t hi[2], lo[2];
+                        split(c < p.r, h.x * f, h.y * f, hi[0], lo[0]);
+                        split(c < p.r, h.z * f, h.w * f, hi[1], lo[1]);
+                        const uint8_t* d = hbuf + (c / 64) * kXBytes + piece(r, (c % 64) / 8) + (c % 8) * 2;
+                        for (int o = 0; o < cs; ++o) {
+                            ptx::cluster_store2(ptx::cluster_addr(d, o), hi[0], hi[1]);
+                            ptx::cluster_store2(ptx::cluster_addr(d + S::kH, o), lo[0], lo[1]);
                         }
                     }
+                    ptx::fence_proxy_async();
                     __syncwarp();
                     if (lane < cs) ptx::cluster_arrive(ptx::cluster_addr(&st.p_done, lane));
                     ok = all(ptx::mbar_wait_cluster(&st.p_done, it & 1));
                     if (!ok) break;
-                }
-                if (live) {
-                    const float f = __ldg(p.scale + t.adapter);
-#pragma unroll
-                    for (int c = 0; c < kR; c += 8) {
-                        uint32_t hi[4], lo[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            // r is even; the padded columns stay zero even where x is not finite
-                            const float u = c + 2 * i < p.r ? h[c + 2 * i] * f : 0.0f, v = c + 2 * i < p.r ? h[c + 2 * i + 1] * f : 0.0f;
-                            hi[i] = pack_bf16x2(u, v);
-                            const float uh = bf16_to_f32(hi[i] & 0xFFFFu), vh = bf16_to_f32(hi[i] >> 16);
-                            // an infinity has no remainder
-                            lo[i] = pack_bf16x2(fabsf(uh) < INFINITY ? u - uh : 0.0f, fabsf(vh) < INFINITY ? v - vh : 0.0f);
-                        }
-                        uint8_t* d = hbuf + (c / 64) * kXBytes + piece(row, (c % 64) / 8);
-                        *reinterpret_cast<uint4*>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4*>(d + S::kH) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                    }
                 }
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
@@ -344,57 +388,67 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             for (int nc = n0; nc < n1; ++nc) {
                 uint8_t* yb = smem + s * S::kStage;
-                if (t.adapter >= 0) {
-                    const uint32_t buf = cc & 1;
-                    ok = all(ptx::mbar_wait(&st.d2_full[buf], (cc >> 1) & 1)) && all(ptx::mbar_wait(&st.full[s], ph));
+                const bool mine = cc % kGroups == static_cast<uint32_t>(g);
+                const uint32_t buf = cc % kBufs, par = (cc / kBufs) & 1;
+                ++cc;
+                if (mine) {
+                    // a stage or accumulator of another group may be a phase ahead: only its own are waited for
+                    ok = all(ptx::mbar_wait(&st.d2_full[buf], par)) && all(ptx::mbar_wait(&st.full[s], ph));
                     if (!ok) break;
-                    ++cc;
-                    ptx::tc_fence_after();
+                    uint32_t o[8][4];
                     if (live) {
-                        uint32_t v[4][16];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) ptx::tmem_ld16(tq + kD2Col + buf * 64 + i * 16, v[i]);
-                        ptx::tmem_ld_wait();
-                        ptx::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(&st.d2_empty[buf]);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
-                            uint4* at = reinterpret_cast<uint4*>(yb + piece(row, j));
-                            const uint4 y = *at;
-                            const uint32_t yy[4] = {y.x, y.y, y.z, y.w};
-                            uint32_t o[4];
+                            const uint4 y = *reinterpret_cast<const uint4*>(yb + piece(row, j));
+                            o[j][0] = y.x, o[j][1] = y.y, o[j][2] = y.z, o[j][3] = y.w;
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&st.empty[s]);
+                    if (t.adapter >= 0) {
+                        ptx::tc_fence_after();
+                        if (live) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int c = j * 8 + 2 * i;
-                                o[i] = pack_bf16x2(bf16_to_f32(yy[i] & 0xFFFFu) + __uint_as_float(v[c / 16][c % 16]),
-                                                   bf16_to_f32(yy[i] >> 16) + __uint_as_float(v[(c + 1) / 16][(c + 1) % 16]));
+                            for (int j0 = 0; j0 < 8; j0 += 4) {
+                                uint32_t v[2][16];
+                                ptx::tmem_ld16(tq + kD2Col + buf * 64 + j0 * 8, v[0]);
+                                ptx::tmem_ld16(tq + kD2Col + buf * 64 + j0 * 8 + 16, v[1]);
+                                ptx::tmem_ld_wait();
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        const int c = j * 8 + 2 * i;
+                                        uint32_t& w = o[j0 + j][i];
+                                        w = pack_bf16x2(bf16_to_f32(w & 0xFFFFu) + __uint_as_float(v[c / 16][c % 16]),
+                                                        bf16_to_f32(w >> 16) + __uint_as_float(v[c / 16][c % 16 + 1]));
+                                    }
                             }
-                            *at = make_uint4(o[0], o[1], o[2], o[3]);
+                        }
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                    }
+                    if (lane == 0) ptx::mbar_arrive(&st.d2_empty[buf]);
+                    if (live) {
+                        // each lane holds a row of 128 bytes: through this warp's buffer, four rows a store instruction
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<uint4*>(ob + piece(lane, j)) = make_uint4(o[j][0], o[j][1], o[j][2], o[j][3]);
+                        __syncwarp();
+                        const int col = nc * 64 + (lane & 7) * 8;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int r = i * 4 + (lane >> 3);
+                            if (q * 32 + r < t.rows && col < p.N)
+                                *reinterpret_cast<uint4*>(p.out + (t.row + q * 32 + r) * p.ld_out + col) =
+                                    *reinterpret_cast<const uint4*>(ob + piece(r, lane & 7));
                         }
                         __syncwarp();
-                    } else if (lane == 0) {
-                        ptx::mbar_arrive(&st.d2_empty[buf]);
                     }
-                } else {
-                    ok = all(ptx::mbar_wait(&st.full[s], ph));
-                    if (!ok) break;
                 }
-                if (live) {
-                    const int col = nc * 64 + (lane & 7) * 8;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int r = q * 32 + i * 4 + (lane >> 3);
-                        if (r < t.rows && col < p.N)
-                            *reinterpret_cast<uint4*>(p.out + (t.row + r) * p.ld_out + col) =
-                                *reinterpret_cast<const uint4*>(yb + piece(r, lane & 7));
-                    }
-                    ptx::fence_proxy_async_smem();  // the next fill of this buffer comes through the async proxy
-                    __syncwarp();
-                }
-                if (lane == 0) ptx::mbar_arrive(&st.empty[s]);
                 if (++s == kStages) { s = 0; ph ^= 1; }
             }
+            if (lane == 0) ptx::mbar_arrive(&st.idle);
         }
         if (!ok) fail();
     }
@@ -404,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tc_fence_after();
     if (warp == 1) {
         __syncwarp();
-        ptx::tmem_dealloc(tmem, 256);
+        ptx::tmem_dealloc(tmem, kTmemCols);
     }
     if (cs > 1) ptx::cluster_sync();  // no CTA leaves while another reads its shared memory
 }
@@ -424,13 +478,13 @@ CUresult map_bank(CUtensorMap* m, const uint16_t* base, int64_t cols, int64_t ro
     return encode_tmap_bf16(m, base, 3, dims, strides, box, 128);
 }
 
-template <int kR>
-cudaError_t launch(const AdapterArgs& a, int sms, cudaStream_t stream)
+template <int kR, int kRows>
+cudaError_t launch(const AdapterArgs& a, int cs, int64_t tiles, int sms, cudaStream_t stream)
 {
     static bool attr_set = false;
     if (!attr_set) {
-        cudaError_t e = cudaFuncSetAttribute(k_adapter_add<kR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem_bytes<kR>()));
+        cudaError_t e = cudaFuncSetAttribute(k_adapter_add<kR, kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(smem_bytes<kR, kRows>()));
         if (e != cudaSuccess) return e;
         attr_set = true;
     }
@@ -439,17 +493,12 @@ cudaError_t launch(const AdapterArgs& a, int sms, cudaStream_t stream)
         map_rows(&y8, a.y, a.N, a.T, a.ld_y, 8) != CUDA_SUCCESS || map_rows(&y32, a.y, a.N, a.T, a.ld_y, 32) != CUDA_SUCCESS ||
         map_bank(&ma, a.a, a.K, a.r, a.n, kR) != CUDA_SUCCESS || map_bank(&mb, a.b, a.r, a.N, a.n, 64) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
-    const int tile_rows = kTileM;
-    // a request of L rows has ceil(L / tile_rows) tiles: at most this many in all
-    const int64_t tiles = a.T / tile_rows + (a.S < a.T ? a.S : a.T);
-    int cs = 8;
-    while (cs > 1 && tiles * cs > sms) cs /= 2;
     const int clusters = static_cast<int>(tiles * cs <= sms ? tiles : sms / cs);
 
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(clusters * cs);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem_bytes<kR>();
+    cfg.dynamicSmemBytes = smem_bytes<kR, kRows>();
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -459,7 +508,7 @@ cudaError_t launch(const AdapterArgs& a, int sms, cudaStream_t stream)
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, k_adapter_add<kR>, a, tile_rows, x8, x32, y8, y32, ma, mb);
+    return cudaLaunchKernelEx(&cfg, k_adapter_add<kR, kRows>, a, kRows, x8, x32, y8, y32, ma, mb);
 }
 
 }  // namespace
@@ -467,10 +516,26 @@ cudaError_t launch(const AdapterArgs& a, int sms, cudaStream_t stream)
 cudaError_t launch_adapter_add(const AdapterArgs& a, int sms, cudaStream_t stream)
 {
     if (a.T <= 0) return cudaSuccess;
-    if (a.r <= 16) return launch<16>(a, sms, stream);
-    if (a.r <= 32) return launch<32>(a, sms, stream);
-    if (a.r <= 64) return launch<64>(a, sms, stream);
-    return launch<128>(a, sms, stream);
+    const int rows_force = std::getenv("AD_ROWS") ? atoi(std::getenv("AD_ROWS")) : 0;
+    const int cs_force = std::getenv("AD_CS") ? atoi(std::getenv("AD_CS")) : 0;
+    // a request of L rows has ceil(L / rows) tiles: at most this many in all
+    auto tiles_of = [&](int rows) { return static_cast<int64_t>(a.T / rows) + (a.S < a.T ? a.S : a.T); };
+    int rows = tiles_of(32) <= 2 * sms ? 32 : 128;
+    if (rows_force) rows = rows_force;
+    const int64_t tiles = tiles_of(rows);
+    int cs = 8;
+    while (cs > 1 && tiles * cs > sms) cs /= 2;
+    if (cs_force) cs = cs_force;
+    if (rows == 32) {
+        if (a.r <= 16) return launch<16, 32>(a, cs, tiles, sms, stream);
+        if (a.r <= 32) return launch<32, 32>(a, cs, tiles, sms, stream);
+        if (a.r <= 64) return launch<64, 32>(a, cs, tiles, sms, stream);
+        return launch<128, 32>(a, cs, tiles, sms, stream);
+    }
+    if (a.r <= 16) return launch<16, 128>(a, cs, tiles, sms, stream);
+    if (a.r <= 32) return launch<32, 128>(a, cs, tiles, sms, stream);
+    if (a.r <= 64) return launch<64, 128>(a, cs, tiles, sms, stream);
+    return launch<128, 128>(a, cs, tiles, sms, stream);
 }
 
 }  // namespace moe

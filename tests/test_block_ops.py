@@ -364,6 +364,12 @@ def test_adapter_many_requests(moe):
     check_adapter(moe, adapter_case([5000], [1], 2, 32, 2048, 2048))
 
 
+@pytest.mark.parametrize("lens", [[1] * 400, [40, 1, 33] * 60, [130, 2] * 150])
+def test_adapter_tiles_with_and_without_adapter_in_turn(moe, lens):
+    # several tiles a multiprocessor, many slices each, copied tiles between the others
+    check_adapter(moe, adapter_case(lens, [(i % 5) - 1 if i % 3 else -1 for i in range(len(lens))], 4, 24, 1032, 2048))
+
+
 def test_adapter_strides_and_in_place(moe):
     for lens in ([5, 1], [300, 70]):
         c = adapter_case(lens, [1, 0], 2, 16, 264, 136, pad=24)
