@@ -95,12 +95,13 @@ struct Walk {
             const unsigned hit = __ballot_sync(0xFFFFFFFFu, before + sum > number);
             if (hit) {
                 const int at = __ffs(hit) - 1;
-                const int first = __shfl_sync(0xFFFFFFFFu, before + sum - n, at);
-                beg = __shfl_sync(0xFFFFFFFFu, beg, at);
-                end = __shfl_sync(0xFFFFFFFFu, end, at);
-                t.adapter = __shfl_sync(0xFFFFFFFFu, ad, at);
-                t.row = beg + (number - first) * tile_rows;
-                t.rows = min(tile_rows, end - t.row);
+                // through warp reductions, whose results are uniform to the compiler: the addresses and loop
+                // bounds that the issuing warps make of them then need no moves to uniform registers
+                const bool me = lane == at;
+                const int row = beg + (number - (before + sum - n)) * tile_rows;
+                t.adapter = __reduce_max_sync(0xFFFFFFFFu, me ? ad : -1);
+                t.row = __reduce_max_sync(0xFFFFFFFFu, me ? row : 0);
+                t.rows = __reduce_max_sync(0xFFFFFFFFu, me ? min(tile_rows, end - row) : 0);
                 return true;
             }
             before += __shfl_sync(0xFFFFFFFFu, sum, 31);
@@ -109,16 +110,19 @@ struct Walk {
     }
 };
 
-// Rows [row, row + rows) x 64 columns at column c into dst: boxes of 8 rows up to 32 rows, else of 32.
-__device__ __forceinline__ uint32_t rows_bytes(int rows) { return rows <= 32 ? (rows + 7) / 8 * 1024u : (rows + 31) / 32 * 4096u; }
-__device__ __forceinline__ void load_rows(uint8_t* dst, const CUtensorMap* m8, const CUtensorMap* m32, uint64_t* bar, int c, int row,
-                                          int rows)
-{
-    if (rows <= 32)
-        for (int i = 0; i < rows; i += 8) ptx::tma_load_2d(dst + i * 128, m8, bar, c, row + i);
-    else
-        for (int i = 0; i < rows; i += 32) ptx::tma_load_2d(dst + i * 128, m32, bar, c, row + i);
-}
+// Rows [row, row + rows) x 64 columns at column c into dst, by one thread: boxes of 8 rows up to 24
+// rows, of 32 up to 96, else one of 128. box: the rows of a box, n: their number.
+struct Boxes {
+    int box, n;
+    __device__ explicit Boxes(int rows) : box(rows <= 24 ? 8 : rows <= 96 ? 32 : 128), n((rows + box - 1) / box) {}
+    __device__ uint32_t bytes() const { return static_cast<uint32_t>(box * n) * 128u; }
+    __device__ void load(uint8_t* dst, const CUtensorMap* m8, const CUtensorMap* m32, const CUtensorMap* m128, uint64_t* bar, int c,
+                         int row) const
+    {
+        const CUtensorMap* m = box == 8 ? m8 : box == 32 ? m32 : m128;
+        for (int i = 0; i < n; ++i) ptx::tma_load_2d(dst + i * box * 128, m, bar, c, row + i * box);
+    }
+};
 
 // 16-byte piece j of row r in the 128-byte-swizzled layout
 __device__ __forceinline__ uint32_t piece(int r, int j) { return r * 128 + ((j ^ (r & 7)) << 4); }
@@ -136,8 +140,9 @@ __device__ __forceinline__ void split(bool in, float u, float v, uint32_t& hi, u
 template <int kR, int kRows>
 __global__ void __launch_bounds__(kThreads, 1)
     k_adapter_add(const __grid_constant__ AdapterArgs p, int tile_rows, const __grid_constant__ CUtensorMap map_x8,
-                  const __grid_constant__ CUtensorMap map_x32, const __grid_constant__ CUtensorMap map_y8,
-                  const __grid_constant__ CUtensorMap map_y32, const __grid_constant__ CUtensorMap map_a,
+                  const __grid_constant__ CUtensorMap map_x32, const __grid_constant__ CUtensorMap map_x128,
+                  const __grid_constant__ CUtensorMap map_y8, const __grid_constant__ CUtensorMap map_y32,
+                  const __grid_constant__ CUtensorMap map_y128, const __grid_constant__ CUtensorMap map_a,
                   const __grid_constant__ CUtensorMap map_b)
 {
     using S = Shape<kR, kRows>;
@@ -148,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* hbuf = smem + kStages * S::kStage;  // hi, lo
     uint8_t* obuf = hbuf + 2 * S::kH;            // rows to store, 4 KB a warp; before that a cluster's partial h
     Tail<kStages>& st = *reinterpret_cast<Tail<kStages>*>(obuf + S::kOut);
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int tid = threadIdx.x, warp = __reduce_max_sync(0xFFFFFFFFu, tid / 32), lane = tid % 32;
     const int cs = static_cast<int>(ptx::cluster_size()), rank = static_cast<int>(ptx::cluster_rank());
     const int cluster = blockIdx.x / cs, n_clusters = gridDim.x / cs;
     const int nk = (p.K + 63) / 64, nn = (p.N + 63) / 64;
@@ -191,97 +196,108 @@ __global__ void __launch_bounds__(kThreads, 1)
     Walk walk;
     Tile t;
 
+    // The issuing warps run their loops whole and one lane issues: loop counters, addresses and
+    // descriptors stay uniform (a loop inside `if (lane == 0)` took 460 cycles a slice of two TMA
+    // copies and 120 an MMA, for moving its operands to uniform registers).
     if (warp == 0) {
+        const bool leader = ptx::elect_one();
         int s = 0;
         uint32_t ph = 0, fills = 0;
         bool ok = true;
         for (int number = cluster; ok && walk.find(p, tile_rows, number, t); number += n_clusters) {
-            if (lane == 0) {
-                const uint32_t xb = rows_bytes(t.rows);
-                for (int kc = k0; ok && t.adapter >= 0 && kc < k1; ++kc) {
-                    ok = ptx::mbar_wait(&st.empty[s], ph ^ 1);
+            const Boxes boxes(t.rows);
+            if (t.adapter >= 0)
+                for (int kc = k0; kc < k1; ++kc) {
+                    ok = __all_sync(0xFFFFFFFFu, ptx::mbar_wait(&st.empty[s], ph ^ 1));
                     if (!ok) break;
                     uint8_t* b = smem + s * S::kStage;
-                    ptx::mbar_arrive_expect_tx(&st.full[s], xb + kR * 128);
-                    load_rows(b, &map_x8, &map_x32, &st.full[s], kc * 64, t.row, t.rows);
-                    ptx::tma_load_3d(b + kXBytes, &map_a, &st.full[s], kc * 64, 0, t.adapter);
+                    if (leader) {
+                        ptx::mbar_arrive_expect_tx(&st.full[s], boxes.bytes() + kR * 128);
+                        ptx::tma_load_3d(b + kXBytes, &map_a, &st.full[s], kc * 64, 0, t.adapter);
+                        boxes.load(b, &map_x8, &map_x32, &map_x128, &st.full[s], kc * 64, t.row);
+                    }
                     ++fills;
                     if (++s == kStages) { s = 0; ph ^= 1; }
                 }
-                for (int nc = n0; ok && nc < n1; ++nc) {
-                    ok = ptx::mbar_wait(&st.empty[s], ph ^ 1);
-                    if (!ok) break;
-                    uint8_t* b = smem + s * S::kStage;
-                    ptx::mbar_arrive_expect_tx(&st.full[s], xb + (t.adapter >= 0 ? S::kW : 0));
-                    load_rows(b, &map_y8, &map_y32, &st.full[s], nc * 64, t.row, t.rows);
+            for (int nc = n0; ok && nc < n1; ++nc) {
+                ok = __all_sync(0xFFFFFFFFu, ptx::mbar_wait(&st.empty[s], ph ^ 1));
+                if (!ok) break;
+                uint8_t* b = smem + s * S::kStage;
+                if (leader) {
+                    ptx::mbar_arrive_expect_tx(&st.full[s], boxes.bytes() + (t.adapter >= 0 ? S::kW : 0));
                     if (t.adapter >= 0)
 #pragma unroll
                         for (int kb = 0; kb < S::kBlocks; ++kb)
                             ptx::tma_load_3d(b + kXBytes + kb * 8192, &map_b, &st.full[s], kb * 64, nc * 64, t.adapter);
-                    ++fills;
-                    if (++s == kStages) { s = 0; ph ^= 1; }
+                    boxes.load(b, &map_y8, &map_y32, &map_y128, &st.full[s], nc * 64, t.row);
                 }
-                if (!ok) fail();
+                ++fills;
+                if (++s == kStages) { s = 0; ph ^= 1; }
             }
-            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
         }
-        if (lane == 0 && !ptx::ring_drain(st.full, kStages, fills)) fail();
+        if (!ok) fail();
+        if (leader && !ptx::ring_drain(st.full, kStages, fills)) fail();
     } else if (warp == 1) {
         constexpr uint32_t idesc1 = ptx::idesc_bf16(kTileM, kR), idesc2 = ptx::idesc_bf16(kTileM, 64);
         const uint64_t dx = ptx::sdesc_sw128(ptx::smem_u32(smem)), dw = ptx::sdesc_sw128(ptx::smem_u32(smem + kXBytes));
         const uint64_t dh = ptx::sdesc_sw128(ptx::smem_u32(hbuf));
         const int ksteps = (p.r + 15) / 16;
+        const bool leader = ptx::elect_one();
+        auto all = [&](bool got) { return __all_sync(0xFFFFFFFFu, got) != 0; };
         int s = 0;
         uint32_t ph = 0, it = 0, cc = 0;
         bool ok = true;
         for (int number = cluster; ok && walk.find(p, tile_rows, number, t); number += n_clusters) {
-            if (lane == 0) {
-                if (t.adapter >= 0) {
-                    for (int kc = k0; kc < k1; ++kc) {
-                        ok = ptx::mbar_wait(&st.full[s], ph);
-                        if (!ok) break;
-                        ptx::tc_fence_after();
-                        const uint64_t so = static_cast<uint64_t>(s) * (S::kStage >> 4);
+            if (t.adapter >= 0) {
+                for (int kc = k0; kc < k1; ++kc) {
+                    ok = all(ptx::mbar_wait(&st.full[s], ph));
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const uint64_t so = static_cast<uint64_t>(s) * (S::kStage >> 4);
+                    if (leader) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             ptx::mma_bf16(tmem, dx + so + kk * 2, dw + so + kk * 2, idesc1, kc > k0 || kk > 0);
                         ptx::mbar_arrive_n(&st.empty[s], 4);
                         ptx::tc_commit(&st.empty[s]);
-                        if (++s == kStages) { s = 0; ph ^= 1; }
                     }
-                    ptx::tc_commit(&st.d1_full);
-                    if (ok) ok = ptx::mbar_wait(&st.h_ready, it & 1);
-                    ++it;
-                    ptx::tc_fence_after();
+                    if (++s == kStages) { s = 0; ph ^= 1; }
                 }
-                for (int nc = n0; ok && nc < n1; ++nc, ++cc) {
-                    const uint32_t buf = cc % kBufs;
-                    ok = ptx::mbar_wait(&st.full[s], ph) && ptx::mbar_wait(&st.d2_empty[buf], ((cc / kBufs) & 1) ^ 1);
-                    if (!ok) break;
-                    if (t.adapter >= 0) {
-                        ptx::tc_fence_after();
-                        const uint64_t so = static_cast<uint64_t>(s) * (S::kStage >> 4);
-                        const uint32_t d = tmem + kD2Col + buf * 64;
-                        for (int kk = 0; kk < ksteps; ++kk) {
+                if (leader) ptx::tc_commit(&st.d1_full);
+                ok = ok && all(ptx::mbar_wait(&st.h_ready, it & 1));
+                ++it;
+                ptx::tc_fence_after();
+            }
+            for (int nc = n0; ok && nc < n1; ++nc, ++cc) {
+                const uint32_t buf = cc % kBufs;
+                ok = all(ptx::mbar_wait(&st.full[s], ph)) && all(ptx::mbar_wait(&st.d2_empty[buf], ((cc / kBufs) & 1) ^ 1));
+                if (!ok) break;
+                if (t.adapter >= 0) {
+                    ptx::tc_fence_after();
+                    const uint64_t so = static_cast<uint64_t>(s) * (S::kStage >> 4);
+                    const uint32_t d = tmem + kD2Col + buf * 64;
+                    if (leader) {
+#pragma unroll
+                        for (int kk = 0; kk < kR / 16; ++kk) {
+                            if (kk >= ksteps) break;
                             const uint64_t ho = (kk >> 2) * (kXBytes >> 4) + (kk & 3) * 2, bo = so + (kk >> 2) * (8192 >> 4) + (kk & 3) * 2;
                             ptx::mma_bf16(d, dh + ho, dw + bo, idesc2, kk > 0);
                             ptx::mma_bf16(d, dh + (S::kH >> 4) + ho, dw + bo, idesc2, 1);
                         }
                         ptx::tc_commit(&st.empty[s]);
                         ptx::tc_commit(&st.d2_full[buf]);
-                    } else {  // a tile to copy takes the same turns, without a product
-                        ptx::mbar_arrive(&st.empty[s]);
-                        ptx::mbar_arrive(&st.d2_full[buf]);
                     }
-                    if (++s == kStages) { s = 0; ph ^= 1; }
+                } else if (leader) {  // a tile to copy takes the same turns, without a product
+                    ptx::mbar_arrive(&st.empty[s]);
+                    ptx::mbar_arrive(&st.d2_full[buf]);
                 }
-                if (!ok) {
-                    fail();
-                    ptx::tc_commit(&st.drain);  // what was issued ends before the tensor memory goes
-                    ptx::mbar_wait(&st.drain, 0);
-                }
+                if (++s == kStages) { s = 0; ph ^= 1; }
             }
-            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+        }
+        if (!ok) {
+            fail();
+            if (leader) ptx::tc_commit(&st.drain);  // what was issued ends before the tensor memory goes
+            ptx::mbar_wait(&st.drain, 0);
         }
     } else {
         // group g: half of h's columns, every kGroups-th slice of phase 2; q: TMEM lane quarter
@@ -488,8 +504,9 @@ cudaError_t launch(const AdapterArgs& a, int cs, int64_t tiles, int sms, cudaStr
         if (e != cudaSuccess) return e;
         attr_set = true;
     }
-    CUtensorMap x8, x32, y8, y32, ma, mb;
+    CUtensorMap x8, x32, x128, y8, y32, y128, ma, mb;
     if (map_rows(&x8, a.x, a.K, a.T, a.ld_x, 8) != CUDA_SUCCESS || map_rows(&x32, a.x, a.K, a.T, a.ld_x, 32) != CUDA_SUCCESS ||
+        map_rows(&x128, a.x, a.K, a.T, a.ld_x, 128) != CUDA_SUCCESS || map_rows(&y128, a.y, a.N, a.T, a.ld_y, 128) != CUDA_SUCCESS ||
         map_rows(&y8, a.y, a.N, a.T, a.ld_y, 8) != CUDA_SUCCESS || map_rows(&y32, a.y, a.N, a.T, a.ld_y, 32) != CUDA_SUCCESS ||
         map_bank(&ma, a.a, a.K, a.r, a.n, kR) != CUDA_SUCCESS || map_bank(&mb, a.b, a.r, a.N, a.n, 64) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
@@ -508,7 +525,7 @@ cudaError_t launch(const AdapterArgs& a, int cs, int64_t tiles, int sms, cudaStr
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, k_adapter_add<kR, kRows>, a, kRows, x8, x32, y8, y32, ma, mb);
+    return cudaLaunchKernelEx(&cfg, k_adapter_add<kR, kRows>, a, kRows, x8, x32, x128, y8, y32, y128, ma, mb);
 }
 
 }  // namespace
