@@ -15,12 +15,13 @@
 // are not stored. The zero fill of TMA pads K, N and the rank.
 #include <cstdlib>
 
-#include "block.cuh"
-#include "ptx_cluster.cuh"
+#include "adapters.cuh"
 
 namespace moe {
 
 namespace {
+
+using namespace adapters;
 
 constexpr int kTileM = 128;            // rows of an MMA
 constexpr int kGroups = 2;             // epilogue groups of four warps; they take phase 2's slices in turn
@@ -64,52 +65,6 @@ constexpr size_t smem_bytes()
     return n;
 }
 
-struct Tile {
-    int row, rows, adapter;  // adapter -1: copy
-};
-
-// Walks the requests in order; every warp that needs the tiles has its own.
-struct Walk {
-    int base = 0, before = 0;  // first segment of the window, tiles before it
-
-    // Warp-wide. The tile of the given number (numbers must not go down), false past the last.
-    __device__ bool find(const AdapterArgs& p, int tile_rows, int number, Tile& t)
-    {
-        const int lane = threadIdx.x & 31;
-        for (; base < p.S; base += 32) {
-            const int s = base + lane;
-            int beg = 0, end = 0, ad = -1, n = 0;
-            if (s < p.S) {
-                beg = __ldg(p.seg_offsets + s);
-                end = __ldg(p.seg_offsets + s + 1);
-                ad = __ldg(p.seg_adapter + s);
-                const bool good = beg >= 0 && beg <= end && end <= p.T && ad >= -1 && ad < p.n;
-                if (good && !(ad < 0 && p.out == p.y)) n = (end - beg + tile_rows - 1) / tile_rows;
-            }
-            int sum = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-                if (lane >= o) sum += v;
-            }
-            const unsigned hit = __ballot_sync(0xFFFFFFFFu, before + sum > number);
-            if (hit) {
-                const int at = __ffs(hit) - 1;
-                // through warp reductions, whose results are uniform to the compiler: the addresses and loop
-                // bounds that the issuing warps make of them then need no moves to uniform registers
-                const bool me = lane == at;
-                const int row = beg + (number - (before + sum - n)) * tile_rows;
-                t.adapter = __reduce_max_sync(0xFFFFFFFFu, me ? ad : -1);
-                t.row = __reduce_max_sync(0xFFFFFFFFu, me ? row : 0);
-                t.rows = __reduce_max_sync(0xFFFFFFFFu, me ? min(tile_rows, end - row) : 0);
-                return true;
-            }
-            before += __shfl_sync(0xFFFFFFFFu, sum, 31);
-        }
-        return false;
-    }
-};
-
 // Rows [row, row + rows) x 64 columns at column c into dst, by one thread: boxes of 8 rows up to 24
 // rows, of 32 up to 96, else one of 128. box: the rows of a box, n: their number.
 struct Boxes {
@@ -126,16 +81,6 @@ struct Boxes {
 
 // 16-byte piece j of row r in the 128-byte-swizzled layout
 __device__ __forceinline__ uint32_t piece(int r, int j) { return r * 128 + ((j ^ (r & 7)) << 4); }
-
-// Two FP32 values (or zeros) as hi + lo, each two bf16: hi the nearest, lo the nearest to what is left.
-__device__ __forceinline__ void split(bool in, float u, float v, uint32_t& hi, uint32_t& lo)
-{
-    if (!in) u = v = 0.0f;  // a padded column stays zero where x is not finite, too
-    hi = pack_bf16x2(u, v);
-    const float uh = bf16_to_f32(hi & 0xFFFFu), vh = bf16_to_f32(hi >> 16);
-    // an infinity has no remainder
-    lo = pack_bf16x2(fabsf(uh) < INFINITY ? u - uh : 0.0f, fabsf(vh) < INFINITY ? v - vh : 0.0f);
-}
 
 template <int kR, int kRows>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -309,14 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         // one lane's wait result may differ from another's only in time: the warp agrees on it
         auto all = [&](bool got) { return __all_sync(0xFFFFFFFFu, got) != 0; };
-        if (cluster == 0 && rank == 0 && ew == 0) {
-            bool bad = __ldg(p.seg_offsets) != 0 || __ldg(p.seg_offsets + p.S) != p.T;
-            for (int i = lane; i < p.S; i += 32) {
-                const int beg = __ldg(p.seg_offsets + i), end = __ldg(p.seg_offsets + i + 1), ad = __ldg(p.seg_adapter + i);
-                bad |= beg < 0 || beg > end || end > p.T || ad < -1 || ad >= p.n;
-            }
-            if (bad) record_status(p.status, kDevBadSegment);
-        }
+        if (cluster == 0 && rank == 0 && ew == 0) check_segments(p);
         for (int number = cluster; ok && walk.find(p, tile_rows, number, t); number += n_clusters, ++tiles) {
             const bool live = q * 32 < t.rows;  // this warp has rows of the tile
             // a cluster: no warp is a tile ahead of another (their buffers are about to hold partial sums)
@@ -535,15 +473,14 @@ cudaError_t launch_adapter_add(const AdapterArgs& a, int sms, cudaStream_t strea
     if (a.T <= 0) return cudaSuccess;
     const int rows_force = std::getenv("AD_ROWS") ? atoi(std::getenv("AD_ROWS")) : 0;
     const int cs_force = std::getenv("AD_CS") ? atoi(std::getenv("AD_CS")) : 0;
-    // a request of L rows has ceil(L / rows) tiles: at most this many in all
-    auto tiles_of = [&](int rows) { return static_cast<int64_t>(a.T / rows) + (a.S < a.T ? a.S : a.T); };
-    int rows = tiles_of(32) <= 2 * sms ? 32 : 128;
+    int rows = a.T <= 8 * a.S ? 8 : a.T <= 4096 ? 32 : 128;
     if (rows_force) rows = rows_force;
-    const int64_t tiles = tiles_of(rows);
+    const int64_t tiles = adapter_tiles(a, rows == 33 ? 32 : rows);
     int cs = 8;
     while (cs > 1 && tiles * cs > sms) cs /= 2;
     if (cs_force) cs = cs_force;
-    if (rows == 32) {
+    if (rows <= 32) return launch_adapter_add_small(a, rows, cs, sms, stream);
+    if (rows == 33) {
         if (a.r <= 16) return launch<16, 32>(a, cs, tiles, sms, stream);
         if (a.r <= 32) return launch<32, 32>(a, cs, tiles, sms, stream);
         if (a.r <= 64) return launch<64, 32>(a, cs, tiles, sms, stream);

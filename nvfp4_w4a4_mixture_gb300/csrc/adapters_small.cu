@@ -1,0 +1,230 @@
+// adapters_small.cu -- low-rank adapters where requests are short or the batch is: tiles of up to 8
+// or 32 rows of one request, bounded by reading A and B (from L2 where requests share an adapter).
+//
+// One CTA of eight warps a tile, or a cluster that shares K and then N. Both products are mma.sync
+// m16n8k16 (bf16, FP32 sums) on operands loaded straight from global memory, 16 bytes a thread: a
+// thread's eight neighbouring k take the places of the fragments' k pairs in both operands alike, so
+// no operand passes through shared memory.
+//   phase 1  h[j][t] = A_j . x_t: rank rows on M, tokens on N; the warps share rank rows and K; their
+//            partial sums meet in shared memory (and through distributed shared memory in a cluster),
+//            always added in the same order; h scale = hi + lo, two bf16 values
+//   phase 2  d[t][c] = (hi + lo)_t . B_c: tokens on M, columns on N. Column 2q + e of product i stands
+//            for column 8q + 2i + e of 32, so that a thread ends with eight neighbouring columns of a
+//            row: one 16-byte load of y and one store of out
+#include "adapters.cuh"
+
+namespace moe {
+
+namespace {
+
+using namespace adapters;
+
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// d += a (rows g and g + 8) b over 32 k: two products of 16.
+__device__ __forceinline__ void mma32(float (&d)[4], const uint4& lo, const uint4& hi, const uint4& b)
+{
+    mma(d, lo.x, hi.x, lo.y, hi.y, b.x, b.y);
+    mma(d, lo.z, hi.z, lo.w, hi.w, b.z, b.w);
+}
+
+__device__ __forceinline__ uint4 load16(const uint16_t* p, bool in)
+{
+    return in ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
+}
+
+template <int kR, int kM>
+__global__ void __launch_bounds__(kThreads, 2) k_adapter_add_small(const __grid_constant__ AdapterArgs p)
+{
+    constexpr int kBlocks = kR / 16, kSplit = kWarps / kBlocks;  // 16-row blocks of the rank, warps that share K
+    constexpr int kSteps = (kR + 31) / 32, kTok = kM / 8, kRowTiles = (kM + 15) / 16;
+    constexpr int kHld = kSteps * 32 + 8;                        // a token's h in shared memory (padded: other banks)
+    constexpr int kUnroll1 = kM == 8 ? 8 : 4, kUnroll2 = kSteps == 1 ? 4 : kSteps == 2 ? 2 : 1;
+    __shared__ float part[kSplit][kR * kM];
+    __shared__ __align__(16) uint16_t h_s[2][kRowTiles * 16][kHld];
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, q = lane % 4;
+    const int cs = static_cast<int>(ptx::cluster_size()), rank = static_cast<int>(ptx::cluster_rank());
+    const int cluster = blockIdx.x / cs, n_clusters = gridDim.x / cs;
+    // rows of h that no token fills, and columns past the rank, stay zero
+    for (int i = tid; i < static_cast<int>(sizeof(h_s) / 4); i += kThreads) reinterpret_cast<uint32_t*>(h_s)[i] = 0u;
+    if (blockIdx.x == 0 && warp == 0) check_segments(p);
+    const int nc = (p.N + 31) / 32, c0 = nc * rank / cs, c1 = nc * (rank + 1) / cs;  // this CTA's slices of 32 columns
+    Walk walk;
+    Tile t;
+    for (int number = cluster; walk.find(p, kM, number, t); number += n_clusters) {
+        if (t.adapter < 0) {
+            const int w = min(c1 * 32, p.N) / 8 - c0 * 4;  // 16-byte pieces of a row
+            for (int i = tid; i < w * t.rows; i += kThreads) {
+                const int64_t row = t.row + i / w;
+                const int col = c0 * 32 + i % w * 8;
+                *reinterpret_cast<uint4*>(p.out + row * p.ld_out + col) = load16(p.y + row * p.ld_y + col, true);
+            }
+            continue;
+        }
+        {
+            const int rb = warp % kBlocks, kw = warp / kBlocks;
+            const int steps = (p.K + 31) / 32, share = cs * kSplit, me = rank * kSplit + kw;
+            const int s0 = steps * me / share, s1 = steps * (me + 1) / share;
+            const int j0 = rb * 16 + g;
+            const uint16_t* a0 = p.a + (static_cast<int64_t>(t.adapter) * p.r + j0) * p.K;
+            const uint16_t* x0 = p.x + (t.row + g) * p.ld_x;
+            float d[kTok][4] = {};
+            for (int s = s0; s < s1; s += kUnroll1) {
+                uint4 av[kUnroll1][2], xv[kUnroll1][kTok];
+#pragma unroll
+                for (int u = 0; u < kUnroll1; ++u) {
+                    const int k = (s + u) * 32 + q * 8;
+                    const bool in = s + u < s1 && k < p.K;
+                    av[u][0] = load16(a0 + k, in && j0 < p.r);
+                    av[u][1] = load16(a0 + static_cast<int64_t>(8) * p.K + k, in && j0 + 8 < p.r);
+#pragma unroll
+                    for (int i = 0; i < kTok; ++i) xv[u][i] = load16(x0 + static_cast<int64_t>(i) * 8 * p.ld_x + k, in && i * 8 + g < t.rows);
+                }
+#pragma unroll
+                for (int u = 0; u < kUnroll1; ++u)
+#pragma unroll
+                    for (int i = 0; i < kTok; ++i) mma32(d[i], av[u][0], av[u][1], xv[u][i]);
+            }
+            float* out = part[kw] + j0 * kM + 2 * q;
+#pragma unroll
+            for (int i = 0; i < kTok; ++i) {
+                *reinterpret_cast<float2*>(out + i * 8) = make_float2(d[i][0], d[i][1]);
+                *reinterpret_cast<float2*>(out + 8 * kM + i * 8) = make_float2(d[i][2], d[i][3]);
+            }
+        }
+        __syncthreads();
+        if (cs > 1) {
+            if (kSplit > 1) {
+                for (int i = tid; i < kR * kM; i += kThreads) {
+                    float v = part[0][i];
+#pragma unroll
+                    for (int w = 1; w < kSplit; ++w) v += part[w][i];
+                    part[0][i] = v;
+                }
+            }
+            ptx::cluster_sync();
+        }
+        const float f = __ldg(p.scale + t.adapter);
+        for (int i = tid; i < kR * kM / 2; i += kThreads) {  // rank rows 2j and 2j + 1 of a token
+            const int tok = i % kM, j = i / kM * 2;
+            float u = 0.0f, v = 0.0f;
+            if (cs > 1) {
+                for (int o = 0; o < cs; ++o) {
+                    const uint32_t at = ptx::cluster_addr(&part[0][j * kM + tok], o);
+                    u += ptx::cluster_load(at);
+                    v += ptx::cluster_load(at + kM * 4);
+                }
+            } else {
+#pragma unroll
+                for (int w = 0; w < kSplit; ++w) {
+                    u += part[w][j * kM + tok];
+                    v += part[w][(j + 1) * kM + tok];
+                }
+            }
+            uint32_t hi, lo;
+            split(j < p.r, u * f, v * f, hi, lo);
+            *reinterpret_cast<uint32_t*>(&h_s[0][tok][j]) = hi;
+            *reinterpret_cast<uint32_t*>(&h_s[1][tok][j]) = lo;
+        }
+        // the next tile's partial sums wait until all of the cluster have read these
+        if (cs > 1) ptx::cluster_sync();
+        else __syncthreads();
+
+        const uint16_t* b0 = p.b + static_cast<int64_t>(t.adapter) * p.N * p.r;
+        for (int c = c0 + warp * kUnroll2; c < c1; c += kWarps * kUnroll2) {
+            uint4 bv[kUnroll2][4][kSteps];
+#pragma unroll
+            for (int u = 0; u < kUnroll2; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int n = (c + u) * 32 + g / 2 * 8 + 2 * i + g % 2;
+#pragma unroll
+                    for (int s = 0; s < kSteps; ++s) {
+                        const int k = s * 32 + q * 8;
+                        bv[u][i][s] = load16(b0 + static_cast<int64_t>(n) * p.r + k, c + u < c1 && n < p.N && k < p.r);
+                    }
+                }
+#pragma unroll
+            for (int u = 0; u < kUnroll2; ++u) {
+                const int col = (c + u) * 32 + q * 8;
+                const bool in = c + u < c1 && col < p.N;
+#pragma unroll
+                for (int m = 0; m < kRowTiles; ++m) {
+                    const int r0 = m * 16 + g, r1 = r0 + 8;
+                    const uint16_t* y0 = p.y + (t.row + r0) * p.ld_y + col;
+                    const uint4 ya = load16(y0, in && r0 < t.rows);
+                    const uint4 yb = load16(y0 + static_cast<int64_t>(8) * p.ld_y, in && r1 < t.rows);
+                    float d[4][4] = {};
+#pragma unroll
+                    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+                        for (int part = 0; part < 2; ++part) {
+                            const uint4 ha = *reinterpret_cast<const uint4*>(&h_s[part][r0][s * 32 + q * 8]);
+                            const uint4 hb = *reinterpret_cast<const uint4*>(&h_s[part][r1][s * 32 + q * 8]);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) mma32(d[i], ha, hb, bv[u][i][s]);
+                        }
+                    const uint32_t yy[2][4] = {{ya.x, ya.y, ya.z, ya.w}, {yb.x, yb.y, yb.z, yb.w}};
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            o[i] = pack_bf16x2(bf16_to_f32(yy[e][i] & 0xFFFFu) + d[i][2 * e], bf16_to_f32(yy[e][i] >> 16) + d[i][2 * e + 1]);
+                        if (in && (e ? r1 : r0) < t.rows)
+                            *reinterpret_cast<uint4*>(p.out + (t.row + (e ? r1 : r0)) * p.ld_out + col) = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                }
+            }
+        }
+        __syncthreads();  // h is read
+    }
+    if (cs > 1) ptx::cluster_sync();
+}
+
+template <int kR, int kM>
+cudaError_t launch(const AdapterArgs& a, int cs, int sms, cudaStream_t stream)
+{
+    const int64_t tiles = adapter_tiles(a, kM), room = 2LL * sms / cs;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((tiles < room ? tiles : room) * cs));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cs;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, k_adapter_add_small<kR, kM>, a);
+}
+
+template <int kM>
+cudaError_t launch_rows(const AdapterArgs& a, int cs, int sms, cudaStream_t stream)
+{
+    if (a.r <= 16) return launch<16, kM>(a, cs, sms, stream);
+    if (a.r <= 32) return launch<32, kM>(a, cs, sms, stream);
+    if (a.r <= 64) return launch<64, kM>(a, cs, sms, stream);
+    return launch<128, kM>(a, cs, sms, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_adapter_add_small(const AdapterArgs& a, int rows, int cs, int sms, cudaStream_t stream)
+{
+    return rows == 8 ? launch_rows<8>(a, cs, sms, stream) : launch_rows<32>(a, cs, sms, stream);
+}
+
+}  // namespace moe

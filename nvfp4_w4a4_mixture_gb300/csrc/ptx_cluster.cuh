@@ -23,6 +23,7 @@ __device__ __forceinline__ uint32_t cluster_size()
 // All threads of all CTAs of the cluster (a hardware barrier; its CTAs run at the same time).
 __device__ __forceinline__ void cluster_sync()
 {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -33,6 +34,13 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank)
     uint32_t a;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
     return a;
+}
+
+__device__ __forceinline__ float cluster_load(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+    return v;
 }
 
 __device__ __forceinline__ float4 cluster_load4(uint32_t addr)
