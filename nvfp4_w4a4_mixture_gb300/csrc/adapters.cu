@@ -1,6 +1,6 @@
 // adapters.cu -- low-rank adapters of many requests: out[t] = y[t] + scale_a B_a (A_a x[t]).
 //
-// The requests' rows are cut into tiles of up to tile_rows (<= 128) rows of one request. A tile is
+// The requests' rows are cut into tiles of up to 128 rows of one request. A tile is
 // two tensor-core products (tcgen05 kind::f16, FP32 in tensor memory) of one CTA or of a cluster:
 //   phase 1  h = x A^T over this CTA's share of K, in slices of 64 columns
 //            (cluster: the partial h of all CTAs are added through distributed shared memory, in the
@@ -8,13 +8,12 @@
 //            h scale = hi + lo, two bf16 values (16 significant bits), written to shared memory as
 //            the A operand of
 //   phase 2  d = hi B^T + lo B^T over this CTA's share of N, in slices of 64 columns; out = y + d
-// Warp 0 streams both phases through one ring by TMA (x and A slices, then y and B slices: phase 2's
-// loads run while phase 1 ends), warp 1 issues the MMAs, warps 2-5 read the accumulators (one TMEM
-// lane quarter each), add y in the ring's buffer and store rows of 128 bytes.
+// Warps 0 and 2 stream both phases through one ring by TMA (x and A slices, then y and B slices: phase
+// 2's loads run while phase 1 ends), warp 1 issues the MMAs, two groups of four warps (a TMEM lane
+// quarter each) take phase 2's slices in turn: they read an accumulator, add y from the ring's buffer
+// and store rows.
 // Rows of a tile beyond its request's end hold whatever the buffers held; rows do not mix, and those
 // are not stored. The zero fill of TMA pads K, N and the rank.
-#include <cstdlib>
-
 #include "adapters.cuh"
 
 namespace moe {
@@ -25,27 +24,26 @@ using namespace adapters;
 
 constexpr int kTileM = 128;            // rows of an MMA
 constexpr int kGroups = 2;             // epilogue groups of four warps; they take phase 2's slices in turn
-constexpr int kEpiWarps = 4 * kGroups, kThreads = 64 + 32 * kEpiWarps;
+constexpr int kEpiWarps = 4 * kGroups, kFirstEpi = 3, kThreads = 32 * (kFirstEpi + kEpiWarps);
 constexpr int kBufs = 2 * kGroups;     // phase-2 accumulators
 constexpr uint32_t kD2Col = 128;       // TMEM columns: h at 0..127, the phase-2 accumulators behind it
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSmemMax = 227 * 1024;
 
-// kR: the rank, padded (16, 32, 64 or 128); kRows: rows that a tile's buffers hold (32 or 128). With 32
-// the MMAs read 96 rows more: what lies behind the buffers, inside this CTA's shared memory.
-template <int kR, int kRows>
+// kR: the rank, padded (16, 32, 64 or 128)
+template <int kR>
 struct Shape {
     static constexpr int kBlocks = (kR + 63) / 64;        // 64-column blocks of the rank
-    static constexpr int kX = kRows * 128;                // x or y slice: 64 bf16 a row
+    static constexpr int kX = kTileM * 128;               // x or y slice: 64 bf16 a row
     static constexpr int kW = kBlocks * 64 * 128;         // bytes of a B slice (64 rows), >= the A slice (kR rows of 128)
     static_assert(kW >= kR * 128, "an A slice fits");
     static constexpr int kStage = kX + kW;
     static constexpr int kH = kBlocks * kX;               // hi (or lo)
     static constexpr int kOutStage = kEpiWarps * 4096;    // 32 rows x 128 bytes a warp
-    static constexpr int kPart = kRows * kR * 4;          // a cluster's partial h, before the stores need their buffers
+    static constexpr int kPart = kTileM * kR * 4;         // a cluster's partial h, before the stores need their buffers
     static constexpr int kOut = kPart > kOutStage ? kPart : kOutStage;
     static constexpr int kStages = (kSmemMax - 2048 - 2 * kH - kOut) / kStage;
-    static_assert(kStages >= 3 && 2 * kH + kOut >= (kBlocks + 1) * kX * 1 + kTileM * 128, "buffers");
+    static_assert(kStages >= 3, "buffers");
 };
 
 template <int kStages>
@@ -56,10 +54,10 @@ struct Tail {
     int abort;
 };
 
-template <int kR, int kRows>
+template <int kR>
 constexpr size_t smem_bytes()
 {
-    using S = Shape<kR, kRows>;
+    using S = Shape<kR>;
     constexpr size_t n = 1024 + static_cast<size_t>(S::kStages) * S::kStage + 2 * S::kH + S::kOut + sizeof(Tail<S::kStages>);
     static_assert(n <= kSmemMax, "shared memory");
     return n;
@@ -82,15 +80,24 @@ struct Boxes {
 // 16-byte piece j of row r in the 128-byte-swizzled layout
 __device__ __forceinline__ uint32_t piece(int r, int j) { return r * 128 + ((j ^ (r & 7)) << 4); }
 
-template <int kR, int kRows>
+// Warp-wide: kN (a multiple of 4) columns of this warp's TMEM lanes.
+template <int kN>
+__device__ __forceinline__ void load_h(uint32_t taddr, uint32_t (&v)[kN])
+{
+#pragma unroll
+    for (int c = 0; c < kN; c += 4) ptx::tmem_ld4(taddr + c, v + c);
+    ptx::tmem_ld_wait();
+}
+
+template <int kR>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_adapter_add(const __grid_constant__ AdapterArgs p, int tile_rows, const __grid_constant__ CUtensorMap map_x8,
+    k_adapter_add(const __grid_constant__ AdapterArgs p, const __grid_constant__ CUtensorMap map_x8,
                   const __grid_constant__ CUtensorMap map_x32, const __grid_constant__ CUtensorMap map_x128,
                   const __grid_constant__ CUtensorMap map_y8, const __grid_constant__ CUtensorMap map_y32,
                   const __grid_constant__ CUtensorMap map_y128, const __grid_constant__ CUtensorMap map_a,
                   const __grid_constant__ CUtensorMap map_b)
 {
-    using S = Shape<kR, kRows>;
+    using S = Shape<kR>;
     constexpr int kXBytes = S::kX;
     constexpr int kStages = S::kStages;
     extern __shared__ uint8_t smem_raw[];
@@ -106,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
-            ptx::mbar_init(&st.full[s], 1);
+            ptx::mbar_init(&st.full[s], 2);   // the two loading warps
             ptx::mbar_init(&st.empty[s], 5);  // the MMA thread and the four warps of an epilogue group
         }
         ptx::mbar_init(&st.d1_full, 1);
@@ -144,37 +151,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The issuing warps run their loops whole and one lane issues: loop counters, addresses and
     // descriptors stay uniform (a loop inside `if (lane == 0)` took 460 cycles a slice of two TMA
     // copies and 120 an MMA, for moving its operands to uniform registers).
-    if (warp == 0) {
-        const bool leader = ptx::elect_one();
+    if (warp == 0 || warp == 2) {
+        // warp 0 loads x and y, warp 2 A and B (one warp's issue of both took 320 cycles a slice)
+        const bool leader = ptx::elect_one(), rows = warp == 0;
         int s = 0;
         uint32_t ph = 0, fills = 0;
         bool ok = true;
-        for (int number = cluster; ok && walk.find(p, tile_rows, number, t); number += n_clusters) {
+        for (int number = cluster; ok && walk.find(p, kTileM, number, t); number += n_clusters) {
             const Boxes boxes(t.rows);
             if (t.adapter >= 0)
                 for (int kc = k0; kc < k1; ++kc) {
-                    ok = __all_sync(0xFFFFFFFFu, ptx::mbar_wait(&st.empty[s], ph ^ 1));
+                    ok = __all_sync(0xFFFFFFFFu, ptx::mbar_wait_near(&st.empty[s], ph ^ 1));
                     if (!ok) break;
                     uint8_t* b = smem + s * S::kStage;
                     if (leader) {
-                        ptx::mbar_arrive_expect_tx(&st.full[s], boxes.bytes() + kR * 128);
-                        ptx::tma_load_3d(b + kXBytes, &map_a, &st.full[s], kc * 64, 0, t.adapter);
-                        boxes.load(b, &map_x8, &map_x32, &map_x128, &st.full[s], kc * 64, t.row);
+                        ptx::mbar_arrive_expect_tx(&st.full[s], rows ? boxes.bytes() : kR * 128);
+                        if (rows) boxes.load(b, &map_x8, &map_x32, &map_x128, &st.full[s], kc * 64, t.row);
+                        else ptx::tma_load_3d(b + kXBytes, &map_a, &st.full[s], kc * 64, 0, t.adapter);
                     }
                     ++fills;
                     if (++s == kStages) { s = 0; ph ^= 1; }
                 }
             for (int nc = n0; ok && nc < n1; ++nc) {
-                ok = __all_sync(0xFFFFFFFFu, ptx::mbar_wait(&st.empty[s], ph ^ 1));
+                ok = __all_sync(0xFFFFFFFFu, ptx::mbar_wait_near(&st.empty[s], ph ^ 1));
                 if (!ok) break;
                 uint8_t* b = smem + s * S::kStage;
                 if (leader) {
-                    ptx::mbar_arrive_expect_tx(&st.full[s], boxes.bytes() + (t.adapter >= 0 ? S::kW : 0));
-                    if (t.adapter >= 0)
+                    if (rows) {
+                        ptx::mbar_arrive_expect_tx(&st.full[s], boxes.bytes());
+                        boxes.load(b, &map_y8, &map_y32, &map_y128, &st.full[s], nc * 64, t.row);
+                    } else if (t.adapter >= 0) {
+                        ptx::mbar_arrive_expect_tx(&st.full[s], S::kW);
 #pragma unroll
                         for (int kb = 0; kb < S::kBlocks; ++kb)
                             ptx::tma_load_3d(b + kXBytes + kb * 8192, &map_b, &st.full[s], kb * 64, nc * 64, t.adapter);
-                    boxes.load(b, &map_y8, &map_y32, &map_y128, &st.full[s], nc * 64, t.row);
+                    } else {
+                        ptx::mbar_arrive(&st.full[s]);
+                    }
                 }
                 ++fills;
                 if (++s == kStages) { s = 0; ph ^= 1; }
@@ -192,10 +205,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         int s = 0;
         uint32_t ph = 0, it = 0, cc = 0;
         bool ok = true;
-        for (int number = cluster; ok && walk.find(p, tile_rows, number, t); number += n_clusters) {
+        for (int number = cluster; ok && walk.find(p, kTileM, number, t); number += n_clusters) {
             if (t.adapter >= 0) {
                 for (int kc = k0; kc < k1; ++kc) {
-                    ok = all(ptx::mbar_wait(&st.full[s], ph));
+                    ok = all(ptx::mbar_wait_near(&st.full[s], ph));
                     if (!ok) break;
                     ptx::tc_fence_after();
                     const uint64_t so = static_cast<uint64_t>(s) * (S::kStage >> 4);
@@ -215,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             for (int nc = n0; ok && nc < n1; ++nc, ++cc) {
                 const uint32_t buf = cc % kBufs;
-                ok = all(ptx::mbar_wait(&st.full[s], ph)) && all(ptx::mbar_wait(&st.d2_empty[buf], ((cc / kBufs) & 1) ^ 1));
+                ok = all(ptx::mbar_wait_near(&st.full[s], ph)) && all(ptx::mbar_wait_near(&st.d2_empty[buf], ((cc / kBufs) & 1) ^ 1));
                 if (!ok) break;
                 if (t.adapter >= 0) {
                     ptx::tc_fence_after();
@@ -245,8 +258,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_wait(&st.drain, 0);
         }
     } else {
-        // group g: half of h's columns, every kGroups-th slice of phase 2; q: TMEM lane quarter
-        const int ew = warp - 2, g = ew / 4, q = warp & 3, row = q * 32 + lane;
+        // group g: its share of h's columns, every kGroups-th slice of phase 2; q: TMEM lane quarter
+        const int ew = warp - kFirstEpi, g = ew / 4, q = warp & 3, row = q * 32 + lane;
         const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16);
         uint8_t* ob = obuf + ew * 4096;
         int s = 0;
@@ -255,35 +268,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         // one lane's wait result may differ from another's only in time: the warp agrees on it
         auto all = [&](bool got) { return __all_sync(0xFFFFFFFFu, got) != 0; };
         if (cluster == 0 && rank == 0 && ew == 0) check_segments(p);
-        for (int number = cluster; ok && walk.find(p, tile_rows, number, t); number += n_clusters, ++tiles) {
+        for (int number = cluster; ok && walk.find(p, kTileM, number, t); number += n_clusters, ++tiles) {
             const bool live = q * 32 < t.rows;  // this warp has rows of the tile
             // a cluster: no warp is a tile ahead of another (their buffers are about to hold partial sums)
             if (cs > 1 && tiles > 0) ok = all(ptx::mbar_wait(&st.idle, (tiles - 1) & 1));
             if (!ok) break;
             if (t.adapter >= 0) {
                 for (s += k1 - k0; s >= kStages; s -= kStages) ph ^= 1;  // phase 1's stages are not its own
-                constexpr int kHalf = kR / kGroups;
-                const int c0 = g * kHalf;
+                constexpr int kShare = kR / kGroups;
+                const int c0 = g * kShare;
                 const float f = __ldg(p.scale + t.adapter);
                 ok = all(ptx::mbar_wait(&st.d1_full, it & 1));
                 if (!ok) break;
                 ptx::tc_fence_after();
                 if (cs == 1) {
                     if (live) {
-                        uint32_t v[kHalf];
+                        uint32_t v[kShare];
+                        load_h<kShare>(tq + c0, v);
 #pragma unroll
-                        for (int c = 0; c < kHalf; c += 8) ptx::tmem_ld8(tq + c0 + c, v + c);
-                        ptx::tmem_ld_wait();
+                        for (int c = 0; c < kShare; c += 4) {
+                            uint32_t hi[2], lo[2];
 #pragma unroll
-                        for (int c = 0; c < kHalf; c += 8) {
-                            uint32_t hi[4], lo[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
+                            for (int i = 0; i < 2; ++i)
                                 split(c0 + c + 2 * i < p.r, __uint_as_float(v[c + 2 * i]) * f, __uint_as_float(v[c + 2 * i + 1]) * f,
                                       hi[i], lo[i]);
-                            uint8_t* d = hbuf + ((c0 + c) / 64) * kXBytes + piece(row, ((c0 + c) % 64) / 8);
-                            *reinterpret_cast<uint4*>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                            *reinterpret_cast<uint4*>(d + S::kH) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                            uint8_t* d = hbuf + ((c0 + c) / 64) * kXBytes + piece(row, ((c0 + c) % 64) / 8) + (c0 + c) % 8 * 2;
+                            *reinterpret_cast<uint2*>(d) = make_uint2(hi[0], hi[1]);
+                            *reinterpret_cast<uint2*>(d + S::kH) = make_uint2(lo[0], lo[1]);
                         }
                     }
                     ptx::tc_fence_before();
@@ -292,17 +303,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // writes it to all of the cluster
                     constexpr int kQuads = kR / 4, kMask = kQuads < 8 ? kQuads - 1 : 7;
                     if (live) {
-                        uint32_t v[kHalf];
+                        uint32_t v[kShare];
                         if (k0 < k1) {
-#pragma unroll
-                            for (int c = 0; c < kHalf; c += 8) ptx::tmem_ld8(tq + c0 + c, v + c);
-                            ptx::tmem_ld_wait();
+                            load_h<kShare>(tq + c0, v);
                         } else {
 #pragma unroll
-                            for (int c = 0; c < kHalf; ++c) v[c] = 0u;
+                            for (int c = 0; c < kShare; ++c) v[c] = 0u;
                         }
 #pragma unroll
-                        for (int c = 0; c < kHalf; c += 4)
+                        for (int c = 0; c < kShare; c += 4)
                             *reinterpret_cast<uint4*>(obuf + (row * kQuads + (((c0 + c) / 4) ^ (row & kMask))) * 16) =
                                 make_uint4(v[c], v[c + 1], v[c + 2], v[c + 3]);
                     }
@@ -347,57 +356,54 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++cc;
                 if (mine) {
                     // a stage or accumulator of another group may be a phase ahead: only its own are waited for
-                    ok = all(ptx::mbar_wait(&st.d2_full[buf], par)) && all(ptx::mbar_wait(&st.full[s], ph));
+                    ok = all(ptx::mbar_wait_near(&st.d2_full[buf], par)) && all(ptx::mbar_wait_near(&st.full[s], ph));
                     if (!ok) break;
-                    uint32_t o[8][4];
                     if (live) {
+                        // this lane's row: 64 sums, then with y 128 bytes of out (o[j]: piece j)
+                        uint32_t v[64], o[8][4];
+                        if (t.adapter >= 0) {
+                            ptx::tc_fence_after();
+#pragma unroll
+                            for (int c = 0; c < 64; c += 16)
+                                ptx::tmem_ld16(tq + kD2Col + buf * 64 + c, *reinterpret_cast<uint32_t(*)[16]>(v + c));
+                            ptx::tmem_ld_wait();
+                            ptx::tc_fence_before();
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 64; ++c) v[c] = 0u;
+                        }
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             const uint4 y = *reinterpret_cast<const uint4*>(yb + piece(row, j));
-                            o[j][0] = y.x, o[j][1] = y.y, o[j][2] = y.z, o[j][3] = y.w;
+                            const uint32_t yy[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                o[j][i] = pack_bf16x2(bf16_to_f32(yy[i] & 0xFFFFu) + __uint_as_float(v[j * 8 + 2 * i]),
+                                                      bf16_to_f32(yy[i] >> 16) + __uint_as_float(v[j * 8 + 2 * i + 1]));
                         }
-                    }
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&st.empty[s]);
-                    if (t.adapter >= 0) {
-                        ptx::tc_fence_after();
-                        if (live) {
-#pragma unroll
-                            for (int j0 = 0; j0 < 8; j0 += 4) {
-                                uint32_t v[2][16];
-                                ptx::tmem_ld16(tq + kD2Col + buf * 64 + j0 * 8, v[0]);
-                                ptx::tmem_ld16(tq + kD2Col + buf * 64 + j0 * 8 + 16, v[1]);
-                                ptx::tmem_ld_wait();
-#pragma unroll
-                                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) {
-                                        const int c = j * 8 + 2 * i;
-                                        uint32_t& w = o[j0 + j][i];
-                                        w = pack_bf16x2(bf16_to_f32(w & 0xFFFFu) + __uint_as_float(v[c / 16][c % 16]),
-                                                        bf16_to_f32(w >> 16) + __uint_as_float(v[c / 16][c % 16 + 1]));
-                                    }
-                            }
-                        }
-                        ptx::tc_fence_before();
                         __syncwarp();
-                    }
-                    if (lane == 0) ptx::mbar_arrive(&st.d2_empty[buf]);
-                    if (live) {
-                        // each lane holds a row of 128 bytes: through this warp's buffer, four rows a store instruction
+                        if (lane == 0) {
+                            ptx::mbar_arrive(&st.empty[s]);
+                            ptx::mbar_arrive(&st.d2_empty[buf]);
+                        }
+                        // through this warp's buffer, so that a store instruction writes four rows of 128 bytes
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
                             *reinterpret_cast<uint4*>(ob + piece(lane, j)) = make_uint4(o[j][0], o[j][1], o[j][2], o[j][3]);
                         __syncwarp();
-                        const int col = nc * 64 + (lane & 7) * 8;
+                        const int col = nc * 64 + (lane & 7) * 8, r0 = lane >> 3;
+                        uint16_t* dst = p.out + (t.row + q * 32 + r0) * p.ld_out + col;
+                        const uint8_t* src = ob + piece(r0, lane & 7);  // rows r0 + 4 i: every other one swaps halves of 64 bytes
+                        const int left = col < p.N ? t.rows - q * 32 - r0 : 0;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int r = i * 4 + (lane >> 3);
-                            if (q * 32 + r < t.rows && col < p.N)
-                                *reinterpret_cast<uint4*>(p.out + (t.row + q * 32 + r) * p.ld_out + col) =
-                                    *reinterpret_cast<const uint4*>(ob + piece(r, lane & 7));
-                        }
+                        for (int i = 0; i < 8; ++i)
+                            if (i * 4 < left)
+                                *reinterpret_cast<uint4*>(dst + i * 4 * p.ld_out) =
+                                    *reinterpret_cast<const uint4*>(ob + i * 512 + ((src - ob) ^ ((i & 1) * 64)));
                         __syncwarp();
+                    } else if (lane == 0) {
+                        ptx::mbar_arrive(&st.empty[s]);
+                        ptx::mbar_arrive(&st.d2_empty[buf]);
                     }
                 }
                 if (++s == kStages) { s = 0; ph ^= 1; }
@@ -432,13 +438,13 @@ CUresult map_bank(CUtensorMap* m, const uint16_t* base, int64_t cols, int64_t ro
     return encode_tmap_bf16(m, base, 3, dims, strides, box, 128);
 }
 
-template <int kR, int kRows>
+template <int kR>
 cudaError_t launch(const AdapterArgs& a, int cs, int64_t tiles, int sms, cudaStream_t stream)
 {
     static bool attr_set = false;
     if (!attr_set) {
-        cudaError_t e = cudaFuncSetAttribute(k_adapter_add<kR, kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem_bytes<kR, kRows>()));
+        cudaError_t e = cudaFuncSetAttribute(k_adapter_add<kR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(smem_bytes<kR>()));
         if (e != cudaSuccess) return e;
         attr_set = true;
     }
@@ -453,7 +459,7 @@ cudaError_t launch(const AdapterArgs& a, int cs, int64_t tiles, int sms, cudaStr
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(clusters * cs);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem_bytes<kR, kRows>();
+    cfg.dynamicSmemBytes = smem_bytes<kR>();
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -463,7 +469,7 @@ cudaError_t launch(const AdapterArgs& a, int cs, int64_t tiles, int sms, cudaStr
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, k_adapter_add<kR, kRows>, a, kRows, x8, x32, x128, y8, y32, y128, ma, mb);
+    return cudaLaunchKernelEx(&cfg, k_adapter_add<kR>, a, x8, x32, x128, y8, y32, y128, ma, mb);
 }
 
 }  // namespace
@@ -471,25 +477,17 @@ cudaError_t launch(const AdapterArgs& a, int cs, int64_t tiles, int sms, cudaStr
 cudaError_t launch_adapter_add(const AdapterArgs& a, int sms, cudaStream_t stream)
 {
     if (a.T <= 0) return cudaSuccess;
-    const int rows_force = std::getenv("AD_ROWS") ? atoi(std::getenv("AD_ROWS")) : 0;
-    const int cs_force = std::getenv("AD_CS") ? atoi(std::getenv("AD_CS")) : 0;
-    int rows = a.T <= 8 * a.S ? 8 : a.T <= 4096 ? 32 : 128;
-    if (rows_force) rows = rows_force;
-    const int64_t tiles = adapter_tiles(a, rows == 33 ? 32 : rows);
+    // short requests (8 rows or fewer on average) and batches too small to give every multiprocessor a
+    // tile of 128 rows go to the mma.sync kernel
+    const int rows = a.T <= 8LL * a.S ? 8 : a.T <= 4096 ? 32 : kTileM;
+    const int64_t tiles = adapter_tiles(a, rows);
     int cs = 8;
     while (cs > 1 && tiles * cs > sms) cs /= 2;
-    if (cs_force) cs = cs_force;
-    if (rows <= 32) return launch_adapter_add_small(a, rows, cs, sms, stream);
-    if (rows == 33) {
-        if (a.r <= 16) return launch<16, 32>(a, cs, tiles, sms, stream);
-        if (a.r <= 32) return launch<32, 32>(a, cs, tiles, sms, stream);
-        if (a.r <= 64) return launch<64, 32>(a, cs, tiles, sms, stream);
-        return launch<128, 32>(a, cs, tiles, sms, stream);
-    }
-    if (a.r <= 16) return launch<16, 128>(a, cs, tiles, sms, stream);
-    if (a.r <= 32) return launch<32, 128>(a, cs, tiles, sms, stream);
-    if (a.r <= 64) return launch<64, 128>(a, cs, tiles, sms, stream);
-    return launch<128, 128>(a, cs, tiles, sms, stream);
+    if (rows < kTileM) return launch_adapter_add_small(a, rows, cs, sms, stream);
+    if (a.r <= 16) return launch<16>(a, cs, tiles, sms, stream);
+    if (a.r <= 32) return launch<32>(a, cs, tiles, sms, stream);
+    if (a.r <= 64) return launch<64>(a, cs, tiles, sms, stream);
+    return launch<128>(a, cs, tiles, sms, stream);
 }
 
 }  // namespace moe
