@@ -625,7 +625,7 @@ moe_status_t moe_norm_residual(const moe_norm_t* N, const uint16_t* y, int64_t l
     a.ld_res_out = T > 1 ? ld_residual_out : H;
     a.x_out = x_out;
     a.ld_x = T > 1 ? ld_x : H;
-    MOE_CUDA(launch_norm_residual(a, static_cast<cudaStream_t>(stream)), "norm launch");
+    MOE_CUDA(launch_norm_residual(a, device_sm_count(), static_cast<cudaStream_t>(stream)), "norm launch");
     return MOE_OK;
 }
 

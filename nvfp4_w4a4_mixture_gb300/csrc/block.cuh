@@ -33,7 +33,7 @@ struct NormArgs {
     uint16_t* x_out;          // nullable
     int64_t ld_x;
 };
-cudaError_t launch_norm_residual(const NormArgs& a, cudaStream_t stream);
+cudaError_t launch_norm_residual(const NormArgs& a, int sms, cudaStream_t stream);
 
 // ---- select_experts.cu
 struct SelectArgs {
