@@ -16,7 +16,10 @@
 //   others   rows with fewer unmasked experts than k, more than kMaxCand candidates (many equal
 //            logits) or logits of +inf (whole_row)
 // The weights are computed from the chosen logits alone.
+#include <cfloat>
+
 #include "block.cuh"
+#include "topk.cuh"
 
 namespace moe {
 
@@ -143,22 +146,29 @@ __device__ __noinline__ unsigned exact_groups(const SelectArgs& a, int64_t t, co
     return __ballot_sync(kFull, real && j == 0 && rank < a.topk_group);
 }
 
+// A candidate: its value as an order-preserving key in the high word, the complement of its id in the
+// low one, so that a larger candidate goes first (larger value, then lower id).
+using Cand = unsigned long long;
+__device__ __forceinline__ Cand make_cand(float v, int id) { return static_cast<Cand>(order_key(v)) << 32 | static_cast<uint32_t>(~id); }
+__device__ __forceinline__ int cand_id(Cand c) { return ~static_cast<int>(static_cast<uint32_t>(c)); }
+__device__ __forceinline__ float cand_value(Cand c) { return key_value(static_cast<uint32_t>(c >> 32)); }
+
 // The first k + 1 of the C candidates in sel, ordered by FP64 values (c64: scratch for C of them).
 template <bool F32>
-__device__ __noinline__ void exact_ranking(const SelectArgs& a, int64_t t, const float2* cand, int C, double* c64, float2* sel)
+__device__ __noinline__ void exact_ranking(const SelectArgs& a, int64_t t, const Cand* cand, int C, double* c64, Cand* sel)
 {
     const Exact score = exact_scores<F32>(a, t, true);
     const int lane = threadIdx.x & 31;
     for (int q = lane; q < C; q += 32) {
-        const int e = __float_as_int(cand[q].y);
+        const int e = cand_id(cand[q]);
         c64[q] = score(load_logit<F32>(a, t, e)) + static_cast<double>(a.bias[e]);
     }
     __syncwarp();
     for (int q = lane; q < C; q += 32) {
         const double me = c64[q];
-        const int id = __float_as_int(cand[q].y);
+        const int id = cand_id(cand[q]);
         int r = 0;
-        for (int o = 0; o < C; ++o) r += ahead(c64[o], __float_as_int(cand[o].y), me, id);
+        for (int o = 0; o < C; ++o) r += ahead(c64[o], cand_id(cand[o]), me, id);
         if (r <= a.k) sel[r] = cand[q];
     }
     __syncwarp();
@@ -260,20 +270,20 @@ __device__ __forceinline__ int expert_of(int i, int lane)
 }
 
 template <int kNper, bool F32, bool VEC>
-__global__ void __launch_bounds__(kWarps * 32, kNper <= 16 ? 10 : 5) k_select_experts(const SelectArgs a)
+__global__ void __launch_bounds__(kWarps * 32, kNper <= 16 ? 8 : 4) k_select_experts(const __grid_constant__ SelectArgs a)
 {
     constexpr int kE = kNper * 32;
-    __shared__ double scratch_s[kWarps][kE < kMaxCand ? kMaxCand : kE];
-    __shared__ float2 cand_s[kWarps][kMaxCand];
-    __shared__ float2 sel_s[kWarps][33];
+    __shared__ __align__(16) double scratch_s[kWarps][kE < kMaxCand ? kMaxCand : kE];
+    __shared__ __align__(16) Cand cand_s[kWarps][kMaxCand];
+    __shared__ Cand sel_s[kWarps][33];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
     if (t >= a.T) return;
     float* c_s = reinterpret_cast<float*>(scratch_s[warp]);
-    float2* cand = cand_s[warp];
-    float2* sel = sel_s[warp];
+    Cand* cand = cand_s[warp];
+    Cand* sel = sel_s[warp];
     const int E = a.E, k = a.k;
 
     // logits; what is masked (NaN included) or no expert is -inf
@@ -314,6 +324,10 @@ __global__ void __launch_bounds__(kWarps * 32, kNper <= 16 ? 10 : 5) k_select_ex
 #pragma unroll
         for (int i = 1; i < kNper; ++i) m = fmaxf(m, c[i]);
         m = warp_max(m);
+        if (!(fabsf(m) < INFINITY)) {  // nothing but masked experts, or logits of +inf
+            whole_row<F32>(a, t, scratch_s[warp]);
+            return;
+        }
         if (need_sum) {
             float sum = 0.0f;
 #pragma unroll
@@ -321,45 +335,64 @@ __global__ void __launch_bounds__(kWarps * 32, kNper <= 16 ? 10 : 5) k_select_ex
             inv_sum = 1.0f / warp_sum(sum);
             smax = inv_sum;
         }
-        if (!(fabsf(m) < INFINITY)) {  // nothing but masked experts, or logits of +inf
-            whole_row<F32>(a, t, scratch_s[warp]);
-            return;
-        }
     }
-    auto score = [&](float l) { return a.sigmoid ? fast_rcp(1.0f + fast_exp(-l)) : fast_exp(l - m) * inv_sum; };
     if (a.bias) {
+        // a masked logit stays -inf; a NaN of the bias becomes -inf
+        auto choice = [&](float l, float s, float b) { return l > -INFINITY ? fmaxf(s + b, -INFINITY) : -INFINITY; };
+        float b[VEC ? 4 : 1];
 #pragma unroll
         for (int i = 0; i < kNper; ++i) {
             const int e = expert_of<VEC>(i, lane);
-            // a masked logit stays -inf; a NaN of the bias becomes -inf
-            const float b = e < E ? __ldg(a.bias + e) : -INFINITY;
-            c[i] = c[i] > -INFINITY ? fmaxf(score(c[i]) + b, -INFINITY) : -INFINITY;
+            if constexpr (VEC) {
+                if (i % 4 == 0) {
+                    const float4 v = e < E ? __ldg(reinterpret_cast<const float4*>(a.bias + e)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    b[0] = v.x, b[1] = v.y, b[2] = v.z, b[3] = v.w;
+                }
+            } else {
+                b[0] = e < E ? __ldg(a.bias + e) : 0.0f;
+            }
+            const float s = a.sigmoid ? fast_rcp(1.0f + fast_exp(-c[i])) : fast_exp(c[i] - m) * inv_sum;
+            c[i] = choice(c[i], s, b[VEC ? i % 4 : 0]);
         }
     }
     const float eps_score = (a.sigmoid ? kEpsSigmoid : kEpsSoftmax) * smax;
 
-    if (groups) {
+    // the values in order of their experts, for the groups and the candidates
 #pragma unroll
-        for (int i = 0; i < kNper; ++i) {
-            const int e = expert_of<VEC>(i, lane);
-            if (!VEC && e < E) c_s[e] = c[i];
-            if (VEC && i % 4 == 0 && e < E)
-                *reinterpret_cast<float4*>(c_s + e) = make_float4(c[i], c[(i + 1) % kNper], c[(i + 2) % kNper], c[(i + 3) % kNper]);
-        }
-        __syncwarp();
+    for (int i = 0; i < kNper; ++i) {
+        const int e = expert_of<VEC>(i, lane);
+        if (VEC && i % 4 == 0)
+            *reinterpret_cast<float4*>(c_s + e) = make_float4(c[i], c[(i + 1) % kNper], c[(i + 2) % kNper], c[(i + 3) % kNper]);
+        if (!VEC) c_s[e] = c[i];
+    }
+    __syncwarp();
+
+    if (groups) {
         const int size = E / a.n_group;
         const int lg = 31 - __clz(32 / a.n_group), per = 1 << lg;  // lanes a group
         const int g = lane >> lg, j = lane & (per - 1);
         float v1 = -INFINITY, v2 = -INFINITY;
+        auto take = [&](float v) {
+            v2 = fmaxf(v2, fminf(v1, v));
+            v1 = fmaxf(v1, v);
+        };
         if (g < a.n_group) {
             // the groups start at different places, so that their lanes read different banks
-            const int n = (size - j + per - 1) >> lg;  // this lane's values: j, j + per, ...
-            int i = n > 0 ? g % n : 0;
-            for (int q = 0; q < n; ++q) {
-                const float v = c_s[g * size + (i << lg) + j];
-                v2 = fmaxf(v2, fminf(v1, v));
-                v1 = fmaxf(v1, v);
-                if (++i == n) i = 0;
+            if constexpr (VEC) {  // groups are multiples of four there
+                const int n = (size / 4 - j + per - 1) >> lg;  // this lane's pieces of four: j, j + per, ...
+                int i = n > 0 ? g % n : 0;
+                for (int q = 0; q < n; ++q) {
+                    const float4 v = *reinterpret_cast<const float4*>(c_s + g * size + ((i << lg) + j) * 4);
+                    take(v.x), take(v.y), take(v.z), take(v.w);
+                    if (++i == n) i = 0;
+                }
+            } else {
+                const int n = (size - j + per - 1) >> lg;
+                int i = n > 0 ? g % n : 0;
+                for (int q = 0; q < n; ++q) {
+                    take(c_s[g * size + (i << lg) + j]);
+                    if (++i == n) i = 0;
+                }
             }
         }
         for (int o = per >> 1; o > 0; o >>= 1) {
@@ -369,6 +402,7 @@ __global__ void __launch_bounds__(kWarps * 32, kNper <= 16 ? 10 : 5) k_select_ex
         }
         float gv = v1;
         if (a.group_top2 && v1 > -INFINITY) {
+            auto score = [&](float l) { return a.sigmoid ? fast_rcp(1.0f + fast_exp(-l)) : fast_exp(l - m); };
             const float s1 = a.bias ? v1 : score(v1);
             gv = v2 > -INFINITY ? s1 + (a.bias ? v2 : score(v2)) : s1;
         }
@@ -380,17 +414,23 @@ __global__ void __launch_bounds__(kWarps * 32, kNper <= 16 ? 10 : 5) k_select_ex
         const bool real = g < a.n_group, stays = real && rank < a.topk_group;
         unsigned keep = __ballot_sync(kFull, stays && j == 0);
         if (a.bias || a.group_top2) {
-            const float lo = -warp_max(stays ? -gv : -INFINITY), hi = warp_max(real && !stays ? gv : -INFINITY);
+            // the last group that stays and the first that goes, by their ranks
+            const unsigned last = __ballot_sync(kFull, real && rank == a.topk_group - 1), first = __ballot_sync(kFull, real && rank == a.topk_group);
+            const float lo = __shfl_sync(kFull, gv, __ffs(last) - 1), hi = __shfl_sync(kFull, gv, __ffs(first) - 1);
             if (hi > -INFINITY && lo - hi <= 4.0f * eps_score + 2.0f * kEpsAdd * (fabsf(lo) + fabsf(hi)))
                 keep = exact_groups<F32>(a, t, c_s, a.group_top2 ? v2 : v1,
                                          a.bias ? 2.0f * (eps_score + kEpsAdd * fabsf(v1)) : 0.0f);
         }
         // e / size for e < 1024: exact, since 1023 * size <= 2^20 < 2^21
         const unsigned mul = ((1u << 21) + size - 1) / size;
+        bool in = false;
 #pragma unroll
         for (int i = 0; i < kNper; ++i) {
-            const unsigned ge = (static_cast<unsigned>(expert_of<VEC>(i, lane)) * mul) >> 21;
-            if (!((keep >> ((ge << lg) & 31u)) & 1u)) c[i] = -INFINITY;
+            if (!VEC || i % 4 == 0) {
+                const unsigned ge = (static_cast<unsigned>(expert_of<VEC>(i, lane)) * mul) >> 21;
+                in = (keep >> ((ge << lg) & 31u)) & 1u;
+            }
+            if (!in) c[i] = -INFINITY;
         }
     }
 
@@ -409,52 +449,50 @@ __global__ void __launch_bounds__(kWarps * 32, kNper <= 16 ? 10 : 5) k_select_ex
     tau = __shfl_sync(kFull, tau, k < 32 ? k : 31);
     // what can be among the k largest in exact arithmetic has a value of at least tau less two errors
     if (a.bias) tau -= 2.0f * (eps_score + kEpsAdd * fabsf(tau));
+    tau = fmaxf(tau, -FLT_MAX);  // a masked value is none
 
     // the values that reach it
     unsigned mine = 0;
 #pragma unroll
-    for (int i = 0; i < kNper; ++i) mine |= (c[i] >= tau && c[i] > -INFINITY ? 1u : 0u) << i;
-    const int cnt = __popc(mine);
-    int pos = cnt;
+    for (int i = 0; i < kNper; ++i) mine |= c[i] >= tau ? 1u << i : 0u;
+    int pos = __popc(mine);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(kFull, pos, o);
         if (lane >= o) pos += v;
     }
     const int C = __shfl_sync(kFull, pos, 31);
-    pos -= cnt;
     if (C < k || C > kMaxCand) {
         __syncwarp();
         whole_row<F32>(a, t, scratch_s[warp]);
         return;
     }
-#pragma unroll
-    for (int i = 0; i < kNper; ++i)
-        if ((mine >> i) & 1u) cand[pos++] = make_float2(c[i], __int_as_float(expert_of<VEC>(i, lane)));
+    for (pos -= __popc(mine); mine; mine &= mine - 1) {  // few lanes have more than one
+        const int i = __ffs(mine) - 1;
+        const int e = VEC ? ((i & ~3) * 32) + lane * 4 + (i & 3) : i * 32 + lane;
+        cand[pos++] = make_cand(c_s[e], e);
+    }
     __syncwarp();
     for (int q = lane; q < C; q += 32) {
-        const float2 me = cand[q];
-        const int id = __float_as_int(me.y);
+        const Cand me = cand[q];
         int r = 0;
-        for (int o = 0; o < C; ++o) {
-            const float2 v = cand[o];
-            r += v.x > me.x || (v.x == me.x && __float_as_int(v.y) < id);
-        }
+#pragma unroll 4
+        for (int o = 0; o < C; ++o) r += cand[o] > me;
         if (r <= k) sel[r] = me;
     }
     __syncwarp();
-    float2 me = sel[lane < k ? lane : 0];
+    Cand me = sel[lane < k ? lane : 0];
     if (a.bias) {
-        const float next = lane < k && lane + 1 < C ? sel[lane + 1].x : -INFINITY;
-        const bool near = next > -INFINITY && me.x - next <= 2.0f * eps_score + kEpsAdd * (fabsf(me.x) + fabsf(next));
+        const float v = cand_value(me), next = lane < k && lane + 1 < C ? cand_value(sel[lane + 1]) : -INFINITY;
+        const bool near = next > -INFINITY && v - next <= 2.0f * eps_score + kEpsAdd * (fabsf(v) + fabsf(next));
         if (__any_sync(kFull, near)) {
             __syncwarp();
             exact_ranking<F32>(a, t, cand, C, scratch_s[warp], sel);
             me = sel[lane < k ? lane : 0];
         }
     }
-    const int id = __float_as_int(me.y);
-    const float l = a.bias ? load_logit<F32>(a, t, id) : me.x;
+    const int id = cand_id(me);
+    const float l = a.bias ? load_logit<F32>(a, t, id) : cand_value(me);
     float s;
     if (a.renormalize) {
         // the scores divided by exp(largest chosen logit), or for sigmoid by no less than that: a factor
@@ -490,9 +528,11 @@ cudaError_t launch(const SelectArgs& a, bool vec, cudaStream_t stream)
 template <bool F32>
 cudaError_t launch_type(const SelectArgs& a, cudaStream_t stream)
 {
-    // four experts a load where every row allows it and there are enough for all lanes
+    // four experts a load where every row, the bias and the groups allow it and there are enough for all
+    // lanes
     constexpr int bytes = F32 ? 4 : 2;
-    const bool vec = a.E % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % (4 * bytes) == 0 && (a.ld % 4 == 0 || a.T == 1);
+    const bool vec = a.E % (4 * a.n_group) == 0 && reinterpret_cast<uintptr_t>(a.logits) % (4 * bytes) == 0 &&
+                     (a.ld % 4 == 0 || a.T == 1) && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
     if (a.E <= 32) return launch<1, F32>(a, vec, stream);
     if (a.E <= 64) return launch<2, F32>(a, vec, stream);
     if (a.E <= 128) return launch<4, F32>(a, vec && a.E > 64, stream);
