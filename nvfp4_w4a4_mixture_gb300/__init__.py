@@ -139,7 +139,8 @@ def _p(t):
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    # the current stream's handle without a torch.cuda.Stream object (3 us of a call on an Arm host)
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def moe_workspace_bytes(H, E, k, I, T):
@@ -406,14 +407,31 @@ def moe_layer_forward_profiled(layer, x, events, residual=None, out=None, ws=Non
     return out
 
 
-def _cuda(t, name, dtype, *shape):
-    """t's data pointer, checked: a CUDA tensor of `dtype` and `shape` whose last dimension is contiguous."""
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def _refuse(t, name, dtype, shape):
     if t.dtype != dtype or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor of %s, got %s on %s" % (name, dtype, t.dtype, t.device))
-    if tuple(t.shape) != shape or (shape[-1] > 1 and t.stride(-1) != 1):
-        raise ValueError("%s must have shape %s and a contiguous last dimension, got %s with strides %s"
-                         % (name, shape, tuple(t.shape), t.stride()))
+    raise ValueError("%s must have shape %s and be contiguous (rows may be strided where that is allowed), got %s with strides %s"
+                     % (name, tuple(shape), tuple(t.shape), t.stride()))
+
+
+def _whole(t, name, dtype, shape):
+    """The data pointer of a contiguous CUDA tensor of that type and shape (an int or None, as ctypes takes it)."""
+    if t.dtype is not dtype or not t.is_cuda or t.shape != shape or not t.is_contiguous():
+        _refuse(t, name, dtype, shape)
     return t.data_ptr()
+
+
+def _rows(t, name, dtype, shape):
+    """(data pointer, elements between two rows) of a CUDA tensor of that type and shape [T, n] whose rows are contiguous."""
+    if t.dtype is dtype and t.is_cuda and t.shape == shape:
+        if t.is_contiguous():
+            return t.data_ptr(), shape[1]
+        if shape[1] == 1 or t.stride(1) == 1:
+            return t.data_ptr(), t.stride(0)
+    _refuse(t, name, dtype, shape)
 
 
 def moe_norm_residual(y, residual, w_post=None, w_pre=None, gate=None, residual_scale=1.0, eps=1e-6, w_offset=0.0,
@@ -422,37 +440,41 @@ def moe_norm_residual(y, residual, w_post=None, w_pre=None, gate=None, residual_
     before the next block (with w_pre): returns (residual_out, x_out), x_out None without w_pre.
 
     y: bf16 [T, H] or None; residual: bf16 or fp32 [T, H] or None. gate: bf16 or fp32, [H] (per channel),
-    [T, 1] (per token), [T, H] or [1, 1]. out: optional (residual_out, x_out) to write into; an entry of
-    None is left out (x_out) or allocated (residual_out). Rows may be strided."""
+    [T, 1] (per token), [T, H] or [1, 1]. out: optional (residual_out, x_out) to write into; a None among
+    them is allocated. Rows may be strided."""
     like = y if y is not None else residual
     if like is None:
         raise ValueError("y and residual are both None")
-    T, H = like.shape
-    bf = torch.bfloat16
-    rt = residual.dtype if residual is not None else bf
-    if rt not in (bf, torch.float32):
+    shape = like.shape
+    T, H = shape
+    rt = residual.dtype if residual is not None else _BF16
+    if rt is not _BF16 and rt is not _F32:
         raise TypeError("residual must be bf16 or fp32, got %s" % rt)
     r_out, x_out = out if out is not None else (None, None)
     if r_out is None:
         r_out = torch.empty(T, H, dtype=rt, device=like.device)
     if x_out is None and w_pre is not None:
-        x_out = torch.empty(T, H, dtype=bf, device=like.device)
+        x_out = torch.empty(T, H, dtype=_BF16, device=like.device)
     g_ptr, g_type, g_channel, g_ld = None, 0, 0, 0
     if gate is not None:
-        if gate.dim() == 1:
-            gate = gate.unsqueeze(0)
-        g_type = DTYPE_F32 if gate.dtype == torch.float32 else DTYPE_BF16
-        g_channel = int(gate.shape[1] != 1)
-        g_ptr = _cuda(gate, "gate", torch.float32 if g_type else bf, 1 if gate.shape[0] == 1 else T, H if g_channel else 1)
-        g_ld = gate.stride(0) if gate.shape[0] > 1 else 0
-    d = NormDesc(H, None if w_post is None else _cuda(w_post, "w_post", bf, H),
-                 None if w_pre is None else _cuda(w_pre, "w_pre", bf, H), eps, w_offset, residual_scale,
-                 int(rt == torch.float32), g_ptr, g_type, g_channel, g_ld)
-    y_ptr, y_ld = (None, 0) if y is None else (_cuda(y, "y", bf, T, H), y.stride(0))
-    r_ptr, r_ld = (None, 0) if residual is None else (_cuda(residual, "residual", rt, T, H), residual.stride(0))
-    x_ptr, x_ld = (None, 0) if x_out is None else (_cuda(x_out, "x_out", bf, T, H), x_out.stride(0))
-    _check(lib().moe_norm_residual(ctypes.byref(d), y_ptr, y_ld, r_ptr, r_ld, T, _cuda(r_out, "residual_out", rt, T, H),
-                                   r_out.stride(0), x_ptr, x_ld, _stream()))
+        g_shape = gate.shape
+        if len(g_shape) == 1:
+            gate, g_shape = gate.unsqueeze(0), (1, g_shape[0])
+        g_type = DTYPE_F32 if gate.dtype is _F32 else DTYPE_BF16
+        g_channel = int(g_shape[1] != 1)
+        g_ptr, g_ld = _rows(gate, "gate", _F32 if g_type else _BF16, (1 if g_shape[0] == 1 else T, H if g_channel else 1))
+        if g_shape[0] == 1:
+            g_ld = 0
+    d = NormDesc(H, None if w_post is None else _whole(w_post, "w_post", _BF16, (H,)),
+                 None if w_pre is None else _whole(w_pre, "w_pre", _BF16, (H,)), eps, w_offset, residual_scale,
+                 DTYPE_F32 if rt is _F32 else DTYPE_BF16, g_ptr, g_type, g_channel, g_ld)
+    y_ptr, y_ld = (None, 0) if y is None else _rows(y, "y", _BF16, shape)
+    r_ptr, r_ld = (None, 0) if residual is None else _rows(residual, "residual", rt, shape)
+    ro_ptr, ro_ld = _rows(r_out, "residual_out", rt, shape)
+    x_ptr, x_ld = (None, 0) if x_out is None else _rows(x_out, "x_out", _BF16, shape)
+    status = lib().moe_norm_residual(d, y_ptr, y_ld, r_ptr, r_ld, T, ro_ptr, ro_ld, x_ptr, x_ld, _stream())
+    if status:
+        _check(status)
     return r_out, x_out
 
 
@@ -461,16 +483,16 @@ def moe_select_experts(logits, k, bias=None, score=SCORE_SOFTMAX, n_group=1, top
     """The k experts of each token and their weights from logits [T, E] (bf16 or fp32, rows may be strided):
     (ids int32 [T, k], weights fp32 [T, k]). bias: fp32 [E], for the choice alone. out: optional (ids, weights)."""
     T, E = logits.shape
-    lt = DTYPE_F32 if logits.dtype == torch.float32 else DTYPE_BF16
-    ids, w = out if out is not None else (torch.empty(T, k, dtype=torch.int32, device=logits.device),
-                                          torch.empty(T, k, dtype=torch.float32, device=logits.device))
-    i_ptr, w_ptr = _cuda(ids, "ids", torch.int32, T, k), _cuda(w, "weights", torch.float32, T, k)
-    if not (ids.is_contiguous() and w.is_contiguous()):
-        raise ValueError("ids and weights must be contiguous")
-    d = RoutingDesc(E, k, score, n_group, topk_group, group_score, int(renormalize), scale,
-                    None if bias is None else _cuda(bias, "bias", torch.float32, E))
-    _check(lib().moe_select_experts(ctypes.byref(d), _cuda(logits, "logits", torch.float32 if lt else torch.bfloat16, T, E),
-                                    lt, logits.stride(0), T, i_ptr, w_ptr, _stream()))
+    lt = logits.dtype
+    l_ptr, l_ld = _rows(logits, "logits", _F32 if lt is _F32 else _BF16, (T, E))
+    ids, w = out if out is not None else (torch.empty(T, k, dtype=_I32, device=logits.device),
+                                          torch.empty(T, k, dtype=_F32, device=logits.device))
+    i_ptr, w_ptr = _whole(ids, "ids", _I32, (T, k)), _whole(w, "weights", _F32, (T, k))
+    d = RoutingDesc(E, k, score, n_group, topk_group, group_score, 1 if renormalize else 0, scale,
+                    None if bias is None else _whole(bias, "bias", _F32, (E,)))
+    status = lib().moe_select_experts(d, l_ptr, DTYPE_F32 if lt is _F32 else DTYPE_BF16, l_ld, T, i_ptr, w_ptr, _stream())
+    if status:
+        _check(status)
     return ids, w
 
 
@@ -482,15 +504,17 @@ def moe_adapter_add(x, y, a, b, scale, seg_offsets, seg_adapter, out=None, ws=No
     n, r, _ = a.shape
     N = y.shape[1]
     S = seg_adapter.shape[0]
-    bf, i32 = torch.bfloat16, torch.int32
     if out is None:
-        out = torch.empty(T, N, dtype=bf, device=y.device)
-    if not (a.is_contiguous() and b.is_contiguous()):
-        raise ValueError("a and b must be contiguous")
-    ws = ws or _ws(4096)
-    d = AdaptersDesc(n, r, K, N, _cuda(a, "a", bf, n, r, K), _cuda(b, "b", bf, n, N, r), _cuda(scale, "scale", torch.float32, n))
-    _check(lib().moe_adapter_add(ctypes.byref(d), _cuda(x, "x", bf, T, K), x.stride(0), T,
-                                 _cuda(seg_offsets, "seg_offsets", i32, S + 1), _cuda(seg_adapter, "seg_adapter", i32, S), S,
-                                 _cuda(y, "y", bf, T, N), y.stride(0), _cuda(out, "out", bf, T, N), out.stride(0), ws.ptr,
-                                 ws.nbytes, _stream()))
+        out = torch.empty(T, N, dtype=_BF16, device=y.device)
+    x_ptr, x_ld = _rows(x, "x", _BF16, (T, K))
+    y_ptr, y_ld = _rows(y, "y", _BF16, (T, N))
+    o_ptr, o_ld = _rows(out, "out", _BF16, (T, N))
+    d = AdaptersDesc(n, r, K, N, _whole(a, "a", _BF16, (n, r, K)), _whole(b, "b", _BF16, (n, N, r)), _whole(scale, "scale", _F32, (n,)))
+    if ws is None:
+        ws = _ws(4096)
+    status = lib().moe_adapter_add(d, x_ptr, x_ld, T, _whole(seg_offsets, "seg_offsets", _I32, (S + 1,)),
+                                   _whole(seg_adapter, "seg_adapter", _I32, (S,)), S, y_ptr, y_ld, o_ptr, o_ld,
+                                   ws.tensor.data_ptr(), ws.nbytes, _stream())
+    if status:
+        _check(status)
     return out
