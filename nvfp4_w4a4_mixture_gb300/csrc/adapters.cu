@@ -477,13 +477,21 @@ cudaError_t launch(const AdapterArgs& a, int cs, int64_t tiles, int sms, cudaStr
 cudaError_t launch_adapter_add(const AdapterArgs& a, int sms, cudaStream_t stream)
 {
     if (a.T <= 0) return cudaSuccess;
-    // short requests (8 rows or fewer on average) and batches too small to give every multiprocessor a
-    // tile of 128 rows go to the mma.sync kernel
-    const int rows = a.T <= 8LL * a.S ? 8 : a.T <= 4096 ? 32 : kTileM;
-    const int64_t tiles = adapter_tiles(a, rows);
-    int cs = 8;
-    while (cs > 1 && tiles * cs > sms) cs /= 2;
-    if (rows < kTileM) return launch_adapter_add_small(a, rows, cs, sms, stream);
+    // CTAs a tile of 128 rows: what fills the multiprocessors once. Clusters of eight need free multiprocessors
+    // side by side (20 of them took 18.2 us where 20 clusters of four took 11.3); a batch hardly ever has all
+    // the tiles that it could have, so a tenth more clusters of two are allowed.
+    const int64_t tiles = adapter_tiles(a, kTileM);
+    const int cs = tiles * 16 <= 2LL * (sms - sms / 8) ? 8 : tiles * 4 <= sms ? 4 : tiles * 20 <= 11LL * sms ? 2 : 1;
+    // Estimated times in ns, from sweeps over 1 to 16,384 tokens of 1 to 256 requests, ranks 16 and 64, K x N
+    // 2048 x 2048 and 512 x 1024 on 152 multiprocessors. Tiles of 8 rows: 4.5 us, 8 ns a tile and 122 ns a MB
+    // of A and B that the tiles read (256 single tokens, rank 64: 20.5 us against 36.9 with tiles of 128; 1,024
+    // tokens of one request, rank 16: 7.7 against 9.7). Tiles of 128: the chain of one tile, shorter the more
+    // CTAs share it, times the rounds of CTAs (2,048 tokens of 64 requests, rank 64: 18.4 us against 21.5; 16,384 of 24:
+    // 38 against 138).
+    const int64_t tiles8 = adapter_tiles(a, 8), width = a.K + a.N, bytes = 2LL * a.r * width;
+    const int64_t t8 = 4500 + tiles8 * (8 + bytes / 8200);
+    const int64_t chain = 8000 + width * (cs >= 4 ? 9 : cs == 2 ? 19 : 36) / 10, ctas = 10 * tiles * cs, round = 11LL * sms;
+    if (t8 <= (ctas <= round ? chain : chain * ctas / round)) return launch_adapter_add_small(a, sms, stream);
     if (a.r <= 16) return launch<16>(a, cs, tiles, sms, stream);
     if (a.r <= 32) return launch<32>(a, cs, tiles, sms, stream);
     if (a.r <= 64) return launch<64>(a, cs, tiles, sms, stream);

@@ -9,8 +9,8 @@ namespace moe {
 // A request of L rows has ceil(L / rows) tiles of up to `rows` rows: at most this many in all.
 inline int64_t adapter_tiles(const AdapterArgs& a, int rows) { return static_cast<int64_t>(a.T / rows) + (a.S < a.T ? a.S : a.T); }
 
-// Tiles of up to rows (8 or 32) rows on mma.sync (adapters_small.cu).
-cudaError_t launch_adapter_add_small(const AdapterArgs& a, int rows, int cs, int sms, cudaStream_t stream);
+// Tiles of up to 8 rows on mma.sync (adapters_small.cu).
+cudaError_t launch_adapter_add_small(const AdapterArgs& a, int sms, cudaStream_t stream);
 
 namespace adapters {
 
@@ -18,25 +18,29 @@ struct Tile {
     int row, rows, adapter;  // adapter -1: copy
 };
 
-// Walks the requests in order; every warp that needs the tiles has its own.
+// Walks the requests in order, 128 at a time (four neighbours a lane); every warp that needs the tiles
+// has its own.
 struct Walk {
-    int base = 0, before = 0;  // first segment of the window, tiles before it
+    int base = 0, before = 0;  // first request of the window, tiles before it
 
     // Warp-wide. The tile of the given number (numbers must not go down), false past the last.
     __device__ bool find(const AdapterArgs& p, int tile_rows, int number, Tile& t)
     {
         const int lane = threadIdx.x & 31;
-        for (; base < p.S; base += 32) {
-            const int s = base + lane;
-            int beg = 0, end = 0, ad = -1, n = 0;
-            if (s < p.S) {
-                beg = __ldg(p.seg_offsets + s);
-                end = __ldg(p.seg_offsets + s + 1);
-                ad = __ldg(p.seg_adapter + s);
-                const bool good = beg >= 0 && beg <= end && end <= p.T && ad >= -1 && ad < p.n;
-                if (good && !(ad < 0 && p.out == p.y)) n = (end - beg + tile_rows - 1) / tile_rows;
+        for (; base < p.S; base += 128) {
+            const int s = base + lane * 4;
+            int off[5], ad[4], n[4], sum = 0;
+#pragma unroll
+            for (int i = 0; i < 5; ++i) off[i] = s + i <= p.S ? __ldg(p.seg_offsets + s + i) : 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ad[i] = s + i < p.S ? __ldg(p.seg_adapter + s + i) : -2;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool good = off[i] >= 0 && off[i] <= off[i + 1] && off[i + 1] <= p.T && ad[i] >= -1 && ad[i] < p.n;
+                n[i] = good && !(ad[i] < 0 && p.out == p.y) ? (off[i + 1] - off[i] + tile_rows - 1) / tile_rows : 0;
+                sum += n[i];
             }
-            int sum = n;
+            const int mine = sum;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
@@ -44,14 +48,25 @@ struct Walk {
             }
             const unsigned hit = __ballot_sync(0xFFFFFFFFu, before + sum > number);
             if (hit) {
-                const int at = __ffs(hit) - 1;
+                int left = number - (before + sum - mine), row = 0, rows = 0, adapter = -1;
+                if (lane == __ffs(hit) - 1) {
+                    bool found = false;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (!found && left < n[i]) {
+                            found = true;
+                            adapter = ad[i];
+                            row = off[i] + left * tile_rows;
+                            rows = min(tile_rows, off[i + 1] - row);
+                        }
+                        left -= n[i];
+                    }
+                }
                 // through warp reductions, whose results are uniform to the compiler: the addresses and loop
                 // bounds that the issuing warps make of them then need no moves to uniform registers
-                const bool me = lane == at;
-                const int row = beg + (number - (before + sum - n)) * tile_rows;
-                t.adapter = __reduce_max_sync(0xFFFFFFFFu, me ? ad : -1);
-                t.row = __reduce_max_sync(0xFFFFFFFFu, me ? row : 0);
-                t.rows = __reduce_max_sync(0xFFFFFFFFu, me ? min(tile_rows, end - row) : 0);
+                t.adapter = __reduce_max_sync(0xFFFFFFFFu, adapter);
+                t.row = __reduce_max_sync(0xFFFFFFFFu, row);
+                t.rows = __reduce_max_sync(0xFFFFFFFFu, rows);
                 return true;
             }
             before += __shfl_sync(0xFFFFFFFFu, sum, 31);

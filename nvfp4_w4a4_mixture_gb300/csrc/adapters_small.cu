@@ -1,5 +1,5 @@
-// adapters_small.cu -- low-rank adapters where requests are short or the batch is: tiles of up to 8
-// or 32 rows of one request, bounded by reading A and B (from L2 where requests share an adapter).
+// adapters_small.cu -- low-rank adapters where requests are short or the batch is: tiles of up to 8 rows
+// of one request, bounded by reading A and B (from L2 where requests share an adapter).
 //
 // One CTA of eight warps a tile, or a cluster that shares K and then N. Both products are mma.sync
 // m16n8k16 (bf16, FP32 sums) on operands loaded straight from global memory, 16 bytes a thread: a
@@ -8,7 +8,7 @@
 //   phase 1  h[j][t] = A_j . x_t: rank rows on M, tokens on N; the warps share rank rows and K; their
 //            partial sums meet in shared memory (and through distributed shared memory in a cluster),
 //            always added in the same order; h scale = hi + lo, two bf16 values
-//   phase 2  d[t][c] = (hi + lo)_t . B_c: tokens on M, columns on N. Column 2q + e of product i stands
+//   phase 2  d[t][c] = (hi + lo)_t . B_c: tokens on M (half of it), columns on N. Column 2q + e of product i stands
 //            for column 8q + 2i + e of 32, so that a thread ends with eight neighbouring columns of a
 //            row: one 16-byte load of y and one store of out
 #include "adapters.cuh"
@@ -19,6 +19,7 @@ namespace {
 
 using namespace adapters;
 
+constexpr int kM = 8;  // rows of a tile
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
@@ -41,15 +42,15 @@ __device__ __forceinline__ uint4 load16(const uint16_t* p, bool in)
     return in ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
 }
 
-template <int kR, int kM>
+template <int kR>
 __global__ void __launch_bounds__(kThreads, 2) k_adapter_add_small(const __grid_constant__ AdapterArgs p)
 {
     constexpr int kBlocks = kR / 16, kSplit = kWarps / kBlocks;  // 16-row blocks of the rank, warps that share K
-    constexpr int kSteps = (kR + 31) / 32, kTok = kM / 8, kRowTiles = (kM + 15) / 16;
+    constexpr int kSteps = (kR + 31) / 32;                       // 32 ranks each
     constexpr int kHld = kSteps * 32 + 8;                        // a token's h in shared memory (padded: other banks)
-    constexpr int kUnroll1 = kM == 8 ? 8 : 4, kUnroll2 = kSteps == 1 ? 4 : kSteps == 2 ? 2 : 1;
+    constexpr int kUnroll1 = 8, kUnroll2 = kSteps <= 2 ? 4 / kSteps : 1;
     __shared__ float part[kSplit][kR * kM];
-    __shared__ __align__(16) uint16_t h_s[2][kRowTiles * 16][kHld];
+    __shared__ __align__(16) uint16_t h_s[2][kM][kHld];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, q = lane % 4;
@@ -78,30 +79,44 @@ __global__ void __launch_bounds__(kThreads, 2) k_adapter_add_small(const __grid_
             const int j0 = rb * 16 + g;
             const uint16_t* a0 = p.a + (static_cast<int64_t>(t.adapter) * p.r + j0) * p.K;
             const uint16_t* x0 = p.x + (t.row + g) * p.ld_x;
-            float d[kTok][4] = {};
+            float d[4] = {};
             for (int s = s0; s < s1; s += kUnroll1) {
-                uint4 av[kUnroll1][2], xv[kUnroll1][kTok];
+                uint4 av[kUnroll1][2], xv[kUnroll1];
 #pragma unroll
                 for (int u = 0; u < kUnroll1; ++u) {
                     const int k = (s + u) * 32 + q * 8;
                     const bool in = s + u < s1 && k < p.K;
                     av[u][0] = load16(a0 + k, in && j0 < p.r);
                     av[u][1] = load16(a0 + static_cast<int64_t>(8) * p.K + k, in && j0 + 8 < p.r);
-#pragma unroll
-                    for (int i = 0; i < kTok; ++i) xv[u][i] = load16(x0 + static_cast<int64_t>(i) * 8 * p.ld_x + k, in && i * 8 + g < t.rows);
+                    xv[u] = load16(x0 + k, in && g < t.rows);
                 }
 #pragma unroll
-                for (int u = 0; u < kUnroll1; ++u)
-#pragma unroll
-                    for (int i = 0; i < kTok; ++i) mma32(d[i], av[u][0], av[u][1], xv[u][i]);
+                for (int u = 0; u < kUnroll1; ++u) mma32(d, av[u][0], av[u][1], xv[u]);
             }
             float* out = part[kw] + j0 * kM + 2 * q;
-#pragma unroll
-            for (int i = 0; i < kTok; ++i) {
-                *reinterpret_cast<float2*>(out + i * 8) = make_float2(d[i][0], d[i][1]);
-                *reinterpret_cast<float2*>(out + 8 * kM + i * 8) = make_float2(d[i][2], d[i][3]);
-            }
+            *reinterpret_cast<float2*>(out) = make_float2(d[0], d[1]);
+            *reinterpret_cast<float2*>(out + 8 * kM) = make_float2(d[2], d[3]);
         }
+        // phase 2's first columns and their y come while the partial sums meet
+        uint4 bv[kUnroll2][4][kSteps], yv[kUnroll2];
+        const uint16_t* b0 = p.b + static_cast<int64_t>(t.adapter) * p.N * p.r;
+        auto load_b = [&](int c) {
+#pragma unroll
+            for (int u = 0; u < kUnroll2; ++u) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int n = (c + u) * 32 + g / 2 * 8 + 2 * i + g % 2;
+#pragma unroll
+                    for (int s = 0; s < kSteps; ++s) {
+                        const int k = s * 32 + q * 8;
+                        bv[u][i][s] = load16(b0 + static_cast<int64_t>(n) * p.r + k, c + u < c1 && n < p.N && k < p.r);
+                    }
+                }
+                const int col = (c + u) * 32 + q * 8;
+                yv[u] = load16(p.y + (t.row + g) * p.ld_y + col, c + u < c1 && col < p.N && g < t.rows);
+            }
+        };
+        load_b(c0 + warp * kUnroll2);
         __syncthreads();
         if (cs > 1) {
             if (kSplit > 1) {
@@ -140,51 +155,27 @@ __global__ void __launch_bounds__(kThreads, 2) k_adapter_add_small(const __grid_
         if (cs > 1) ptx::cluster_sync();
         else __syncthreads();
 
-        const uint16_t* b0 = p.b + static_cast<int64_t>(t.adapter) * p.N * p.r;
         for (int c = c0 + warp * kUnroll2; c < c1; c += kWarps * kUnroll2) {
-            uint4 bv[kUnroll2][4][kSteps];
-#pragma unroll
-            for (int u = 0; u < kUnroll2; ++u)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int n = (c + u) * 32 + g / 2 * 8 + 2 * i + g % 2;
-#pragma unroll
-                    for (int s = 0; s < kSteps; ++s) {
-                        const int k = s * 32 + q * 8;
-                        bv[u][i][s] = load16(b0 + static_cast<int64_t>(n) * p.r + k, c + u < c1 && n < p.N && k < p.r);
-                    }
-                }
+            if (c != c0 + warp * kUnroll2) load_b(c);
 #pragma unroll
             for (int u = 0; u < kUnroll2; ++u) {
                 const int col = (c + u) * 32 + q * 8;
-                const bool in = c + u < c1 && col < p.N;
+                float d[4][4] = {};
 #pragma unroll
-                for (int m = 0; m < kRowTiles; ++m) {
-                    const int r0 = m * 16 + g, r1 = r0 + 8;
-                    const uint16_t* y0 = p.y + (t.row + r0) * p.ld_y + col;
-                    const uint4 ya = load16(y0, in && r0 < t.rows);
-                    const uint4 yb = load16(y0 + static_cast<int64_t>(8) * p.ld_y, in && r1 < t.rows);
-                    float d[4][4] = {};
-#pragma unroll
-                    for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-                        for (int part = 0; part < 2; ++part) {
-                            const uint4 ha = *reinterpret_cast<const uint4*>(&h_s[part][r0][s * 32 + q * 8]);
-                            const uint4 hb = *reinterpret_cast<const uint4*>(&h_s[part][r1][s * 32 + q * 8]);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) mma32(d[i], ha, hb, bv[u][i][s]);
-                        }
-                    const uint32_t yy[2][4] = {{ya.x, ya.y, ya.z, ya.w}, {yb.x, yb.y, yb.z, yb.w}};
+                for (int s = 0; s < kSteps; ++s)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        uint32_t o[4];
+                        const uint4 h = *reinterpret_cast<const uint4*>(&h_s[e][g][s * 32 + q * 8]), none = make_uint4(0, 0, 0, 0);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            o[i] = pack_bf16x2(bf16_to_f32(yy[e][i] & 0xFFFFu) + d[i][2 * e], bf16_to_f32(yy[e][i] >> 16) + d[i][2 * e + 1]);
-                        if (in && (e ? r1 : r0) < t.rows)
-                            *reinterpret_cast<uint4*>(p.out + (t.row + (e ? r1 : r0)) * p.ld_out + col) = make_uint4(o[0], o[1], o[2], o[3]);
+                        for (int i = 0; i < 4; ++i) mma32(d[i], h, none, bv[u][i][s]);
                     }
-                }
+                const uint32_t yy[4] = {yv[u].x, yv[u].y, yv[u].z, yv[u].w};
+                uint32_t o[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    o[i] = pack_bf16x2(bf16_to_f32(yy[i] & 0xFFFFu) + d[i][0], bf16_to_f32(yy[i] >> 16) + d[i][1]);
+                if (c + u < c1 && col < p.N && g < t.rows)
+                    *reinterpret_cast<uint4*>(p.out + (t.row + g) * p.ld_out + col) = make_uint4(o[0], o[1], o[2], o[3]);
             }
         }
         __syncthreads();  // h is read
@@ -192,10 +183,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_adapter_add_small(const __grid_
     if (cs > 1) ptx::cluster_sync();
 }
 
-template <int kR, int kM>
-cudaError_t launch(const AdapterArgs& a, int cs, int sms, cudaStream_t stream)
+template <int kR>
+cudaError_t launch(const AdapterArgs& a, int cs, int64_t tiles, int sms, cudaStream_t stream)
 {
-    const int64_t tiles = adapter_tiles(a, kM), room = 2LL * sms / cs;
+    const int64_t room = 2LL * sms / cs;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((tiles < room ? tiles : room) * cs));
     cfg.blockDim = dim3(kThreads);
@@ -208,23 +199,24 @@ cudaError_t launch(const AdapterArgs& a, int cs, int sms, cudaStream_t stream)
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, k_adapter_add_small<kR, kM>, a);
-}
-
-template <int kM>
-cudaError_t launch_rows(const AdapterArgs& a, int cs, int sms, cudaStream_t stream)
-{
-    if (a.r <= 16) return launch<16, kM>(a, cs, sms, stream);
-    if (a.r <= 32) return launch<32, kM>(a, cs, sms, stream);
-    if (a.r <= 64) return launch<64, kM>(a, cs, sms, stream);
-    return launch<128, kM>(a, cs, sms, stream);
+    return cudaLaunchKernelEx(&cfg, k_adapter_add_small<kR>, a);
 }
 
 }  // namespace
 
-cudaError_t launch_adapter_add_small(const AdapterArgs& a, int rows, int cs, int sms, cudaStream_t stream)
+cudaError_t launch_adapter_add_small(const AdapterArgs& a, int sms, cudaStream_t stream)
 {
-    return rows == 8 ? launch_rows<8>(a, cs, sms, stream) : launch_rows<32>(a, cs, sms, stream);
+    // CTAs a tile: up to one round of two CTAs a multiprocessor, while a CTA keeps 64 KB of A and B to read
+    // (32 KB where there is room for all in one CTA a multiprocessor): 64 requests of rank 64 14.1 us with one
+    // CTA a tile, 9.5 with four; of rank 16 7.1 with one, 6.4 with two, 7.6 with four. Eight for a few tiles
+    // alone: 4 tokens of rank 64 6.7 us against 7.2 with four, 256 tokens of one request 9.0 against 7.6.
+    const int64_t tiles = adapter_tiles(a, kM), bytes = 2LL * a.r * (a.K + a.N);
+    int cs = tiles * 16 <= sms ? 8 : 4;
+    while (cs > 1 && (tiles * cs > 2LL * sms || bytes / cs < (tiles * cs > sms ? 65536 : 32768))) cs /= 2;
+    if (a.r <= 16) return launch<16>(a, cs, tiles, sms, stream);
+    if (a.r <= 32) return launch<32>(a, cs, tiles, sms, stream);
+    if (a.r <= 64) return launch<64>(a, cs, tiles, sms, stream);
+    return launch<128>(a, cs, tiles, sms, stream);
 }
 
 }  // namespace moe

@@ -355,6 +355,13 @@ def test_adapter_shapes(moe, r, K, N):
     check_adapter(moe, adapter_case([150, 3, 1, 17], [1, 0, -1, 1], 2, r, K, N))
 
 
+@pytest.mark.parametrize("r,K,N", [(8, 8, 8), (16, 72, 56), (24, 200, 2000), (48, 2056, 1032), (64, 512, 264), (120, 1000, 8), (128, 2048, 2048)])
+@pytest.mark.parametrize("lens", [[1100], [1500, 3, 1, 900, 128, 700], [129, 2] * 100])
+def test_adapter_long_requests(moe, r, K, N, lens):
+    # enough rows for the kernel of 128-row tiles, one CTA a tile or several
+    check_adapter(moe, adapter_case(lens, [(i % 4) - 1 if i else 1 for i in range(len(lens))], 3, r, K, N))
+
+
 def test_adapter_many_requests(moe):
     rng = np.random.default_rng(0)
     lens = [int(v) for v in rng.integers(0, 6, 700)]
