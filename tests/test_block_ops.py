@@ -115,7 +115,7 @@ def test_norm_sizes(moe, T, H):
     check_norm(moe, T, H, rt=torch.float32, gate="channel", alpha=0.5, off=1.0, seed=1)
 
 
-@pytest.mark.parametrize("gate,gate_type", itertools.product(["channel", "token", "element", "one"], [BF, torch.float32]))
+@pytest.mark.parametrize("gate,gate_type", list(itertools.product(["channel", "token", "element", "one"], [BF, torch.float32])))
 def test_norm_gates(moe, gate, gate_type):
     for T, H in ((5, 2048), (130, 264)):
         check_norm(moe, T, H, gate=gate, gate_type=gate_type, alpha=0.7071)
