@@ -311,14 +311,18 @@ __global__ void __launch_bounds__(kWarps * 32, kNper <= 16 ? 8 : 4) k_select_exp
             c[i] = e < E ? load_logit<F32>(a, t, e) : -INFINITY;
         }
     }
-#pragma unroll
-    for (int i = 0; i < kNper; ++i) c[i] = fmaxf(c[i], -INFINITY);
-
+    // Whether every logit and bias is finite: products with 0 add up to 0 then (on the FMA pipe, which has
+    // room; the comparisons that masks need run on the other, which has none).
+    float chk = 0.0f;
     // the row's maximum and the softmax's sum, where anything needs them
     const bool groups = a.n_group > 1 && a.topk_group < a.n_group;
     const bool need_sum = !a.sigmoid && (a.bias || !a.renormalize);
     float m = 0.0f, inv_sum = 1.0f, smax = 1.0f;
     const bool have_m = !a.sigmoid && (need_sum || groups);
+    if (have_m || groups) {  // elsewhere a NaN fails every comparison that it meets, as a masked value does
+#pragma unroll
+        for (int i = 0; i < kNper; ++i) c[i] = fmaxf(c[i], -INFINITY);
+    }
     if (have_m) {
         m = c[0];
 #pragma unroll
@@ -337,23 +341,34 @@ __global__ void __launch_bounds__(kWarps * 32, kNper <= 16 ? 8 : 4) k_select_exp
         }
     }
     if (a.bias) {
-        // a masked logit stays -inf; a NaN of the bias becomes -inf
-        auto choice = [&](float l, float s, float b) { return l > -INFINITY ? fmaxf(s + b, -INFINITY) : -INFINITY; };
-        float b[VEC ? 4 : 1];
+        float b[kNper];
 #pragma unroll
         for (int i = 0; i < kNper; ++i) {
             const int e = expert_of<VEC>(i, lane);
             if constexpr (VEC) {
                 if (i % 4 == 0) {
                     const float4 v = e < E ? __ldg(reinterpret_cast<const float4*>(a.bias + e)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    b[0] = v.x, b[1] = v.y, b[2] = v.z, b[3] = v.w;
+                    b[i] = v.x, b[(i + 1) % kNper] = v.y, b[(i + 2) % kNper] = v.z, b[(i + 3) % kNper] = v.w;
                 }
             } else {
-                b[0] = e < E ? __ldg(a.bias + e) : 0.0f;
+                b[i] = e < E ? __ldg(a.bias + e) : 0.0f;
             }
-            const float s = a.sigmoid ? fast_rcp(1.0f + fast_exp(-c[i])) : fast_exp(c[i] - m) * inv_sum;
-            c[i] = choice(c[i], s, b[VEC ? i % 4 : 0]);
         }
+#pragma unroll
+        for (int i = 0; i < kNper; ++i) chk = fmaf(c[i], 0.0f, fmaf(b[i], 0.0f, chk));
+        const bool finite = __all_sync(kFull, chk == 0.0f);  // false too where there are fewer experts than slots
+        auto scores = [&](auto score) {
+            if (finite) {
+#pragma unroll
+                for (int i = 0; i < kNper; ++i) c[i] = score(c[i]) + b[i];
+            } else {
+                // a masked logit stays -inf; a NaN of the logit or the bias becomes -inf
+#pragma unroll
+                for (int i = 0; i < kNper; ++i) c[i] = c[i] > -INFINITY ? fmaxf(score(c[i]) + b[i], -INFINITY) : -INFINITY;
+            }
+        };
+        if (a.sigmoid) scores([](float l) { return fast_rcp(1.0f + fast_exp(-l)); });
+        else scores([&](float l) { return fast_exp(l - m) * inv_sum; });
     }
     const float eps_score = (a.sigmoid ? kEpsSigmoid : kEpsSoftmax) * smax;
 
@@ -438,14 +453,18 @@ __global__ void __launch_bounds__(kWarps * 32, kNper <= 16 ? 8 : 4) k_select_exp
     float tau = c[0];
 #pragma unroll
     for (int i = 1; i < kNper; ++i) tau = fmaxf(tau, c[i]);
+    tau = fmaxf(tau, -INFINITY);  // a lane of NaN
+    // descending runs everywhere: where a stage wants an ascending one, the values change their sign for it
 #pragma unroll
-    for (int s = 2; s <= 32; s <<= 1)
+    for (int s = 2; s <= 32; s <<= 1) {
+        const float flip = ((lane & s) != 0) != ((lane & (s >> 1)) != 0 && s > 2) ? -1.0f : 1.0f;
+        tau *= flip;
 #pragma unroll
         for (int o = s >> 1; o > 0; o >>= 1) {
             const float v = __shfl_xor_sync(kFull, tau, o);
-            const bool larger = ((lane & o) == 0) == ((lane & s) == 0);  // descending runs where bit s is clear
-            tau = larger ? fmaxf(tau, v) : fminf(tau, v);
+            tau = (lane & o) == 0 ? fmaxf(tau, v) : fminf(tau, v);
         }
+    }
     tau = __shfl_sync(kFull, tau, k < 32 ? k : 31);
     // what can be among the k largest in exact arithmetic has a value of at least tau less two errors
     if (a.bias) tau -= 2.0f * (eps_score + kEpsAdd * fabsf(tau));
@@ -473,12 +492,21 @@ __global__ void __launch_bounds__(kWarps * 32, kNper <= 16 ? 8 : 4) k_select_exp
         cand[pos++] = make_cand(c_s[e], e);
     }
     __syncwarp();
-    for (int q = lane; q < C; q += 32) {
-        const Cand me = cand[q];
+    if (C <= 16) {  // two lanes a candidate
+        const Cand me = cand[lane >> 1];
         int r = 0;
 #pragma unroll 4
-        for (int o = 0; o < C; ++o) r += cand[o] > me;
-        if (r <= k) sel[r] = me;
+        for (int o = lane & 1; o < C; o += 2) r += cand[o] > me;
+        r += __shfl_xor_sync(kFull, r, 1);
+        if (lane < 2 * C && r <= k) sel[r] = me;
+    } else {
+        for (int q = lane; q < C; q += 32) {
+            const Cand me = cand[q];
+            int r = 0;
+#pragma unroll 4
+            for (int o = 0; o < C; ++o) r += cand[o] > me;
+            if (r <= k) sel[r] = me;
+        }
     }
     __syncwarp();
     Cand me = sel[lane < k ? lane : 0];
@@ -497,7 +525,7 @@ __global__ void __launch_bounds__(kWarps * 32, kNper <= 16 ? 8 : 4) k_select_exp
     if (a.renormalize) {
         // the scores divided by exp(largest chosen logit), or for sigmoid by no less than that: a factor
         // that the sum divides out, so that small scores keep their ratios
-        const float top = warp_max(lane < k ? l : -INFINITY);
+        const float top = a.bias ? warp_max(lane < k ? l : -INFINITY) : __shfl_sync(kFull, l, 0);
         if ((a.sigmoid ? top : have_m ? top - m : 0.0f) < -80.0f) {  // scores that underflow here: in FP64
             whole_row<F32>(a, t, scratch_s[warp]);
             return;
