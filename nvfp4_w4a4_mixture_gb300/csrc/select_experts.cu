@@ -11,8 +11,7 @@
 //            and ranked by (c descending, id ascending)
 //   exact    where two neighbours of the ranking, or the last group that stays and the first that
 //            goes, are nearer than their errors, the candidates are ranked again in FP64
-//            (exact_ranking, exact_groups). FP64 runs at 1/64 of the FP32 rate, so only the values
-//            that can matter are computed again
+//            (exact_ranking, exact_groups). Only the values that can matter are computed again
 //   others   rows with fewer unmasked experts than k, more than kMaxCand candidates (many equal
 //            logits) or logits of +inf (whole_row)
 // The weights are computed from the chosen logits alone.
@@ -75,16 +74,53 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
-// Scores in FP64. m: the row's largest logit (softmax); sum: its softmax sum, or 1 where only the
+// FP64 runs at 1/64 of the FP32 rate here (a warp instruction takes some 58 cycles), so the exponential
+// and the reciprocal are as short as 52 bits allow: the table-driven exponential of Tang (ACM TOMS 15,
+// 1989), x = (n / 32) ln 2 + r with |r| <= ln 2 / 64, exp(x) = 2^(n / 32) (1 + r + ... + r^6 / 720), and two
+// Newton steps from the FP32 reciprocal. Both are off by about an ulp; with the library's functions a token that
+// is ranked again took 2.8 us.
+__device__ const double kExp2[32] = {  // 2^(j / 32)
+    0x1.0000000000000p+0, 0x1.059b0d3158574p+0, 0x1.0b5586cf9890fp+0, 0x1.11301d0125b51p+0,
+    0x1.172b83c7d517bp+0, 0x1.1d4873168b9aap+0, 0x1.2387a6e756238p+0, 0x1.29e9df51fdee1p+0,
+    0x1.306fe0a31b715p+0, 0x1.371a7373aa9cbp+0, 0x1.3dea64c123422p+0, 0x1.44e086061892dp+0,
+    0x1.4bfdad5362a27p+0, 0x1.5342b569d4f82p+0, 0x1.5ab07dd485429p+0, 0x1.6247eb03a5585p+0,
+    0x1.6a09e667f3bcdp+0, 0x1.71f75e8ec5f74p+0, 0x1.7a11473eb0187p+0, 0x1.82589994cce13p+0,
+    0x1.8ace5422aa0dbp+0, 0x1.93737b0cdc5e5p+0, 0x1.9c49182a3f090p+0, 0x1.a5503b23e255dp+0,
+    0x1.ae89f995ad3adp+0, 0x1.b7f76f2fb5e47p+0, 0x1.c199bdd85529cp+0, 0x1.cb720dcef9069p+0,
+    0x1.d5818dcfba487p+0, 0x1.dfc97337b9b5fp+0, 0x1.ea4afa2a490dap+0, 0x1.f50765b6e4540p+0};
+
+__device__ __forceinline__ double exp64(double x)
+{
+    if (!(fabs(x) < 700.0)) return exp(x);
+    const int n = __double2int_rn(x * 0x1.71547652b82fep+5);
+    const double r = fma(n, -0x1.473de6af278edp-39, fma(n, -0x1.62e42fef00000p-6, x));  // the longer part of ln 2 / 32 is exact times n
+    double p = fma(r, 1.0 / 720, 1.0 / 120);
+    p = fma(r, p, 1.0 / 24);
+    p = fma(r, p, 1.0 / 6);
+    p = fma(r, p, 0.5);
+    p = fma(r, p, 1.0);
+    p = fma(r, p, 1.0) * kExp2[n & 31];
+    return __hiloint2double(__double2hiint(p) + ((n >> 5) << 20), __double2loint(p));
+}
+
+__device__ __forceinline__ double rcp64(double d)
+{
+    if (!(d < 1e30)) return 1.0 / d;
+    double r = fast_rcp(static_cast<float>(d));
+    r = fma(r, fma(-d, r, 1.0), r);
+    return fma(r, fma(-d, r, 1.0), r);
+}
+
+// Scores in FP64. m: the row's largest logit (softmax); scale: 1 / its softmax sum, or 1 where only the
 // order or ratios of scores are asked for.
 struct Exact {
     bool sigmoid;
-    double m, sum;
+    double m, scale;
     __device__ __forceinline__ double operator()(float l) const
     {
         if (!(l > -INFINITY)) return 0.0;
-        if (sigmoid) return 1.0 / (1.0 + exp(-static_cast<double>(l)));
-        return (l == m ? 1.0 : exp(static_cast<double>(l) - m)) / sum;
+        if (sigmoid) return rcp64(1.0 + exp64(-static_cast<double>(l)));
+        return (l == m ? 1.0 : exp64(static_cast<double>(l) - m)) * scale;
     }
 };
 
@@ -102,7 +138,7 @@ __device__ __noinline__ Exact exact_scores(const SelectArgs& a, int64_t t, bool 
     for (int e = lane; e < a.E; e += 32) sum += x(load_logit<F32>(a, t, e));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-    x.sum = sum;
+    x.scale = rcp64(sum);
     return x;
 }
 
@@ -155,20 +191,22 @@ __device__ __forceinline__ float cand_value(Cand c) { return key_value(static_ca
 
 // The first k + 1 of the C candidates in sel, ordered by FP64 values (c64: scratch for C of them).
 template <bool F32>
-__device__ __noinline__ void exact_ranking(const SelectArgs& a, int64_t t, const Cand* cand, int C, double* c64, Cand* sel)
+__device__ __noinline__ void exact_ranking(const SelectArgs& a, int64_t t, const Cand* cand, int C, unsigned long long* c64, Cand* sel)
 {
     const Exact score = exact_scores<F32>(a, t, true);
     const int lane = threadIdx.x & 31;
     for (int q = lane; q < C; q += 32) {
         const int e = cand_id(cand[q]);
-        c64[q] = score(load_logit<F32>(a, t, e)) + static_cast<double>(a.bias[e]);
+        // as an order-preserving integer (integers compare at their full rate); -0 does not arise from a sum
+        const long long v = __double_as_longlong(score(load_logit<F32>(a, t, e)) + static_cast<double>(a.bias[e]));
+        c64[q] = v < 0 ? ~static_cast<unsigned long long>(v) : static_cast<unsigned long long>(v) | 1ull << 63;
     }
     __syncwarp();
     for (int q = lane; q < C; q += 32) {
-        const double me = c64[q];
+        const unsigned long long me = c64[q];
         const int id = cand_id(cand[q]);
         int r = 0;
-        for (int o = 0; o < C; ++o) r += ahead(c64[o], cand_id(cand[o]), me, id);
+        for (int o = 0; o < C; ++o) r += c64[o] > me || (c64[o] == me && cand_id(cand[o]) < id);
         if (r <= a.k) sel[r] = cand[q];
     }
     __syncwarp();
@@ -515,7 +553,7 @@ __global__ void __launch_bounds__(kWarps * 32, kNper <= 16 ? 8 : 4) k_select_exp
         const bool near = next > -INFINITY && v - next <= 2.0f * eps_score + kEpsAdd * (fabsf(v) + fabsf(next));
         if (__any_sync(kFull, near)) {
             __syncwarp();
-            exact_ranking<F32>(a, t, cand, C, scratch_s[warp], sel);
+            exact_ranking<F32>(a, t, cand, C, reinterpret_cast<unsigned long long*>(scratch_s[warp]), sel);
             me = sel[lane < k ? lane : 0];
         }
     }
