@@ -48,6 +48,10 @@ struct SelectArgs {
     int64_t ld;
     int32_t* ids;
     float* w;
+    // set by the launcher: experts a group, log2 of the lanes that take a group, and the multiplier with
+    // which (e * group_of_mul) >> 21 is expert e's group
+    int group_size, group_lanes_log2;
+    unsigned group_of_mul;
 };
 cudaError_t launch_select_experts(const SelectArgs& a, cudaStream_t stream);
 

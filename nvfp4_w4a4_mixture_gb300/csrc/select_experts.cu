@@ -148,8 +148,8 @@ template <bool F32>
 __device__ __noinline__ unsigned exact_groups(const SelectArgs& a, int64_t t, const float* c_s, float v2, float margin)
 {
     const Exact score = exact_scores<F32>(a, t, a.bias != nullptr);
-    const int lane = threadIdx.x & 31, size = a.E / a.n_group;
-    const int lg = 31 - __clz(32 / a.n_group), per = 1 << lg, g = lane >> lg, j = lane & (per - 1);
+    const int lane = threadIdx.x & 31, size = a.group_size;
+    const int lg = a.group_lanes_log2, per = 1 << lg, g = lane >> lg, j = lane & (per - 1);
     const bool real = g < a.n_group;
     const float thr = v2 < INFINITY ? v2 - margin : v2;  // -inf where the group has one unmasked expert or none
     uint64_t hits = 0;              // this lane's values: j, j + per, ... (at most 43 of them)
@@ -421,8 +421,7 @@ __global__ void __launch_bounds__(kWarps * 32, kNper <= 16 ? 8 : 4) k_select_exp
     __syncwarp();
 
     if (groups) {
-        const int size = E / a.n_group;
-        const int lg = 31 - __clz(32 / a.n_group), per = 1 << lg;  // lanes a group
+        const int size = a.group_size, lg = a.group_lanes_log2, per = 1 << lg;
         const int g = lane >> lg, j = lane & (per - 1);
         float v1 = -INFINITY, v2 = -INFINITY;
         auto take = [&](float v) {
@@ -433,7 +432,7 @@ __global__ void __launch_bounds__(kWarps * 32, kNper <= 16 ? 8 : 4) k_select_exp
             // the groups start at different places, so that their lanes read different banks
             if constexpr (VEC) {  // groups are multiples of four there
                 const int n = (size / 4 - j + per - 1) >> lg;  // this lane's pieces of four: j, j + per, ...
-                int i = n > 0 ? g % n : 0;
+                int i = max(min(g, n - 1), 0);
                 for (int q = 0; q < n; ++q) {
                     const float4 v = *reinterpret_cast<const float4*>(c_s + g * size + ((i << lg) + j) * 4);
                     take(v.x), take(v.y), take(v.z), take(v.w);
@@ -441,7 +440,7 @@ __global__ void __launch_bounds__(kWarps * 32, kNper <= 16 ? 8 : 4) k_select_exp
                 }
             } else {
                 const int n = (size - j + per - 1) >> lg;
-                int i = n > 0 ? g % n : 0;
+                int i = max(min(g, n - 1), 0);
                 for (int q = 0; q < n; ++q) {
                     take(c_s[g * size + (i << lg) + j]);
                     if (++i == n) i = 0;
@@ -474,13 +473,11 @@ __global__ void __launch_bounds__(kWarps * 32, kNper <= 16 ? 8 : 4) k_select_exp
                 keep = exact_groups<F32>(a, t, c_s, a.group_top2 ? v2 : v1,
                                          a.bias ? 2.0f * (eps_score + kEpsAdd * fabsf(v1)) : 0.0f);
         }
-        // e / size for e < 1024: exact, since 1023 * size <= 2^20 < 2^21
-        const unsigned mul = ((1u << 21) + size - 1) / size;
         bool in = false;
 #pragma unroll
         for (int i = 0; i < kNper; ++i) {
             if (!VEC || i % 4 == 0) {
-                const unsigned ge = (static_cast<unsigned>(expert_of<VEC>(i, lane)) * mul) >> 21;
+                const unsigned ge = (static_cast<unsigned>(expert_of<VEC>(i, lane)) * a.group_of_mul) >> 21;
                 in = (keep >> ((ge << lg) & 31u)) & 1u;
             }
             if (!in) c[i] = -INFINITY;
@@ -612,7 +609,13 @@ cudaError_t launch_type(const SelectArgs& a, cudaStream_t stream)
 cudaError_t launch_select_experts(const SelectArgs& a, cudaStream_t stream)
 {
     if (a.T <= 0) return cudaSuccess;
-    return a.logits_f32 ? launch_type<true>(a, stream) : launch_type<false>(a, stream);
+    SelectArgs b = a;
+    b.group_size = a.E / a.n_group;
+    b.group_lanes_log2 = 0;
+    while ((2 << b.group_lanes_log2) * a.n_group <= 32) ++b.group_lanes_log2;
+    // e / size for e < 1024 as a product: exact, since 1023 * size <= 2^20 < 2^21
+    b.group_of_mul = ((1u << 21) + b.group_size - 1) / b.group_size;
+    return a.logits_f32 ? launch_type<true>(b, stream) : launch_type<false>(b, stream);
 }
 
 }  // namespace moe
