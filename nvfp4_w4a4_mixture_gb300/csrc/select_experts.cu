@@ -1,20 +1,22 @@
 // select_experts.cu -- the choice of k experts per token from given logits: softmax or sigmoid
 // scores, a bias for the choice alone, groups, top-k, weights.
 //
-// One warp per token, the E choice values c in registers (kNper a lane). Without a bias c is the
-// logit itself (a larger logit is a larger score), so the order is exact; with one, c = score + bias
-// in FP32 with an error of at most eps.
-//   groups   c goes to shared memory, 32 / n_group lanes (a power of two) take a group's two largest
-//            values, a warp-wide rank count keeps topk_group groups, the others' c become -inf
-//   choice   the 32 lane maxima are sorted across the lanes; the (k + 1)-th is a lower bound of the
+// kL lanes a token: 16 (two tokens a warp) for many tokens and up to 256 experts, else 32.
+// The E choice values c are in registers (kNper a lane). Without a bias c is the logit itself (a larger
+// logit is a larger score), so the order is exact; with one, c = score + bias in FP32 with an error of
+// at most eps.
+//   groups   c goes to shared memory, kL / n_group lanes (a power of two) take a group's two largest
+//            values, a rank count keeps topk_group groups, the others' c become -inf
+//   choice   the lane maxima are sorted across the lanes; the (k + 1)-th is a lower bound of the
 //            (k + 1)-th largest value, and the few values that reach it are compacted into a list
 //            and ranked by (c descending, id ascending)
 //   exact    where two neighbours of the ranking, or the last group that stays and the first that
 //            goes, are nearer than their errors, the candidates are ranked again in FP64
 //            (exact_ranking, exact_groups). Only the values that can matter are computed again
-//   others   rows with fewer unmasked experts than k, more than kMaxCand candidates (many equal
+//   others   rows with fewer unmasked experts than k, more candidates than the list holds (many equal
 //            logits) or logits of +inf (whole_row)
 // The weights are computed from the chosen logits alone.
+// Bounded by instruction issue: the steps across lanes cost what they cost for one token or for two.
 #include <cfloat>
 
 #include "block.cuh"
@@ -26,7 +28,6 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr unsigned kFull = 0xFFFFFFFFu;
-constexpr int kMaxCand = 128;  // of E <= 1024 values; ranked in FP64 in the same scratch
 
 // Bounds of a score's error relative to the row's largest possible score (1; softmax: the row's
 // largest). Exponential 2^(x log2 e): ex2.approx is off by 2^-22, its argument by 1.5 * 2^-24 |x|
@@ -142,14 +143,29 @@ __device__ __noinline__ Exact exact_scores(const SelectArgs& a, int64_t t, bool 
     return x;
 }
 
-// The groups that stay (bit of a group's first lane), from FP64 values; the FP32 choice values are in
-// c_s. Only what lies within the error of a group's second largest can be one of its two largest.
+// The groups that stay (a bit each), from FP64 values; the FP32 choice values are in c_s, off by at most
+// eps_score and their last rounding. Only what lies within that of a group's second largest can be one
+// of its two largest.
 template <bool F32>
-__device__ __noinline__ unsigned exact_groups(const SelectArgs& a, int64_t t, const float* c_s, float v2, float margin)
+__device__ __noinline__ unsigned exact_groups(const SelectArgs& a, int64_t t, const float* c_s, float eps_score)
 {
     const Exact score = exact_scores<F32>(a, t, a.bias != nullptr);
     const int lane = threadIdx.x & 31, size = a.group_size;
     const int lg = a.group_lanes_log2, per = 1 << lg, g = lane >> lg, j = lane & (per - 1);
+    float top = -INFINITY, v2 = -INFINITY;
+    if (g < a.n_group)
+        for (int i = j; i < size; i += per) {
+            const float v = c_s[g * size + i];
+            v2 = fmaxf(v2, fminf(top, v));
+            top = fmaxf(top, v);
+        }
+    for (int o = per >> 1; o > 0; o >>= 1) {
+        const float o1 = __shfl_xor_sync(kFull, top, o), o2 = __shfl_xor_sync(kFull, v2, o);
+        v2 = fmaxf(fminf(top, o1), fmaxf(v2, o2));
+        top = fmaxf(top, o1);
+    }
+    if (!a.group_top2) v2 = top;
+    const float margin = a.bias ? 2.0f * (eps_score + kEpsAdd * fabsf(top)) : 0.0f;
     const bool real = g < a.n_group;
     const float thr = v2 < INFINITY ? v2 - margin : v2;  // -inf where the group has one unmasked expert or none
     uint64_t hits = 0;              // this lane's values: j, j + per, ... (at most 43 of them)
@@ -179,7 +195,7 @@ __device__ __noinline__ unsigned exact_groups(const SelectArgs& a, int64_t t, co
         const double ov = __shfl_sync(kFull, gv, o << lg);
         rank += ov > gv || (ov == gv && o < g);
     }
-    return __ballot_sync(kFull, real && j == 0 && rank < a.topk_group);
+    return __reduce_or_sync(kFull, real && rank < a.topk_group ? 1u << g : 0u);
 }
 
 // A candidate: its value as an order-preserving key in the high word, the complement of its id in the
@@ -300,36 +316,58 @@ __device__ __forceinline__ void whole_row(const SelectArgs& a, int64_t t, double
     else whole_row<F32, float>(a, t, reinterpret_cast<float*>(scratch));
 }
 
-// Expert held in slot i of a lane: 4 neighbours a 16-byte (bf16: 8-byte) load, or one.
-template <bool VEC>
-__device__ __forceinline__ int expert_of(int i, int lane)
+template <int kL>
+__device__ __forceinline__ float lanes_max(float v)
 {
-    return VEC ? ((i >> 2) * 32 + lane) * 4 + (i & 3) : i * 32 + lane;
+#pragma unroll
+    for (int o = kL / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+    return v;
 }
 
-template <int kNper, bool F32, bool VEC>
-__global__ void __launch_bounds__(kWarps * 32, kNper <= 16 ? 8 : 4) k_select_experts(const __grid_constant__ SelectArgs a)
+template <int kL>
+__device__ __forceinline__ float lanes_sum(float v)
 {
-    constexpr int kE = kNper * 32;
-    __shared__ __align__(16) double scratch_s[kWarps][kE < kMaxCand ? kMaxCand : kE];
-    __shared__ __align__(16) Cand cand_s[kWarps][kMaxCand];
-    __shared__ Cand sel_s[kWarps][33];
+#pragma unroll
+    for (int o = kL / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+
+// Expert held in slot i of a token's lane: 4 neighbours a 16-byte (bf16: 8-byte) load, or one.
+template <int kL, bool VEC>
+__device__ __forceinline__ int expert_of(int i, int lane)
+{
+    return VEC ? ((i >> 2) * kL + lane) * 4 + (i & 3) : i * kL + lane;
+}
+
+template <int kL, int kNper, bool F32, bool VEC>
+__global__ void __launch_bounds__(kWarps * 32, kNper < 8 || (kL == 32 && kNper <= 16) ? 8 : kNper <= 16 ? 6 : 4) k_select_experts(const __grid_constant__ SelectArgs a)
+{
+    constexpr int kTok = 32 / kL, kE = kNper * kL;
+    constexpr int kCap = kL == 32 ? 128 : 64;  // candidates a token
+    // the choice values of kTok tokens, then FP64 values of one
+    __shared__ __align__(16) unsigned char scratch_s[kWarps][8 * (kE < kCap ? kCap : kE)];
+    __shared__ __align__(16) Cand cand_s[kWarps][kTok][kCap];
+    __shared__ Cand sel_s[kWarps][kTok][kL + 1];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-    if (t >= a.T) return;
-    float* c_s = reinterpret_cast<float*>(scratch_s[warp]);
-    Cand* cand = cand_s[warp];
-    Cand* sel = sel_s[warp];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / kL, sl = lane % kL;
+    const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kTok;
+    if (t0 >= a.T) return;
+    const bool valid = kL == 32 || t0 + sub < a.T;
+    const int64_t t = valid ? t0 + sub : t0;  // lanes past the last token repeat the one before and store nothing
+    float* c_all = reinterpret_cast<float*>(scratch_s[warp]);
+    float* c_s = c_all + sub * kE;
+    Cand* cand = cand_s[warp][sub];
+    Cand* sel = sel_s[warp][sub];
     const int E = a.E, k = a.k;
+    bool whole = false;  // this token goes to whole_row
 
-    // logits; what is masked (NaN included) or no expert is -inf
+    // logits; what is masked or no expert is -inf (or NaN until it is cleaned)
     float c[kNper];
     if constexpr (VEC) {
 #pragma unroll
         for (int i = 0; i < kNper; i += 4) {
-            const int e = expert_of<true>(i, lane);
+            const int e = expert_of<kL, true>(i, sl);
             c[i] = c[i + 1] = c[i + 2] = c[i + 3] = -INFINITY;
             if (e < E) {
                 if constexpr (F32) {
@@ -345,13 +383,11 @@ __global__ void __launch_bounds__(kWarps * 32, kNper <= 16 ? 8 : 4) k_select_exp
     } else {
 #pragma unroll
         for (int i = 0; i < kNper; ++i) {
-            const int e = expert_of<false>(i, lane);
+            const int e = expert_of<kL, false>(i, sl);
             c[i] = e < E ? load_logit<F32>(a, t, e) : -INFINITY;
         }
     }
-    // Whether every logit and bias is finite: products with 0 add up to 0 then (on the FMA pipe, which has
-    // room; the comparisons that masks need run on the other, which has none).
-    float chk = 0.0f;
+
     // the row's maximum and the softmax's sum, where anything needs them
     const bool groups = a.n_group > 1 && a.topk_group < a.n_group;
     const bool need_sum = !a.sigmoid && (a.bias || !a.renormalize);
@@ -365,36 +401,43 @@ __global__ void __launch_bounds__(kWarps * 32, kNper <= 16 ? 8 : 4) k_select_exp
         m = c[0];
 #pragma unroll
         for (int i = 1; i < kNper; ++i) m = fmaxf(m, c[i]);
-        m = warp_max(m);
+        m = lanes_max<kL>(m);
         if (!(fabsf(m) < INFINITY)) {  // nothing but masked experts, or logits of +inf
-            whole_row<F32>(a, t, scratch_s[warp]);
-            return;
+            if (kL == 32) {  // a warp with one token may leave at once
+                whole_row<F32>(a, t0, reinterpret_cast<double*>(scratch_s[warp]));
+                return;
+            }
+            whole = true;
+            m = 0.0f;
         }
         if (need_sum) {
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < kNper; ++i) sum += fast_exp(c[i] - m);
-            inv_sum = 1.0f / warp_sum(sum);
+            inv_sum = 1.0f / lanes_sum<kL>(sum);
             smax = inv_sum;
         }
     }
     if (a.bias) {
+        constexpr int kStep = VEC ? 4 : 1;
         float b[kNper];
 #pragma unroll
-        for (int i = 0; i < kNper; ++i) {
-            const int e = expert_of<VEC>(i, lane);
+        for (int i = 0; i < kNper; i += kStep) {
+            const int e = expert_of<kL, VEC>(i, sl);
             if constexpr (VEC) {
-                if (i % 4 == 0) {
-                    const float4 v = e < E ? __ldg(reinterpret_cast<const float4*>(a.bias + e)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    b[i] = v.x, b[(i + 1) % kNper] = v.y, b[(i + 2) % kNper] = v.z, b[(i + 3) % kNper] = v.w;
-                }
+                const float4 v = e < E ? __ldg(reinterpret_cast<const float4*>(a.bias + e)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                b[i] = v.x, b[i + 1] = v.y, b[i + 2] = v.z, b[i + 3] = v.w;
             } else {
                 b[i] = e < E ? __ldg(a.bias + e) : 0.0f;
             }
         }
+        // Whether every logit and bias is finite: products with 0 add up to 0 then (on the FMA pipe, which has
+        // room; the comparisons that masks need run on the other, which has none). False, too, where there are
+        // fewer experts than slots.
+        float chk = 0.0f;
 #pragma unroll
         for (int i = 0; i < kNper; ++i) chk = fmaf(c[i], 0.0f, fmaf(b[i], 0.0f, chk));
-        const bool finite = __all_sync(kFull, chk == 0.0f);  // false too where there are fewer experts than slots
+        const bool finite = __all_sync(kFull, chk == 0.0f);
         auto scores = [&](auto score) {
             if (finite) {
 #pragma unroll
@@ -410,19 +453,18 @@ __global__ void __launch_bounds__(kWarps * 32, kNper <= 16 ? 8 : 4) k_select_exp
     }
     const float eps_score = (a.sigmoid ? kEpsSigmoid : kEpsSoftmax) * smax;
 
-    // the values in order of their experts, for the groups and the candidates
-#pragma unroll
-    for (int i = 0; i < kNper; ++i) {
-        const int e = expert_of<VEC>(i, lane);
-        if (VEC && i % 4 == 0)
-            *reinterpret_cast<float4*>(c_s + e) = make_float4(c[i], c[(i + 1) % kNper], c[(i + 2) % kNper], c[(i + 3) % kNper]);
-        if (!VEC) c_s[e] = c[i];
-    }
-    __syncwarp();
-
     if (groups) {
-        const int size = a.group_size, lg = a.group_lanes_log2, per = 1 << lg;
-        const int g = lane >> lg, j = lane & (per - 1);
+        // the values in order of their experts, so that a few lanes can take a group
+#pragma unroll
+        for (int i = 0; i < kNper; ++i) {
+            const int e = expert_of<kL, VEC>(i, sl);
+            if (VEC && i % 4 == 0)
+                *reinterpret_cast<float4*>(c_s + e) = make_float4(c[i], c[(i + 1) % kNper], c[(i + 2) % kNper], c[(i + 3) % kNper]);
+            if (!VEC) c_s[e] = c[i];
+        }
+        __syncwarp();
+        const int size = a.group_size, lg = a.group_lanes_log2 - (kL == 16 ? 1 : 0), per = 1 << lg;
+        const int g = sl >> lg, j = sl & (per - 1);
         float v1 = -INFINITY, v2 = -INFINITY;
         auto take = [&](float v) {
             v2 = fmaxf(v2, fminf(v1, v));
@@ -460,24 +502,39 @@ __global__ void __launch_bounds__(kWarps * 32, kNper <= 16 ? 8 : 4) k_select_exp
         }
         int rank = 0;
         for (int o = 0; o < a.n_group; ++o) {
-            const float ov = __shfl_sync(kFull, gv, o << lg);
+            const float ov = __shfl_sync(kFull, gv, o << lg, kL);
             rank += ov > gv || (ov == gv && o < g);
         }
-        const bool real = g < a.n_group, stays = real && rank < a.topk_group;
-        unsigned keep = __ballot_sync(kFull, stays && j == 0);
+        const bool real = g < a.n_group;
+        // a group's bit is that of its first lane
+        unsigned keep = __ballot_sync(kFull, real && j == 0 && rank < a.topk_group) >> (sub * kL);
         if (a.bias || a.group_top2) {
             // the last group that stays and the first that goes, by their ranks
-            const unsigned last = __ballot_sync(kFull, real && rank == a.topk_group - 1), first = __ballot_sync(kFull, real && rank == a.topk_group);
-            const float lo = __shfl_sync(kFull, gv, __ffs(last) - 1), hi = __shfl_sync(kFull, gv, __ffs(first) - 1);
-            if (hi > -INFINITY && lo - hi <= 4.0f * eps_score + 2.0f * kEpsAdd * (fabsf(lo) + fabsf(hi)))
-                keep = exact_groups<F32>(a, t, c_s, a.group_top2 ? v2 : v1,
-                                         a.bias ? 2.0f * (eps_score + kEpsAdd * fabsf(v1)) : 0.0f);
+            const unsigned last = __ballot_sync(kFull, real && rank == a.topk_group - 1) >> (sub * kL);
+            const unsigned first = __ballot_sync(kFull, real && rank == a.topk_group) >> (sub * kL);
+            const float lo = __shfl_sync(kFull, gv, __ffs(last) - 1, kL), hi = __shfl_sync(kFull, gv, __ffs(first) - 1, kL);
+            const bool near = valid && !whole && hi > -INFINITY &&
+                              lo - hi <= 4.0f * eps_score + 2.0f * kEpsAdd * (fabsf(lo) + fabsf(hi));
+            auto decide = [&](int h, float eps) {
+                const unsigned stay = exact_groups<F32>(a, t0 + h, c_all + h * kE, eps);
+                if (sub == h) {
+                    keep = 0;
+                    for (int o = 0; o < a.n_group; ++o) keep |= ((stay >> o) & 1u) << (o << lg);
+                }
+            };
+            if constexpr (kL == 32) {
+                if (near) decide(0, eps_score);
+            } else {
+#pragma unroll 1
+                for (unsigned n = __ballot_sync(kFull, near && sl == 0); n; n &= n - 1)
+                    decide((__ffs(n) - 1) / kL, __shfl_sync(kFull, eps_score, __ffs(n) - 1));
+            }
         }
         bool in = false;
 #pragma unroll
         for (int i = 0; i < kNper; ++i) {
             if (!VEC || i % 4 == 0) {
-                const unsigned ge = (static_cast<unsigned>(expert_of<VEC>(i, lane)) * a.group_of_mul) >> 21;
+                const unsigned ge = (static_cast<unsigned>(expert_of<kL, VEC>(i, sl)) * a.group_of_mul) >> 21;
                 in = (keep >> ((ge << lg) & 31u)) & 1u;
             }
             if (!in) c[i] = -INFINITY;
@@ -491,16 +548,16 @@ __global__ void __launch_bounds__(kWarps * 32, kNper <= 16 ? 8 : 4) k_select_exp
     tau = fmaxf(tau, -INFINITY);  // a lane of NaN
     // descending runs everywhere: where a stage wants an ascending one, the values change their sign for it
 #pragma unroll
-    for (int s = 2; s <= 32; s <<= 1) {
-        const float flip = ((lane & s) != 0) != ((lane & (s >> 1)) != 0 && s > 2) ? -1.0f : 1.0f;
+    for (int s = 2; s <= kL; s <<= 1) {
+        const float flip = ((sl & s) != 0) != ((sl & (s >> 1)) != 0 && s > 2) ? -1.0f : 1.0f;
         tau *= flip;
 #pragma unroll
         for (int o = s >> 1; o > 0; o >>= 1) {
             const float v = __shfl_xor_sync(kFull, tau, o);
-            tau = (lane & o) == 0 ? fmaxf(tau, v) : fminf(tau, v);
+            tau = (sl & o) == 0 ? fmaxf(tau, v) : fminf(tau, v);
         }
     }
-    tau = __shfl_sync(kFull, tau, k < 32 ? k : 31);
+    tau = __shfl_sync(kFull, tau, k < kL ? k : kL - 1, kL);
     // what can be among the k largest in exact arithmetic has a value of at least tau less two errors
     if (a.bias) tau -= 2.0f * (eps_score + kEpsAdd * fabsf(tau));
     tau = fmaxf(tau, -FLT_MAX);  // a masked value is none
@@ -511,23 +568,34 @@ __global__ void __launch_bounds__(kWarps * 32, kNper <= 16 ? 8 : 4) k_select_exp
     for (int i = 0; i < kNper; ++i) mine |= c[i] >= tau ? 1u << i : 0u;
     int pos = __popc(mine);
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(kFull, pos, o);
-        if (lane >= o) pos += v;
+    for (int o = 1; o < kL; o <<= 1) {
+        const int v = __shfl_up_sync(kFull, pos, o, kL);
+        if (sl >= o) pos += v;
     }
-    const int C = __shfl_sync(kFull, pos, 31);
-    if (C < k || C > kMaxCand) {
-        __syncwarp();
-        whole_row<F32>(a, t, scratch_s[warp]);
-        return;
+    int C = __shfl_sync(kFull, pos, kL - 1, kL);
+    pos -= __popc(mine);
+    whole = whole || C < k || C > kCap;
+    if (whole) {
+        if (kL == 32) {
+            __syncwarp();
+            whole_row<F32>(a, t0, reinterpret_cast<double*>(scratch_s[warp]));
+            return;
+        }
+        C = 0;
+        mine = 0;
     }
-    for (pos -= __popc(mine); mine; mine &= mine - 1) {  // few lanes have more than one
-        const int i = __ffs(mine) - 1;
-        const int e = VEC ? ((i & ~3) * 32) + lane * 4 + (i & 3) : i * 32 + lane;
-        cand[pos++] = make_cand(c_s[e], e);
+    // Straight-line stores: as a loop over a lane's bits, nvcc 13.0 ran the body once for lanes without any.
+    Cand* list = cand + pos;
+#pragma unroll
+    for (int i = 0; i < kNper; ++i)
+        if ((mine >> i) & 1u) *list++ = static_cast<Cand>(__float_as_uint(c[i])) << 32 | static_cast<uint32_t>(expert_of<kL, VEC>(i, sl));
+    __syncwarp();
+    for (int q = sl; q < C; q += kL) {
+        const Cand v = cand[q];
+        cand[q] = make_cand(__uint_as_float(static_cast<uint32_t>(v >> 32)), static_cast<int>(static_cast<uint32_t>(v)));
     }
     __syncwarp();
-    if (C <= 16) {  // two lanes a candidate
+    if (kL == 32 && C <= 16) {  // two lanes a candidate
         const Cand me = cand[lane >> 1];
         int r = 0;
 #pragma unroll 4
@@ -535,7 +603,7 @@ __global__ void __launch_bounds__(kWarps * 32, kNper <= 16 ? 8 : 4) k_select_exp
         r += __shfl_xor_sync(kFull, r, 1);
         if (lane < 2 * C && r <= k) sel[r] = me;
     } else {
-        for (int q = lane; q < C; q += 32) {
+        for (int q = sl; q < C; q += kL) {
             const Cand me = cand[q];
             int r = 0;
 #pragma unroll 4
@@ -544,14 +612,23 @@ __global__ void __launch_bounds__(kWarps * 32, kNper <= 16 ? 8 : 4) k_select_exp
         }
     }
     __syncwarp();
-    Cand me = sel[lane < k ? lane : 0];
+    const Cand none = make_cand(0.0f, 0);
+    Cand me = whole ? none : sel[sl < k ? sl : 0];
     if (a.bias) {
-        const float v = cand_value(me), next = lane < k && lane + 1 < C ? cand_value(sel[lane + 1]) : -INFINITY;
-        const bool near = next > -INFINITY && v - next <= 2.0f * eps_score + kEpsAdd * (fabsf(v) + fabsf(next));
-        if (__any_sync(kFull, near)) {
-            __syncwarp();
-            exact_ranking<F32>(a, t, cand, C, reinterpret_cast<unsigned long long*>(scratch_s[warp]), sel);
-            me = sel[lane < k ? lane : 0];
+        const float v = cand_value(me), next = sl < k && sl + 1 < C ? cand_value(sel[sl + 1]) : -INFINITY;
+        const bool near = valid && next > -INFINITY && v - next <= 2.0f * eps_score + kEpsAdd * (fabsf(v) + fabsf(next));
+        const unsigned who = __ballot_sync(kFull, near);
+        if (who) {
+#pragma unroll 1
+            for (int h = 0; h < kTok; ++h) {
+                const unsigned all = kL == 32 ? kFull : 0xFFFFu << (h * 16);
+                if (who & all) {
+                    __syncwarp();
+                    exact_ranking<F32>(a, t0 + h, cand_s[warp][h], __shfl_sync(kFull, C, h * kL),
+                                       reinterpret_cast<unsigned long long*>(scratch_s[warp]), sel_s[warp][h]);
+                }
+            }
+            if (!whole) me = sel[sl < k ? sl : 0];
         }
     }
     const int id = cand_id(me);
@@ -560,32 +637,41 @@ __global__ void __launch_bounds__(kWarps * 32, kNper <= 16 ? 8 : 4) k_select_exp
     if (a.renormalize) {
         // the scores divided by exp(largest chosen logit), or for sigmoid by no less than that: a factor
         // that the sum divides out, so that small scores keep their ratios
-        const float top = a.bias ? warp_max(lane < k ? l : -INFINITY) : __shfl_sync(kFull, l, 0);
-        if ((a.sigmoid ? top : have_m ? top - m : 0.0f) < -80.0f) {  // scores that underflow here: in FP64
-            whole_row<F32>(a, t, scratch_s[warp]);
+        const float top = a.bias ? lanes_max<kL>(sl < k ? l : -INFINITY) : __shfl_sync(kFull, l, 0, kL);
+        whole = whole || (a.sigmoid ? top : have_m ? top - m : 0.0f) < -80.0f;  // scores that underflow here: in FP64
+        if (kL == 32 && whole) {
+            whole_row<F32>(a, t0, reinterpret_cast<double*>(scratch_s[warp]));
             return;
         }
         const float f = a.sigmoid ? fminf(top, 0.0f) : top;
         s = l == f ? 1.0f : expf(l - f);
         if (a.sigmoid) s = l < 0.0f ? s / (1.0f + expf(l)) : 1.0f / (1.0f + expf(-l));  // f is 0 there
-        s /= warp_sum(lane < k ? s : 0.0f);
+        s /= lanes_sum<kL>(sl < k ? s : 0.0f);
     } else {
         s = a.sigmoid ? 1.0f / (1.0f + expf(-l)) : expf(l - m) * inv_sum;
     }
-    if (lane < k) {
-        a.ids[t * k + lane] = id;
-        a.w[t * k + lane] = s * a.scale;
+    if (kL == 32 ? sl < k : valid && !whole && sl < k) {
+        a.ids[t * k + sl] = id;
+        a.w[t * k + sl] = s * a.scale;
+    }
+    if constexpr (kL < 32) {
+#pragma unroll 1
+        for (unsigned n = __ballot_sync(kFull, whole && valid && sl == 0); n; n &= n - 1) {
+            __syncwarp();
+            whole_row<F32>(a, t0 + (__ffs(n) - 1) / kL, reinterpret_cast<double*>(scratch_s[warp]));
+        }
     }
 }
 
-template <int kNper, bool F32>
+template <int kL, int kNper, bool F32>
 cudaError_t launch(const SelectArgs& a, bool vec, cudaStream_t stream)
 {
-    const dim3 grid((a.T + kWarps - 1) / kWarps), block(kWarps * 32);
+    constexpr int per_cta = kWarps * (32 / kL);
+    const dim3 grid((a.T + per_cta - 1) / per_cta), block(kWarps * 32);
     if constexpr (kNper >= 4) {
-        if (vec) return launch_pdl(k_select_experts<kNper, F32, true>, grid, block, 0, stream, a);
+        if (vec) return launch_pdl(k_select_experts<kL, kNper, F32, true>, grid, block, 0, stream, a);
     }
-    return launch_pdl(k_select_experts<kNper, F32, false>, grid, block, 0, stream, a);
+    return launch_pdl(k_select_experts<kL, kNper, F32, false>, grid, block, 0, stream, a);
 }
 
 template <bool F32>
@@ -596,12 +682,21 @@ cudaError_t launch_type(const SelectArgs& a, cudaStream_t stream)
     constexpr int bytes = F32 ? 4 : 2;
     const bool vec = a.E % (4 * a.n_group) == 0 && reinterpret_cast<uintptr_t>(a.logits) % (4 * bytes) == 0 &&
                      (a.ld % 4 == 0 || a.T == 1) && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
-    if (a.E <= 32) return launch<1, F32>(a, vec, stream);
-    if (a.E <= 64) return launch<2, F32>(a, vec, stream);
-    if (a.E <= 128) return launch<4, F32>(a, vec && a.E > 64, stream);
-    if (a.E <= 256) return launch<8, F32>(a, vec, stream);
-    if (a.E <= 512) return launch<16, F32>(a, vec, stream);
-    return launch<32, F32>(a, vec, stream);
+    // Two tokens a warp where there are several for every multiprocessor (12,365 x 160, 3 of 8 groups: 9.3 us
+    // against 11.1; of 512 experts a lane would hold 32 values, whose registers cost more than the shared steps
+    // save: 16,384 x 512 14.0 us against 12.4). k + 1 of 16 lane maxima still leave a short list of candidates.
+    if (a.E <= 256 && a.k <= 12 && a.n_group <= 16 && a.T >= 16 * device_sm_count()) {
+        if (a.E <= 32) return launch<16, 2, F32>(a, vec, stream);
+        if (a.E <= 64) return launch<16, 4, F32>(a, vec && a.E >= 64, stream);
+        if (a.E <= 128) return launch<16, 8, F32>(a, vec, stream);
+        if (a.E <= 192) return launch<16, 12, F32>(a, vec, stream);
+        return launch<16, 16, F32>(a, vec, stream);
+    }
+    if (a.E <= 32) return launch<32, 1, F32>(a, vec, stream);
+    if (a.E <= 128) return launch<32, 4, F32>(a, vec && a.E >= 128, stream);
+    if (a.E <= 256) return launch<32, 8, F32>(a, vec, stream);
+    if (a.E <= 512) return launch<32, 16, F32>(a, vec, stream);
+    return launch<32, 32, F32>(a, vec, stream);
 }
 
 }  // namespace

@@ -212,6 +212,25 @@ def test_select_sizes(moe, T, E, k, G, keep, score):
         check_select(moe, randn(g, T, E, dtype=dtype), k, bias=b, score=score, G=G, keep=keep, top2=top2, renorm=renorm, scale=scale)
 
 
+@pytest.mark.parametrize("T,E,k,G,keep", [(2433, 16, 2, 1, 1), (2600, 60, 4, 1, 1), (2432, 128, 8, 8, 4), (3001, 160, 6, 8, 3),
+                                          (2501, 192, 12, 16, 8), (2700, 256, 8, 8, 4), (2435, 31, 7, 1, 1), (2433, 250, 10, 5, 2)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_select_many_tokens(moe, T, E, k, G, keep, score):
+    # two tokens a warp; an odd number of them, rows of equal, masked and nearly equal values among the others
+    g = gen(T + E)
+    bias = randn(g, E, std=0.02)
+    level = (0.75 - torch.sigmoid(torch.linspace(-1, 1, E, device="cuda").double())).float()
+    for dtype, b, top2, renorm in ((torch.float32, bias, True, True), (torch.float32, None, False, False), (BF, None, True, True),
+                                   (BF, bias, False, True), (torch.float32, level, True, True)):
+        l = randn(g, T, E, dtype=dtype)
+        l[5], l[8] = 0.25, float("-inf")
+        l[11, ::2], l[14, 1::2] = float("-inf"), float("nan")
+        l[17, : E // 2], l[20, 3] = float("-inf"), float("inf")
+        l[100:140] = torch.linspace(-1, 1, E, device="cuda")
+        l[T - 1] = 1.0
+        check_select(moe, l, k, bias=b, score=score, G=G, keep=keep, top2=top2, renorm=renorm)
+
+
 def test_select_strided_and_unaligned_rows(moe):
     g = gen(3)
     for E, pad in ((512, 1), (512, 16), (160, 3), (256, 8)):
