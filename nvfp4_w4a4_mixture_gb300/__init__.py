@@ -5,12 +5,15 @@ provides device memory and the current stream. There is no CPU fallback: every c
 the shared library is missing or returns an error.
 """
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libmoe_nvfp4.so")
+CALLS_PATH = os.path.join(_HERE, "_lib", "_calls.so")
 
 EPI_F32, EPI_BF16, EPI_SWIGLU_NVFP4 = 0, 1, 2
 SCHED_AUTO, SCHED_ACT_ON_M, SCHED_WEIGHTS_ON_M, SCHED_WIDE, SCHED_WIDE_ROWS = 0, 0x100, 0x200, 0x400, 0x800
@@ -70,6 +73,18 @@ class AdaptersDesc(ctypes.Structure):
 
 
 _lib = None
+_calls = None  # the C marshalling of the block calls (csrc/calls.c), where it was built
+
+
+def _load_calls(L):
+    global _calls
+    if os.path.exists(CALLS_PATH):
+        loader = importlib.machinery.ExtensionFileLoader("_calls", CALLS_PATH)
+        mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_calls", loader))
+        loader.exec_module(mod)
+        mod.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (L.moe_norm_residual, L.moe_select_experts, L.moe_adapter_add)),
+                 torch.bfloat16, torch.float32, torch.int32)
+        _calls = mod
 
 
 def lib():
@@ -124,6 +139,7 @@ def lib():
         L.moe_select_experts.argtypes = [ctypes.POINTER(RoutingDesc), vp, i32, i64, i32, vp, vp, vp]
         L.moe_adapter_add.restype = i32
         L.moe_adapter_add.argtypes = [ctypes.POINTER(AdaptersDesc), vp, i64, i32, vp, vp, i32, vp, i64, vp, i64, vp, sz, vp]
+        _load_calls(L)
         _lib = L
     return _lib
 
@@ -160,6 +176,7 @@ class Workspace:
         off = (-self.buf.data_ptr()) % 256
         self.tensor = self.buf[off: off + self.nbytes]
         self.tensor[:256].zero_()
+        self.address = self.tensor.data_ptr()
 
     @property
     def ptr(self):
@@ -445,16 +462,29 @@ def moe_norm_residual(y, residual, w_post=None, w_pre=None, gate=None, residual_
     like = y if y is not None else residual
     if like is None:
         raise ValueError("y and residual are both None")
-    shape = like.shape
+    r_out, x_out = out if out is not None else (None, None)
+    if r_out is None:
+        r_out = torch.empty(like.shape, dtype=_BF16 if residual is None else residual.dtype, device=like.device)
+    if x_out is None and w_pre is not None:
+        x_out = torch.empty(like.shape, dtype=_BF16, device=like.device)
+    if _lib is None:
+        lib()
+    status = -1
+    if _calls is not None and like.is_cuda:
+        status = _calls.norm_residual(y, residual, w_post, w_pre, gate, residual_scale, eps, w_offset, r_out, x_out, _stream())
+    if status < 0:
+        status = _norm_residual(y, residual, w_post, w_pre, gate, residual_scale, eps, w_offset, r_out, x_out)
+    if status:
+        _check(status)
+    return r_out, x_out
+
+
+def _norm_residual(y, residual, w_post, w_pre, gate, residual_scale, eps, w_offset, r_out, x_out):
+    shape = (y if y is not None else residual).shape
     T, H = shape
     rt = residual.dtype if residual is not None else _BF16
     if rt is not _BF16 and rt is not _F32:
         raise TypeError("residual must be bf16 or fp32, got %s" % rt)
-    r_out, x_out = out if out is not None else (None, None)
-    if r_out is None:
-        r_out = torch.empty(T, H, dtype=rt, device=like.device)
-    if x_out is None and w_pre is not None:
-        x_out = torch.empty(T, H, dtype=_BF16, device=like.device)
     g_ptr, g_type, g_channel, g_ld = None, 0, 0, 0
     if gate is not None:
         g_shape = gate.shape
@@ -472,25 +502,31 @@ def moe_norm_residual(y, residual, w_post=None, w_pre=None, gate=None, residual_
     r_ptr, r_ld = (None, 0) if residual is None else _rows(residual, "residual", rt, shape)
     ro_ptr, ro_ld = _rows(r_out, "residual_out", rt, shape)
     x_ptr, x_ld = (None, 0) if x_out is None else _rows(x_out, "x_out", _BF16, shape)
-    status = lib().moe_norm_residual(d, y_ptr, y_ld, r_ptr, r_ld, T, ro_ptr, ro_ld, x_ptr, x_ld, _stream())
-    if status:
-        _check(status)
-    return r_out, x_out
+    return lib().moe_norm_residual(d, y_ptr, y_ld, r_ptr, r_ld, T, ro_ptr, ro_ld, x_ptr, x_ld, _stream())
 
 
 def moe_select_experts(logits, k, bias=None, score=SCORE_SOFTMAX, n_group=1, topk_group=1, group_score=GROUP_MAX,
                        renormalize=True, scale=1.0, out=None):
     """The k experts of each token and their weights from logits [T, E] (bf16 or fp32, rows may be strided):
     (ids int32 [T, k], weights fp32 [T, k]). bias: fp32 [E], for the choice alone. out: optional (ids, weights)."""
-    T, E = logits.shape
-    lt = logits.dtype
-    l_ptr, l_ld = _rows(logits, "logits", _F32 if lt is _F32 else _BF16, (T, E))
-    ids, w = out if out is not None else (torch.empty(T, k, dtype=_I32, device=logits.device),
-                                          torch.empty(T, k, dtype=_F32, device=logits.device))
-    i_ptr, w_ptr = _whole(ids, "ids", _I32, (T, k)), _whole(w, "weights", _F32, (T, k))
-    d = RoutingDesc(E, k, score, n_group, topk_group, group_score, 1 if renormalize else 0, scale,
-                    None if bias is None else _whole(bias, "bias", _F32, (E,)))
-    status = lib().moe_select_experts(d, l_ptr, DTYPE_F32 if lt is _F32 else DTYPE_BF16, l_ld, T, i_ptr, w_ptr, _stream())
+    if out is None:
+        T = logits.shape[0]
+        out = torch.empty(T, k, dtype=_I32, device=logits.device), torch.empty(T, k, dtype=_F32, device=logits.device)
+    ids, w = out
+    if _lib is None:
+        lib()
+    status = -1
+    if _calls is not None and logits.is_cuda:
+        status = _calls.select_experts(logits, k, bias, score, n_group, topk_group, group_score, renormalize, scale, ids, w,
+                                       _stream())
+    if status < 0:
+        T, E = logits.shape
+        lt = logits.dtype
+        l_ptr, l_ld = _rows(logits, "logits", _F32 if lt is _F32 else _BF16, (T, E))
+        i_ptr, w_ptr = _whole(ids, "ids", _I32, (T, k)), _whole(w, "weights", _F32, (T, k))
+        d = RoutingDesc(E, k, score, n_group, topk_group, group_score, 1 if renormalize else 0, scale,
+                        None if bias is None else _whole(bias, "bias", _F32, (E,)))
+        status = lib().moe_select_experts(d, l_ptr, DTYPE_F32 if lt is _F32 else DTYPE_BF16, l_ld, T, i_ptr, w_ptr, _stream())
     if status:
         _check(status)
     return ids, w
@@ -499,22 +535,30 @@ def moe_select_experts(logits, k, bias=None, score=SCORE_SOFTMAX, n_group=1, top
 def moe_adapter_add(x, y, a, b, scale, seg_offsets, seg_adapter, out=None, ws=None):
     """y + scale[i] * (x A_i^T) B_i^T per request, i its adapter (-1: y alone). x bf16 [T, K]; y bf16 [T, N];
     a bf16 [n, r, K]; b bf16 [n, N, r]; scale fp32 [n]; request s has the rows seg_offsets[s] ..
-    seg_offsets[s + 1] (int32 [S + 1]) and the adapter seg_adapter[s] (int32 [S]). out: optional, may be y."""
-    T, K = x.shape
-    n, r, _ = a.shape
-    N = y.shape[1]
-    S = seg_adapter.shape[0]
+    seg_offsets[s + 1] (int32 [S + 1]) and the adapter seg_adapter[s] (int32 [S]). out: optional, may be y.
+    x, y and out may have strided rows."""
     if out is None:
-        out = torch.empty(T, N, dtype=_BF16, device=y.device)
-    x_ptr, x_ld = _rows(x, "x", _BF16, (T, K))
-    y_ptr, y_ld = _rows(y, "y", _BF16, (T, N))
-    o_ptr, o_ld = _rows(out, "out", _BF16, (T, N))
-    d = AdaptersDesc(n, r, K, N, _whole(a, "a", _BF16, (n, r, K)), _whole(b, "b", _BF16, (n, N, r)), _whole(scale, "scale", _F32, (n,)))
-    if ws is None:
-        ws = _ws(4096)
-    status = lib().moe_adapter_add(d, x_ptr, x_ld, T, _whole(seg_offsets, "seg_offsets", _I32, (S + 1,)),
-                                   _whole(seg_adapter, "seg_adapter", _I32, (S,)), S, y_ptr, y_ld, o_ptr, o_ld,
-                                   ws.tensor.data_ptr(), ws.nbytes, _stream())
+        out = torch.empty(y.shape, dtype=_BF16, device=y.device)
+    if _lib is None:
+        lib()
+    status = -1
+    if x.is_cuda:
+        if ws is None:
+            ws = _ws(4096)
+        if _calls is not None:
+            status = _calls.adapter_add(x, y, a, b, scale, seg_offsets, seg_adapter, out, ws.address, ws.nbytes, _stream())
+    if status < 0:
+        T, K = x.shape
+        n, r, _ = a.shape
+        N, S = y.shape[1], seg_adapter.shape[0]
+        x_ptr, x_ld = _rows(x, "x", _BF16, (T, K))
+        y_ptr, y_ld = _rows(y, "y", _BF16, (T, N))
+        o_ptr, o_ld = _rows(out, "out", _BF16, (T, N))
+        d = AdaptersDesc(n, r, K, N, _whole(a, "a", _BF16, (n, r, K)), _whole(b, "b", _BF16, (n, N, r)),
+                         _whole(scale, "scale", _F32, (n,)))
+        status = lib().moe_adapter_add(d, x_ptr, x_ld, T, _whole(seg_offsets, "seg_offsets", _I32, (S + 1,)),
+                                       _whole(seg_adapter, "seg_adapter", _I32, (S,)), S, y_ptr, y_ld, o_ptr, o_ld,
+                                       ws.address, ws.nbytes, _stream())
     if status:
         _check(status)
     return out

@@ -9,12 +9,14 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 SRC_DIR = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_lib")
 OBJ_DIR = os.path.join(OUT_DIR, "obj")
 LIB = os.path.join(OUT_DIR, "libmoe_nvfp4.so")
+CALLS_SRC, CALLS = os.path.join(SRC_DIR, "calls.c"), os.path.join(OUT_DIR, "_calls.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -35,7 +37,26 @@ def _deps_mtime():
     return max(os.path.getmtime(f) for f in files)
 
 
+def build_calls(force: bool = False) -> None:
+    """The C marshalling of the block calls (calls.c), where Python's headers are installed; without it the
+    same calls go through ctypes."""
+    include = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        return
+    newest = max(os.path.getmtime(f) for f in [CALLS_SRC] + glob.glob(os.path.join(INCLUDE, "*.h")))
+    if not force and os.path.exists(CALLS) and os.path.getmtime(CALLS) >= newest:
+        return
+    os.makedirs(OUT_DIR, exist_ok=True)
+    tmp = CALLS + ".tmp.%d" % os.getpid()
+    cmd = ["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I" + include, "-I" + INCLUDE, CALLS_SRC, "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("gcc failed for %s:\n%s\n%s" % (CALLS_SRC, r.stdout, r.stderr))
+    os.replace(tmp, CALLS)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_calls(force)
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
         return LIB
     os.makedirs(OBJ_DIR, exist_ok=True)

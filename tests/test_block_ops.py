@@ -482,6 +482,36 @@ def test_repeatable_on_a_stream_and_in_a_graph(moe, T):
             assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
 
 
+@pytest.mark.parametrize("T", [1, 4, 300])
+def test_both_marshallings_give_the_same(moe, monkeypatch, T):
+    for f, *shapes in calls(moe, T):
+        new = lambda: tuple(torch.zeros(s, dtype=d, device="cuda") for s, d in shapes)  # noqa: E731
+        first, again = new(), new()
+        f(first)
+        monkeypatch.setattr(moe, "_calls", None)
+        f(again)
+        monkeypatch.undo()
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def test_binding_refuses_on_the_device(moe):
+    y = torch.zeros(4, 64, dtype=BF, device="cuda")
+    w = torch.ones(64, dtype=BF, device="cuda")
+    with pytest.raises(TypeError, match="w_pre"):
+        moe.moe_norm_residual(y, y, w_pre=w.float())
+    with pytest.raises(ValueError, match="gate"):
+        moe.moe_norm_residual(y, y, gate=torch.ones(3, 64, dtype=BF, device="cuda"))
+    with pytest.raises(ValueError, match="y must"):
+        moe.moe_norm_residual(y.t().contiguous().t(), y)
+    with pytest.raises(moe.MoeError, match="overlaps"):
+        moe.moe_norm_residual(y, y.clone(), w_pre=w, out=(y, torch.empty_like(y)))
+    with pytest.raises(moe.MoeError, match="k=5"):
+        moe.moe_select_experts(torch.zeros(4, 4, device="cuda"), 5)
+    with pytest.raises(TypeError, match="seg_offsets"):
+        moe.moe_adapter_add(y, y, torch.zeros(1, 8, 64, dtype=BF, device="cuda"), torch.zeros(1, 64, 8, dtype=BF, device="cuda"),
+                            torch.ones(1, device="cuda"), torch.tensor([0, 4], device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda"))
+
+
 def test_outputs_stay_inside_their_rows(moe):
     # what lies between and behind the outputs' rows is left alone
     T, H = 37, 264

@@ -179,3 +179,95 @@ def test_binding_refuses_other_types_and_shapes(m):
     with pytest.raises(TypeError, match="CUDA"):
         m.moe_adapter_add(y, y, torch.zeros(1, 8, 64, dtype=bf), torch.zeros(1, 64, 8, dtype=bf), torch.ones(1),
                           torch.tensor([0, 4], dtype=torch.int32), torch.zeros(1, dtype=torch.int32), ws=m)
+
+
+class FakeTensor:
+    def __init__(self, dtype, shape, ptr, cuda=True, contiguous=True):
+        self.dtype, self.shape, self.ptr, self.is_cuda, self.contiguous = dtype, tuple(shape), ptr, cuda, contiguous
+
+    def is_contiguous(self):
+        return self.contiguous
+
+    def data_ptr(self):
+        return self.ptr
+
+
+@pytest.fixture
+def calls(m):
+    """The C marshalling bound to functions that record what they are given, and the record."""
+    import torch
+
+    if m._calls is None:
+        pytest.skip("built without Python's headers")
+    c, got = ctypes, []
+    vp, i32, i64, sz = c.c_void_p, c.c_int, c.c_int64, c.c_size_t
+    fields = lambda d: tuple(getattr(d, n) for n, _ in d._fields_)  # noqa: E731
+    proto = (c.CFUNCTYPE(i32, c.POINTER(m.NormDesc), vp, i64, vp, i64, i32, vp, i64, vp, i64, vp),
+             c.CFUNCTYPE(i32, c.POINTER(m.RoutingDesc), vp, i32, i64, i32, vp, vp, vp),
+             c.CFUNCTYPE(i32, c.POINTER(m.AdaptersDesc), vp, i64, i32, vp, vp, i32, vp, i64, vp, i64, vp, sz, vp))
+
+    def record(d, *rest):
+        got.append((fields(d.contents), rest))
+        return 2
+
+    fs = [p(record) for p in proto]
+    m._calls.bind(*(c.cast(f, vp).value for f in fs), torch.bfloat16, torch.float32, torch.int32)
+    yield m._calls, got
+    m._load_calls(m.lib())
+
+
+def test_c_marshalling_passes_what_it_is_given(calls):
+    import torch
+
+    calls, got = calls
+    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    y, r, x = FakeTensor(bf, (4, 64), 10), FakeTensor(f32, (4, 64), 11), FakeTensor(bf, (4, 64), 12)
+    w = FakeTensor(bf, (64,), 13)
+    gates = {None: (None, 0, 0, 0), FakeTensor(bf, (64,), 14): (14, 0, 1, 0), FakeTensor(f32, (4, 1), 15): (15, 1, 0, 1),
+             FakeTensor(bf, (4, 64), 16): (16, 0, 1, 64)}
+    for g, (p_, t_, c_, ld_) in gates.items():
+        assert calls.norm_residual(y, r, w, w, g, 0.5, 0.25, 1.0, r, x, 99) == 2
+        d, rest = got.pop()
+        assert d == (64, 13, 13, 0.25, 1.0, 0.5, 1, p_, t_, c_, ld_)
+        assert rest == (10, 64, 11, 64, 4, 11, 64, 12, 64, 99)
+    assert calls.norm_residual(None, y, None, w, None, 1.0, 0.5, 0.0, y, x, 0) == 2
+    assert got.pop() == ((64, None, 13, 0.5, 0.0, 1.0, 0, None, 0, 0, 0), (None, 64, 10, 64, 4, 10, 64, 12, 64, None))
+    l, ids, wt, b = FakeTensor(bf, (5, 16), 20), FakeTensor(i32, (5, 3), 21), FakeTensor(f32, (5, 3), 22), FakeTensor(f32, (16,), 23)
+    assert calls.select_experts(l, 3, b, 1, 4, 2, 1, True, 2.5, ids, wt, 7) == 2
+    assert got.pop() == ((16, 3, 1, 4, 2, 1, 1, 2.5, 23), (20, 0, 16, 5, 21, 22, 7))
+    a_, b_, s = FakeTensor(bf, (2, 8, 64), 30), FakeTensor(bf, (2, 32, 8), 31), FakeTensor(f32, (2,), 32)
+    off, ad, o = FakeTensor(i32, (4,), 33), FakeTensor(i32, (3,), 34), FakeTensor(bf, (4, 32), 35)
+    assert calls.adapter_add(y, o, a_, b_, s, off, ad, o, 36, 4096, 8) == 2
+    assert got.pop() == ((2, 8, 64, 32, 30, 31, 32), (10, 64, 4, 33, 34, 3, 35, 32, 35, 32, 36, 4096, 8))
+    assert not got
+
+
+def test_c_marshalling_leaves_the_rest_alone(calls):
+    import torch
+
+    calls, got = calls
+    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    T = FakeTensor
+
+    def norm(y=T(bf, (4, 64), 1), r=T(bf, (4, 64), 2), w=T(bf, (64,), 3), g=None, ro=T(bf, (4, 64), 4), x=T(bf, (4, 64), 5)):
+        return calls.norm_residual(y, r, w, w, g, 1.0, 1e-6, 0.0, ro, x, 0)
+
+    assert norm() == 2
+    got.clear()
+    for kw in (dict(y=T(f32, (4, 64), 1)), dict(y=T(bf, (4, 64), 1, cuda=False)), dict(y=T(bf, (4, 64), 1, contiguous=False)),
+               dict(y=T(bf, (4, 72), 1)), dict(y=T(bf, (256,), 1)), dict(r=T(torch.float16, (4, 64), 2)), dict(r=T(f32, (4, 64), 2)),
+               dict(w=T(bf, (72,), 3)), dict(w=T(f32, (64,), 3)), dict(g=T(bf, (3, 64), 6)), dict(g=T(torch.float16, (64,), 6)),
+               dict(g=T(bf, (1, 64), 6)), dict(ro=None), dict(ro=T(bf, (4, 64), 4, cuda=False)), dict(x=T(bf, (5, 64), 5)), dict(y=3),
+               dict(y=T(bf, (1 << 40, 64), 1))):
+        assert norm(**kw) == -1, kw
+    l, ids, wt = T(f32, (5, 16), 20), T(i32, (5, 3), 21), T(f32, (5, 3), 22)
+    for args in ((l, 4, None), (l, 0, None), (l, "3", None), (l, 3, T(bf, (16,), 1)), (T(i32, (5, 16), 20), 3, None)):
+        assert calls.select_experts(*args, 1, 1, 1, 0, True, 1.0, ids, wt, 0) == -1, args
+    y, a_, b_, s = T(bf, (4, 64), 10), T(bf, (2, 8, 64), 30), T(bf, (2, 64, 8), 31), T(f32, (2,), 32)
+    off, ad = T(i32, (4,), 33), T(i32, (3,), 34)
+    for args in ((y, y, a_, T(bf, (2, 64, 16), 31), s, off, ad, y), (y, y, a_, b_, s, T(i32, (3,), 33), ad, y),
+                 (y, y, T(bf, (2, 8, 72), 30), b_, s, off, ad, y), (y, y, a_, b_, s, off, T(torch.int64, (3,), 34), y),
+                 (y, y, a_, b_, s, off, ad, T(bf, (4, 72), 1)), (y, y, a_, b_, T(f32, (3,), 32), off, ad, y)):
+        assert calls.adapter_add(*args, 36, 4096, 0) == -1
+    assert calls.adapter_add(y) == -1 and calls.norm_residual() == -1
+    assert not got
