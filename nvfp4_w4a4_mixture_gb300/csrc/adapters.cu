@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto fail = [&]() {
         if (atomicExch(&st.abort, 1) == 0) record_status(p.status, kDevTimeoutAdapter);
     };
-    Walk walk;
+    Walk<kTileM> walk;
     Tile t;
 
     // The issuing warps run their loops whole and one lane issues: loop counters, addresses and
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int s = 0;
         uint32_t ph = 0, fills = 0;
         bool ok = true;
-        for (int number = cluster; ok && walk.find(p, kTileM, number, t); number += n_clusters) {
+        for (int number = cluster; ok && walk.find(p, number, t); number += n_clusters) {
             const Boxes boxes(t.rows);
             if (t.adapter >= 0)
                 for (int kc = k0; kc < k1; ++kc) {
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int s = 0;
         uint32_t ph = 0, it = 0, cc = 0;
         bool ok = true;
-        for (int number = cluster; ok && walk.find(p, kTileM, number, t); number += n_clusters) {
+        for (int number = cluster; ok && walk.find(p, number, t); number += n_clusters) {
             if (t.adapter >= 0) {
                 for (int kc = k0; kc < k1; ++kc) {
                     ok = all(ptx::mbar_wait_near(&st.full[s], ph));
@@ -267,8 +267,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         // one lane's wait result may differ from another's only in time: the warp agrees on it
         auto all = [&](bool got) { return __all_sync(0xFFFFFFFFu, got) != 0; };
-        if (cluster == 0 && rank == 0 && ew == 0) check_segments(p);
-        for (int number = cluster; ok && walk.find(p, kTileM, number, t); number += n_clusters, ++tiles) {
+        const bool check = cluster == 0 && rank == 0 && ew == 0;
+        for (int number = cluster; ok && walk.find(p, number, t, check); number += n_clusters, ++tiles) {
             const bool live = q * 32 < t.rows;  // this warp has rows of the tile
             // a cluster: no warp is a tile ahead of another (their buffers are about to hold partial sums)
             if (cs > 1 && tiles > 0) ok = all(ptx::mbar_wait(&st.idle, (tiles - 1) & 1));
@@ -381,6 +381,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 o[j][i] = pack_bf16x2(bf16_to_f32(yy[i] & 0xFFFFu) + __uint_as_float(v[j * 8 + 2 * i]),
                                                       bf16_to_f32(yy[i] >> 16) + __uint_as_float(v[j * 8 + 2 * i + 1]));
                         }
+                        // y has to be in registers before the stage goes back. Without the fence the compiler's last uses of the
+                        // loads may follow the arrivals, and loads that queued behind stores then read the next fill.
+                        __threadfence_block();
                         __syncwarp();
                         if (lane == 0) {
                             ptx::mbar_arrive(&st.empty[s]);
@@ -411,6 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) ptx::mbar_arrive(&st.idle);
         }
         if (!ok) fail();
+        if (check) report(p, walk);
     }
     __syncwarp();
     ptx::tc_fence_before();

@@ -7,7 +7,7 @@
 namespace moe {
 
 // A request of L rows has ceil(L / rows) tiles of up to `rows` rows: at most this many in all.
-inline int64_t adapter_tiles(const AdapterArgs& a, int rows) { return static_cast<int64_t>(a.T / rows) + (a.S < a.T ? a.S : a.T); }
+__host__ __device__ inline int64_t adapter_tiles(const AdapterArgs& a, int rows) { return static_cast<int64_t>(a.T / rows) + (a.S < a.T ? a.S : a.T); }
 
 // Tiles of up to 8 rows on mma.sync (adapters_small.cu).
 cudaError_t launch_adapter_add_small(const AdapterArgs& a, int sms, cudaStream_t stream);
@@ -19,13 +19,16 @@ struct Tile {
 };
 
 // Walks the requests in order, 128 at a time (four neighbours a lane); every warp that needs the tiles
-// has its own.
+// has its own. kRows: the rows of a full tile.
+template <int kRows>
 struct Walk {
     int base = 0, before = 0;  // first request of the window, tiles before it
+    bool bad = false;          // this lane has met a request that breaks the rules (where it looks for them)
 
     // Warp-wide. The tile of the given number (numbers must not go down), false past the last.
-    __device__ bool find(const AdapterArgs& p, int tile_rows, int number, Tile& t)
+    __device__ bool find(const AdapterArgs& p, int number, Tile& t, bool check = false)
     {
+        if (number >= adapter_tiles(p, kRows)) return false;
         const int lane = threadIdx.x & 31;
         for (; base < p.S; base += 128) {
             const int s = base + lane * 4;
@@ -37,8 +40,14 @@ struct Walk {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const bool good = off[i] >= 0 && off[i] <= off[i + 1] && off[i + 1] <= p.T && ad[i] >= -1 && ad[i] < p.n;
-                n[i] = good && !(ad[i] < 0 && p.out == p.y) ? (off[i + 1] - off[i] + tile_rows - 1) / tile_rows : 0;
+                n[i] = good && !(ad[i] < 0 && p.out == p.y) ? static_cast<int>((static_cast<unsigned>(off[i + 1] - off[i]) + kRows - 1) / kRows) : 0;
                 sum += n[i];
+            }
+            if (check) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    bad |= s + i < p.S && (off[i] < 0 || off[i] > off[i + 1] || ad[i] < -1 || ad[i] >= p.n || (s + i == 0 && off[i] != 0) ||
+                                           (s + i + 1 == p.S && off[i + 1] != p.T));
             }
             const int mine = sum;
 #pragma unroll
@@ -53,11 +62,11 @@ struct Walk {
                     bool found = false;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        if (!found && left < n[i]) {
+                        if (!found && left >= 0 && left < n[i]) {
                             found = true;
                             adapter = ad[i];
-                            row = off[i] + left * tile_rows;
-                            rows = min(tile_rows, off[i + 1] - row);
+                            row = off[i] + left * kRows;
+                            rows = min(kRows, off[i + 1] - row);
                         }
                         left -= n[i];
                     }
@@ -75,16 +84,16 @@ struct Walk {
     }
 };
 
-// One warp: whether the requests follow the rules (in order, without gaps, adapters in range).
-__device__ __forceinline__ void check_segments(const AdapterArgs& p)
+// One warp that has called find with `check`: reports whether the requests follow the rules (in order,
+// without gaps, adapters in range). The first 128 are known from its first find.
+template <int kRows>
+__device__ __forceinline__ void report(const AdapterArgs& p, Walk<kRows>& w)
 {
-    const int lane = threadIdx.x & 31;
-    bool bad = __ldg(p.seg_offsets) != 0 || __ldg(p.seg_offsets + p.S) != p.T;
-    for (int i = lane; i < p.S; i += 32) {
+    for (int i = 128 + static_cast<int>(threadIdx.x & 31); i < p.S; i += 32) {
         const int beg = __ldg(p.seg_offsets + i), end = __ldg(p.seg_offsets + i + 1), ad = __ldg(p.seg_adapter + i);
-        bad |= beg < 0 || beg > end || end > p.T || ad < -1 || ad >= p.n;
+        w.bad |= beg < 0 || beg > end || ad < -1 || ad >= p.n || (i + 1 == p.S && end != p.T);
     }
-    if (bad) record_status(p.status, kDevBadSegment);
+    if (w.bad) record_status(p.status, kDevBadSegment);
 }
 
 // Two FP32 values (or zeros) as hi + lo, each two bf16: hi the nearest, lo the nearest to what is left.

@@ -8,9 +8,10 @@
 //   phase 1  h[j][t] = A_j . x_t: rank rows on M, tokens on N; the warps share rank rows and K; their
 //            partial sums meet in shared memory (and through distributed shared memory in a cluster),
 //            always added in the same order; h scale = hi + lo, two bf16 values
-//   phase 2  d[t][c] = (hi + lo)_t . B_c: tokens on M (half of it), columns on N. Column 2q + e of product i stands
-//            for column 8q + 2i + e of 32, so that a thread ends with eight neighbouring columns of a
-//            row: one 16-byte load of y and one store of out
+//   phase 2  d[t][c] = hi_t . B_c + lo_t . B_c: tokens on M, hi in rows 0..7 and lo in rows 8..15 (their
+//            sums are added at the end), columns on N. Column 2q + e of product i stands for column 8q + 2i
+//            + e of 32, so that a thread ends with eight neighbouring columns of a row: one 16-byte load of
+//            y and one store of out. Ranks up to 16 take 8 bytes a thread and one product of 16.
 #include "adapters.cuh"
 
 namespace moe {
@@ -49,20 +50,21 @@ __global__ void __launch_bounds__(kThreads, 2) k_adapter_add_small(const __grid_
     constexpr int kSteps = (kR + 31) / 32;                       // 32 ranks each
     constexpr int kHld = kSteps * 32 + 8;                        // a token's h in shared memory (padded: other banks)
     constexpr int kUnroll1 = 8, kUnroll2 = kSteps <= 2 ? 4 / kSteps : 1;
-    __shared__ float part[kSplit][kR * kM];
+    __shared__ float part[kSplit][kR * kM], sums[8][kR * kM];  // of the warps that share K, of the cluster's CTAs
     __shared__ __align__(16) uint16_t h_s[2][kM][kHld];
-    ptx::griddep_wait();
-    ptx::griddep_launch_dependents();
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, q = lane % 4;
     const int cs = static_cast<int>(ptx::cluster_size()), rank = static_cast<int>(ptx::cluster_rank());
     const int cluster = blockIdx.x / cs, n_clusters = gridDim.x / cs;
     // rows of h that no token fills, and columns past the rank, stay zero
     for (int i = tid; i < static_cast<int>(sizeof(h_s) / 4); i += kThreads) reinterpret_cast<uint32_t*>(h_s)[i] = 0u;
-    if (blockIdx.x == 0 && warp == 0) check_segments(p);
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
     const int nc = (p.N + 31) / 32, c0 = nc * rank / cs, c1 = nc * (rank + 1) / cs;  // this CTA's slices of 32 columns
-    Walk walk;
+    Walk<kM> walk;
     Tile t;
-    for (int number = cluster; walk.find(p, kM, number, t); number += n_clusters) {
+    const bool check = blockIdx.x == 0 && warp == 0;
+    bool sent = false;
+    for (int number = cluster; walk.find(p, number, t, check); number += n_clusters) {
         if (t.adapter < 0) {
             const int w = min(c1 * 32, p.N) / 8 - c0 * 4;  // 16-byte pieces of a row
             for (int i = tid; i < w * t.rows; i += kThreads) {
@@ -72,6 +74,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_adapter_add_small(const __grid_
             }
             continue;
         }
+        if (sent) ptx::cluster_wait();  // all of the cluster have read the sums of the tile before
         {
             const int rb = warp % kBlocks, kw = warp / kBlocks;
             const int steps = (p.K + 31) / 32, share = cs * kSplit, me = rank * kSplit + kw;
@@ -108,8 +111,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_adapter_add_small(const __grid_
                     const int n = (c + u) * 32 + g / 2 * 8 + 2 * i + g % 2;
 #pragma unroll
                     for (int s = 0; s < kSteps; ++s) {
-                        const int k = s * 32 + q * 8;
-                        bv[u][i][s] = load16(b0 + static_cast<int64_t>(n) * p.r + k, c + u < c1 && n < p.N && k < p.r);
+                        const int k = kR == 16 ? q * 4 : s * 32 + q * 8;
+                        const bool in = c + u < c1 && n < p.N && k < p.r;
+                        if constexpr (kR == 16) {
+                            const uint2 v = in ? __ldg(reinterpret_cast<const uint2*>(b0 + n * p.r + k)) : make_uint2(0, 0);
+                            bv[u][i][s] = make_uint4(v.x, v.y, 0, 0);
+                        } else {
+                            bv[u][i][s] = load16(b0 + n * p.r + k, in);
+                        }
                     }
                 }
                 const int col = (c + u) * 32 + q * 8;
@@ -118,14 +127,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_adapter_add_small(const __grid_
         };
         load_b(c0 + warp * kUnroll2);
         __syncthreads();
-        if (cs > 1) {
-            if (kSplit > 1) {
-                for (int i = tid; i < kR * kM; i += kThreads) {
-                    float v = part[0][i];
+        if (cs > 1) {  // this CTA's sum goes to every CTA of the cluster
+            for (int i = tid; i < kR * kM; i += kThreads) {
+                float v = part[0][i];
 #pragma unroll
-                    for (int w = 1; w < kSplit; ++w) v += part[w][i];
-                    part[0][i] = v;
-                }
+                for (int w = 1; w < kSplit; ++w) v += part[w][i];
+                for (int o = 0; o < cs; ++o) ptx::cluster_store(ptx::cluster_addr(&sums[rank][i], o), v);
             }
             ptx::cluster_sync();
         }
@@ -135,9 +142,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_adapter_add_small(const __grid_
             float u = 0.0f, v = 0.0f;
             if (cs > 1) {
                 for (int o = 0; o < cs; ++o) {
-                    const uint32_t at = ptx::cluster_addr(&part[0][j * kM + tok], o);
-                    u += ptx::cluster_load(at);
-                    v += ptx::cluster_load(at + kM * 4);
+                    u += sums[o][j * kM + tok];
+                    v += sums[o][(j + 1) * kM + tok];
                 }
             } else {
 #pragma unroll
@@ -151,10 +157,22 @@ __global__ void __launch_bounds__(kThreads, 2) k_adapter_add_small(const __grid_
             *reinterpret_cast<uint32_t*>(&h_s[0][tok][j]) = hi;
             *reinterpret_cast<uint32_t*>(&h_s[1][tok][j]) = lo;
         }
-        // the next tile's partial sums wait until all of the cluster have read these
-        if (cs > 1) ptx::cluster_sync();
-        else __syncthreads();
+        if (cs > 1) ptx::cluster_arrive_all();  // this CTA has read the cluster's sums
+        sent = cs > 1;
+        __syncthreads();
 
+        uint4 hi[kSteps], lo[kSteps];  // token g's h, in the order of the products' k
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            if constexpr (kR == 16) {
+                const uint2 a = *reinterpret_cast<const uint2*>(&h_s[0][g][q * 4]), b = *reinterpret_cast<const uint2*>(&h_s[1][g][q * 4]);
+                hi[s] = make_uint4(a.x, a.y, 0, 0);
+                lo[s] = make_uint4(b.x, b.y, 0, 0);
+            } else {
+                hi[s] = *reinterpret_cast<const uint4*>(&h_s[0][g][s * 32 + q * 8]);
+                lo[s] = *reinterpret_cast<const uint4*>(&h_s[1][g][s * 32 + q * 8]);
+            }
+        }
         for (int c = c0 + warp * kUnroll2; c < c1; c += kWarps * kUnroll2) {
             if (c != c0 + warp * kUnroll2) load_b(c);
 #pragma unroll
@@ -164,23 +182,23 @@ __global__ void __launch_bounds__(kThreads, 2) k_adapter_add_small(const __grid_
 #pragma unroll
                 for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint4 h = *reinterpret_cast<const uint4*>(&h_s[e][g][s * 32 + q * 8]), none = make_uint4(0, 0, 0, 0);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) mma32(d[i], h, none, bv[u][i][s]);
+                    for (int i = 0; i < 4; ++i) {
+                        if (kR == 16) mma(d[i], hi[s].x, lo[s].x, hi[s].y, lo[s].y, bv[u][i][s].x, bv[u][i][s].y);
+                        else mma32(d[i], hi[s], lo[s], bv[u][i][s]);
                     }
                 const uint32_t yy[4] = {yv[u].x, yv[u].y, yv[u].z, yv[u].w};
                 uint32_t o[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    o[i] = pack_bf16x2(bf16_to_f32(yy[i] & 0xFFFFu) + d[i][0], bf16_to_f32(yy[i] >> 16) + d[i][1]);
+                    o[i] = pack_bf16x2(bf16_to_f32(yy[i] & 0xFFFFu) + (d[i][0] + d[i][2]), bf16_to_f32(yy[i] >> 16) + (d[i][1] + d[i][3]));
                 if (c + u < c1 && col < p.N && g < t.rows)
                     *reinterpret_cast<uint4*>(p.out + (t.row + g) * p.ld_out + col) = make_uint4(o[0], o[1], o[2], o[3]);
             }
         }
         __syncthreads();  // h is read
     }
-    if (cs > 1) ptx::cluster_sync();
+    if (check) report(p, walk);
+    if (sent) ptx::cluster_wait();
 }
 
 template <int kR>

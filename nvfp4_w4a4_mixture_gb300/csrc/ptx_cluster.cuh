@@ -20,12 +20,24 @@ __device__ __forceinline__ uint32_t cluster_size()
     return r;
 }
 
-// All threads of all CTAs of the cluster (a hardware barrier; its CTAs run at the same time).
-__device__ __forceinline__ void cluster_sync()
+// A barrier of all threads of all CTAs of the cluster (in hardware; its CTAs run at the same time), in two
+// halves: every thread arrives, and later waits for all the others' arrivals.
+__device__ __forceinline__ void cluster_arrive_all()
 {
     __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_wait()
+{
+    __syncwarp();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    cluster_arrive_all();
+    cluster_wait();
 }
 
 // The address, in the cluster's window, of this CTA's shared address p in the CTA of the given rank.
@@ -36,11 +48,9 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank)
     return a;
 }
 
-__device__ __forceinline__ float cluster_load(uint32_t addr)
+__device__ __forceinline__ void cluster_store(uint32_t addr, float v)
 {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
-    return v;
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 __device__ __forceinline__ float4 cluster_load4(uint32_t addr)

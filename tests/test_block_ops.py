@@ -396,6 +396,24 @@ def test_adapter_tiles_with_and_without_adapter_in_turn(moe, lens):
     check_adapter(moe, adapter_case(lens, [(i % 5) - 1 if i % 3 else -1 for i in range(len(lens))], 4, 24, 1032, 2048))
 
 
+@pytest.mark.parametrize("lens,r,K,N", [([1500, 3, 1, 900, 128, 700], 128, 2048, 2048), ([700] * 20, 64, 1032, 2056),
+                                        ([129, 2] * 150, 32, 2048, 2048), ([1] * 256, 16, 2048, 2048), ([3, 1, 5], 64, 2048, 2048)])
+def test_adapter_repeats_itself(moe, lens, r, K, N):
+    # the same bits every time, also while other work keeps the memory busy
+    c = adapter_case(lens, [(i % 4) - 1 if i else 1 for i in range(len(lens))], 3, r, K, N)
+    want = check_adapter(moe, c).clone()
+    out, busy = torch.empty_like(want), randn(gen(1), 2048, 2048)
+    same = torch.ones((), dtype=torch.bool, device="cuda")
+    for i in range(300):
+        out.fill_(7.0)
+        if i % 3 == 1:
+            busy = busy @ busy * 1e-3
+        moe.moe_adapter_add(**c, out=out)
+        same &= (out == want).all()
+    moe.moe_read_device_status()
+    assert bool(same)
+
+
 def test_adapter_strides_and_in_place(moe):
     for lens in ([5, 1], [300, 70]):
         c = adapter_case(lens, [1, 0], 2, 16, 264, 136, pad=24)
