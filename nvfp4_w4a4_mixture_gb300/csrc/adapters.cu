@@ -487,14 +487,15 @@ cudaError_t launch_adapter_add(const AdapterArgs& a, int sms, cudaStream_t strea
     const int64_t tiles = adapter_tiles(a, kTileM);
     const int cs = tiles * 16 <= 2LL * (sms - sms / 8) ? 8 : tiles * 4 <= sms ? 4 : tiles * 20 <= 11LL * sms ? 2 : 1;
     // Estimated times in ns, from sweeps over 1 to 16,384 tokens of 1 to 256 requests, ranks 16 and 64, K x N
-    // 2048 x 2048 and 512 x 1024 on 152 multiprocessors. Tiles of 8 rows: 4.5 us, 8 ns a tile and 122 ns a MB
-    // of A and B that the tiles read (256 single tokens, rank 64: 20.5 us against 36.9 with tiles of 128; 1,024
-    // tokens of one request, rank 16: 7.7 against 9.7). Tiles of 128: the chain of one tile, shorter the more
-    // CTAs share it, times the rounds of CTAs (2,048 tokens of 64 requests, rank 64: 18.4 us against 21.5; 16,384 of 24:
-    // 38 against 138).
-    const int64_t tiles8 = adapter_tiles(a, 8), width = a.K + a.N, bytes = 2LL * a.r * width;
-    const int64_t t8 = 4500 + tiles8 * (8 + bytes / 8200);
-    const int64_t chain = 8000 + width * (cs >= 4 ? 9 : cs == 2 ? 19 : 36) / 10, ctas = 10 * tiles * cs, round = 11LL * sms;
+    // 2048 x 2048 and 512 x 1024 on 152 multiprocessors. Tiles of 8 rows: 4 us, 5 ns a tile and 105 ns a MB of
+    // A and B (of padded rank) that the tiles read (256 single tokens, rank 64: 17.8 us against 36.9 with tiles
+    // of 128; 4,113 tokens of 77 requests, rank 40: 30 against 23.4). Tiles of 128: the chain of one tile,
+    // shorter the more CTAs share it, times the rounds of CTAs (4,113 tokens of 16 requests, rank 64: 18.4 us
+    // against 33; 16,384 of 24: 38 against 130).
+    const int64_t tiles8 = adapter_tiles(a, 8), width = a.K + a.N, padded = a.r <= 16 ? 16 : a.r <= 32 ? 32 : a.r <= 64 ? 64 : 128;
+    const int64_t t8 = 4000 + tiles8 * (5 + 2 * padded * width / 9500);
+    const int64_t chain = (cs == 8 ? 6500 : 8000) + width * (cs >= 4 ? 9 : cs == 2 ? 19 : 36) / 10 + 30 * a.r;
+    const int64_t ctas = 10 * tiles * cs, round = 11LL * sms;
     if (t8 <= (ctas <= round ? chain : chain * ctas / round)) return launch_adapter_add_small(a, sms, stream);
     if (a.r <= 16) return launch<16>(a, cs, tiles, sms, stream);
     if (a.r <= 32) return launch<32>(a, cs, tiles, sms, stream);
