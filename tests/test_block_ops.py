@@ -109,7 +109,9 @@ def check_norm(moe, T, H, rt=BF, gate=None, gate_type=BF, post=True, pre=True, w
 
 
 @pytest.mark.parametrize("T,H", [(1, 8), (1, 2048), (4, 2048), (3, 24), (33, 136), (7, 1032), (5, 2056), (9, 4096), (70, 8192),
-                                 (2, 8184), (300, 2048), (1000, 512), (4097, 256), (2500, 2056)])
+                                 (2, 8184), (300, 2048), (1000, 512), (4097, 256), (2500, 2056),
+                                 (2000, 768), (701, 640), (1999, 1024), (1501, 1272), (1500, 1536), (901, 2824), (900, 4096),
+                                 (700, 4608), (500, 5128), (305, 6152), (613, 8192)])
 def test_norm_sizes(moe, T, H):
     check_norm(moe, T, H)
     check_norm(moe, T, H, rt=torch.float32, gate="channel", alpha=0.5, off=1.0, seed=1)
