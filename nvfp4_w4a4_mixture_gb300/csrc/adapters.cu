@@ -1,6 +1,6 @@
 // adapters.cu -- low-rank adapters of many requests: out[t] = y[t] + scale_a B_a (A_a x[t]).
 //
-// The requests' rows are cut into tiles of up to 128 rows of one request. A tile is
+// The requests' rows are cut into tiles of up to 128 (or 64) rows of one request. A tile is
 // two tensor-core products (tcgen05 kind::f16, FP32 in tensor memory) of one CTA or of a cluster:
 //   phase 1  h = x A^T over this CTA's share of K, in slices of 64 columns
 //            (cluster: the partial h of all CTAs are added through distributed shared memory, in the
@@ -14,7 +14,7 @@
 // and store rows.
 // Bounded by memory where the batch fills the multiprocessors (16,384 tokens of 24 requests, rank 64,
 // 2048 x 2048: 37.5 us, 5.5 TB/s, 82 % of what a copy reaches), else by the chain of one tile (4,113
-// tokens of 77 requests, rank 40, 2056 x 1032: 23.4 us, 109 CTAs).
+// tokens of 77 requests, rank 40, 2056 x 1032: 17.0 us, 141 CTAs).
 // Rows of a tile beyond its request's end hold whatever the buffers held; rows do not mix, and those
 // are not stored. The zero fill of TMA pads K, N and the rank.
 #include "adapters.cuh"
@@ -33,20 +33,22 @@ constexpr uint32_t kD2Col = 128;       // TMEM columns: h at 0..127, the phase-2
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSmemMax = 227 * 1024;
 
-// kR: the rank, padded (16, 32, 64 or 128)
-template <int kR>
+// kR: the rank, padded (16, 32, 64 or 128); kRows: the most rows of a tile (128 or 64: of an MMA's other rows the
+// operands are whatever lies behind in shared memory)
+template <int kR, int kRows>
 struct Shape {
     static constexpr int kBlocks = (kR + 63) / 64;        // 64-column blocks of the rank
-    static constexpr int kX = kTileM * 128;               // x or y slice: 64 bf16 a row
+    static constexpr int kX = kRows * 128;                // x or y slice: 64 bf16 a row
     static constexpr int kW = kBlocks * 64 * 128;         // bytes of a B slice (64 rows), >= the A slice (kR rows of 128)
     static_assert(kW >= kR * 128, "an A slice fits");
     static constexpr int kStage = kX + kW;
     static constexpr int kH = kBlocks * kX;               // hi (or lo)
-    static constexpr int kOutStage = kEpiWarps * 4096;    // 32 rows x 128 bytes a warp
-    static constexpr int kPart = kTileM * kR * 4;         // a cluster's partial h, before the stores need their buffers
+    static constexpr int kOutStage = kGroups * kRows * 128;  // 32 rows x 128 bytes a warp that has rows
+    static constexpr int kPart = kRows * kR * 4;          // a cluster's partial h, before the stores need their buffers
     static constexpr int kOut = kPart > kOutStage ? kPart : kOutStage;
     static constexpr int kStages = (kSmemMax - 2048 - 2 * kH - kOut) / kStage;
     static_assert(kStages >= 3, "buffers");
+    static_assert(kX + kW >= kTileM * 128 && kX + kOut >= kTileM * 128, "an MMA's 128 rows stay inside");
 };
 
 template <int kStages>
@@ -57,25 +59,26 @@ struct Tail {
     int abort;
 };
 
-template <int kR>
+template <int kR, int kRows>
 constexpr size_t smem_bytes()
 {
-    using S = Shape<kR>;
+    using S = Shape<kR, kRows>;
     constexpr size_t n = 1024 + static_cast<size_t>(S::kStages) * S::kStage + 2 * S::kH + S::kOut + sizeof(Tail<S::kStages>);
     static_assert(n <= kSmemMax, "shared memory");
     return n;
 }
 
 // Rows [row, row + rows) x 64 columns at column c into dst, by one thread: boxes of 8 rows up to 24
-// rows, of 32 up to 96, else one of 128. box: the rows of a box, n: their number.
+// rows, of 32 up to 32 less than a full tile, else one of a tile. box: the rows of a box, n: their number.
+template <int kRows>
 struct Boxes {
     int box, n;
-    __device__ explicit Boxes(int rows) : box(rows <= 24 ? 8 : rows <= 96 ? 32 : 128), n((rows + box - 1) / box) {}
+    __device__ explicit Boxes(int rows) : box(rows <= 24 ? 8 : rows <= kRows - 32 ? 32 : kRows), n((rows + box - 1) / box) {}
     __device__ uint32_t bytes() const { return static_cast<uint32_t>(box * n) * 128u; }
-    __device__ void load(uint8_t* dst, const CUtensorMap* m8, const CUtensorMap* m32, const CUtensorMap* m128, uint64_t* bar, int c,
+    __device__ void load(uint8_t* dst, const CUtensorMap* m8, const CUtensorMap* m32, const CUtensorMap* m_all, uint64_t* bar, int c,
                          int row) const
     {
-        const CUtensorMap* m = box == 8 ? m8 : box == 32 ? m32 : m128;
+        const CUtensorMap* m = box == 8 ? m8 : box == 32 ? m32 : m_all;
         for (int i = 0; i < n; ++i) ptx::tma_load_2d(dst + i * box * 128, m, bar, c, row + i * box);
     }
 };
@@ -92,15 +95,15 @@ __device__ __forceinline__ void load_h(uint32_t taddr, uint32_t (&v)[kN])
     ptx::tmem_ld_wait();
 }
 
-template <int kR>
+template <int kR, int kRows>
 __global__ void __launch_bounds__(kThreads, 1)
     k_adapter_add(const __grid_constant__ AdapterArgs p, const __grid_constant__ CUtensorMap map_x8,
-                  const __grid_constant__ CUtensorMap map_x32, const __grid_constant__ CUtensorMap map_x128,
+                  const __grid_constant__ CUtensorMap map_x32, const __grid_constant__ CUtensorMap map_x,
                   const __grid_constant__ CUtensorMap map_y8, const __grid_constant__ CUtensorMap map_y32,
-                  const __grid_constant__ CUtensorMap map_y128, const __grid_constant__ CUtensorMap map_a,
+                  const __grid_constant__ CUtensorMap map_y, const __grid_constant__ CUtensorMap map_a,
                   const __grid_constant__ CUtensorMap map_b)
 {
-    using S = Shape<kR>;
+    using S = Shape<kR, kRows>;
     constexpr int kXBytes = S::kX;
     constexpr int kStages = S::kStages;
     extern __shared__ uint8_t smem_raw[];
@@ -148,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto fail = [&]() {
         if (atomicExch(&st.abort, 1) == 0) record_status(p.status, kDevTimeoutAdapter);
     };
-    Walk<kTileM> walk;
+    Walk<kRows> walk;
     Tile t;
 
     // The issuing warps run their loops whole and one lane issues: loop counters, addresses and
@@ -161,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t ph = 0, fills = 0;
         bool ok = true;
         for (int number = cluster; ok && walk.find(p, number, t); number += n_clusters) {
-            const Boxes boxes(t.rows);
+            const Boxes<kRows> boxes(t.rows);
             if (t.adapter >= 0)
                 for (int kc = k0; kc < k1; ++kc) {
                     ok = __all_sync(0xFFFFFFFFu, ptx::mbar_wait_near(&st.empty[s], ph ^ 1));
@@ -169,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint8_t* b = smem + s * S::kStage;
                     if (leader) {
                         ptx::mbar_arrive_expect_tx(&st.full[s], rows ? boxes.bytes() : kR * 128);
-                        if (rows) boxes.load(b, &map_x8, &map_x32, &map_x128, &st.full[s], kc * 64, t.row);
+                        if (rows) boxes.load(b, &map_x8, &map_x32, &map_x, &st.full[s], kc * 64, t.row);
                         else ptx::tma_load_3d(b + kXBytes, &map_a, &st.full[s], kc * 64, 0, t.adapter);
                     }
                     ++fills;
@@ -182,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (leader) {
                     if (rows) {
                         ptx::mbar_arrive_expect_tx(&st.full[s], boxes.bytes());
-                        boxes.load(b, &map_y8, &map_y32, &map_y128, &st.full[s], nc * 64, t.row);
+                        boxes.load(b, &map_y8, &map_y32, &map_y, &st.full[s], nc * 64, t.row);
                     } else if (t.adapter >= 0) {
                         ptx::mbar_arrive_expect_tx(&st.full[s], S::kW);
 #pragma unroll
@@ -264,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // group g: its share of h's columns, every kGroups-th slice of phase 2; q: TMEM lane quarter
         const int ew = warp - kFirstEpi, g = ew / 4, q = warp & 3, row = q * 32 + lane;
         const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16);
-        uint8_t* ob = obuf + ew * 4096;
+        const uint32_t ob = ptx::smem_u32(obuf) + (g * (kRows / 32) + q) * 4096;  // (of a warp that has rows)
         int s = 0;
         uint32_t ph = 0, it = 0, cc = 0, tiles = 0;
         bool ok = true;
@@ -296,8 +299,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 split(c0 + c + 2 * i < p.r, __uint_as_float(v[c + 2 * i]) * f, __uint_as_float(v[c + 2 * i + 1]) * f,
                                       hi[i], lo[i]);
                             uint8_t* d = hbuf + ((c0 + c) / 64) * kXBytes + piece(row, ((c0 + c) % 64) / 8) + (c0 + c) % 8 * 2;
-                            *reinterpret_cast<uint2*>(d) = make_uint2(hi[0], hi[1]);
-                            *reinterpret_cast<uint2*>(d + S::kH) = make_uint2(lo[0], lo[1]);
+                            ptx::shared_store8(ptx::smem_u32(d), hi[0], hi[1]);
+                            ptx::shared_store8(ptx::smem_u32(d + S::kH), lo[0], lo[1]);
                         }
                     }
                     ptx::tc_fence_before();
@@ -315,8 +318,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
 #pragma unroll
                         for (int c = 0; c < kShare; c += 4)
-                            *reinterpret_cast<uint4*>(obuf + (row * kQuads + (((c0 + c) / 4) ^ (row & kMask))) * 16) =
-                                make_uint4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+                            ptx::shared_store16(ptx::smem_u32(obuf) + (row * kQuads + (((c0 + c) / 4) ^ (row & kMask))) * 16,
+                                                make_uint4(v[c], v[c + 1], v[c + 2], v[c + 3]));
                     }
                     ptx::tc_fence_before();
                     __syncwarp();
@@ -353,7 +356,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++it;
             }
             for (int nc = n0; nc < n1; ++nc) {
-                uint8_t* yb = smem + s * S::kStage;
                 const bool mine = cc % kGroups == static_cast<uint32_t>(g);
                 const uint32_t buf = cc % kBufs, par = (cc / kBufs) & 1;
                 ++cc;
@@ -363,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     if (live) {
                         // this lane's row: 64 sums, then with y 128 bytes of out (o[j]: piece j)
-                        uint32_t v[64], o[8][4];
+                        uint32_t v[64], o[8][4], seen = 0;
                         if (t.adapter >= 0) {
                             ptx::tc_fence_after();
 #pragma unroll
@@ -375,37 +377,41 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int c = 0; c < 64; ++c) v[c] = 0u;
                         }
+                        const uint32_t yb = ptx::smem_u32(smem) + s * S::kStage;
+                        uint4 y[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) y[j] = ptx::shared_load16(yb + piece(row, j));
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
-                            const uint4 y = *reinterpret_cast<const uint4*>(yb + piece(row, j));
-                            const uint32_t yy[4] = {y.x, y.y, y.z, y.w};
+                            const uint32_t yy[4] = {y[j].x, y[j].y, y[j].z, y[j].w};
+                            seen |= yy[0] | yy[1] | yy[2] | yy[3];
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
                                 o[j][i] = pack_bf16x2(bf16_to_f32(yy[i] & 0xFFFFu) + __uint_as_float(v[j * 8 + 2 * i]),
                                                       bf16_to_f32(yy[i] >> 16) + __uint_as_float(v[j * 8 + 2 * i + 1]));
                         }
-                        // y has to be in registers before the stage goes back. Without the fence the compiler's last uses of the
-                        // loads may follow the arrivals, and loads that queued behind stores then read the next fill.
-                        __threadfence_block();
-                        __syncwarp();
+                        // y has to be in all lanes' registers before the stage goes back, or its next fill may be read: the
+                        // arrival's address takes a zero from the loaded values, one that the compiler cannot know. (A fence
+                        // would wait for the rows that were stored a slice ago, too.)
+                        const uint32_t zero = __reduce_or_sync(0xFFFFFFFFu, seen) & static_cast<uint32_t>(p.zero);
                         if (lane == 0) {
-                            ptx::mbar_arrive(&st.empty[s]);
+                            ptx::mbar_arrive(&st.empty[s + zero]);
                             ptx::mbar_arrive(&st.d2_empty[buf]);
                         }
                         // through this warp's buffer, so that a store instruction writes four rows of 128 bytes
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            *reinterpret_cast<uint4*>(ob + piece(lane, j)) = make_uint4(o[j][0], o[j][1], o[j][2], o[j][3]);
+                        for (int j = 0; j < 8; ++j) ptx::shared_store16(ob + piece(lane, j), make_uint4(o[j][0], o[j][1], o[j][2], o[j][3]));
                         __syncwarp();
                         const int col = nc * 64 + (lane & 7) * 8, r0 = lane >> 3;
                         uint16_t* dst = p.out + (t.row + q * 32 + r0) * p.ld_out + col;
-                        const uint8_t* src = ob + piece(r0, lane & 7);  // rows r0 + 4 i: every other one swaps halves of 64 bytes
+                        const uint32_t src = piece(r0, lane & 7);  // rows r0 + 4 i: every other one swaps halves of 64 bytes
                         const int left = col < p.N ? t.rows - q * 32 - r0 : 0;
+                        uint4 w[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) w[i] = ptx::shared_load16(ob + i * 512 + (src ^ ((i & 1) * 64)));
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            if (i * 4 < left)
-                                *reinterpret_cast<uint4*>(dst + i * 4 * p.ld_out) =
-                                    *reinterpret_cast<const uint4*>(ob + i * 512 + ((src - ob) ^ ((i & 1) * 64)));
+                            if (i * 4 < left) *reinterpret_cast<uint4*>(dst + i * 4 * p.ld_out) = w[i];
                         __syncwarp();
                     } else if (lane == 0) {
                         ptx::mbar_arrive(&st.empty[s]);
@@ -445,19 +451,19 @@ CUresult map_bank(CUtensorMap* m, const uint16_t* base, int64_t cols, int64_t ro
     return encode_tmap_bf16(m, base, 3, dims, strides, box, 128);
 }
 
-template <int kR>
-cudaError_t launch(const AdapterArgs& a, int cs, int64_t tiles, int sms, cudaStream_t stream)
+template <int kR, int kRows>
+cudaError_t launch_rows(const AdapterArgs& a, int cs, int64_t tiles, int sms, cudaStream_t stream)
 {
     static bool attr_set = false;
     if (!attr_set) {
-        cudaError_t e = cudaFuncSetAttribute(k_adapter_add<kR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem_bytes<kR>()));
+        cudaError_t e = cudaFuncSetAttribute(k_adapter_add<kR, kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(smem_bytes<kR, kRows>()));
         if (e != cudaSuccess) return e;
         attr_set = true;
     }
-    CUtensorMap x8, x32, x128, y8, y32, y128, ma, mb;
+    CUtensorMap x8, x32, x, y8, y32, y, ma, mb;
     if (map_rows(&x8, a.x, a.K, a.T, a.ld_x, 8) != CUDA_SUCCESS || map_rows(&x32, a.x, a.K, a.T, a.ld_x, 32) != CUDA_SUCCESS ||
-        map_rows(&x128, a.x, a.K, a.T, a.ld_x, 128) != CUDA_SUCCESS || map_rows(&y128, a.y, a.N, a.T, a.ld_y, 128) != CUDA_SUCCESS ||
+        map_rows(&x, a.x, a.K, a.T, a.ld_x, kRows) != CUDA_SUCCESS || map_rows(&y, a.y, a.N, a.T, a.ld_y, kRows) != CUDA_SUCCESS ||
         map_rows(&y8, a.y, a.N, a.T, a.ld_y, 8) != CUDA_SUCCESS || map_rows(&y32, a.y, a.N, a.T, a.ld_y, 32) != CUDA_SUCCESS ||
         map_bank(&ma, a.a, a.K, a.r, a.n, kR) != CUDA_SUCCESS || map_bank(&mb, a.b, a.r, a.N, a.n, 64) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
@@ -466,7 +472,7 @@ cudaError_t launch(const AdapterArgs& a, int cs, int64_t tiles, int sms, cudaStr
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(clusters * cs);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem_bytes<kR>();
+    cfg.dynamicSmemBytes = smem_bytes<kR, kRows>();
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -476,7 +482,14 @@ cudaError_t launch(const AdapterArgs& a, int cs, int64_t tiles, int sms, cudaStr
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, k_adapter_add<kR>, a, x8, x32, x128, y8, y32, y128, ma, mb);
+    return cudaLaunchKernelEx(&cfg, k_adapter_add<kR, kRows>, a, x8, x32, x, y8, y32, y, ma, mb);
+}
+
+template <int kR>
+cudaError_t launch(const AdapterArgs& a, int cs, bool short_tiles, int sms, cudaStream_t stream)
+{
+    return short_tiles ? launch_rows<kR, 64>(a, cs, adapter_tiles(a, 64), sms, stream)
+                       : launch_rows<kR, kTileM>(a, cs, adapter_tiles(a, kTileM), sms, stream);
 }
 
 }  // namespace
@@ -498,12 +511,15 @@ cudaError_t launch_adapter_add(const AdapterArgs& a, int sms, cudaStream_t strea
     const int64_t tiles8 = adapter_tiles(a, 8), width = a.K + a.N, padded = a.r <= 16 ? 16 : a.r <= 32 ? 32 : a.r <= 64 ? 64 : 128;
     const int64_t t8 = 4000 + tiles8 * (5 + 2 * padded * width / 9500);
     const int64_t chain = (cs == 8 ? 6500 : 8000) + width * (cs >= 4 ? 9 : cs == 2 ? 19 : 36) / 10 + 30 * a.r;
+    // Tiles of 64 rows where one CTA a tile takes them in one round (4,113 tokens of 77 requests, rank 40: 17.0 us
+    // against 23.4; 6,000 of 50, rank 64: 25.6 against 28.7; 10,000 of 20 need two rounds: 47.0 against 31.5).
+    const bool short_tiles = cs == 1 && adapter_tiles(a, 64) <= sms + sms / 32;
     const int64_t ctas = 10 * tiles * cs, round = 11LL * sms;
     if (t8 <= (ctas <= round ? chain : chain * ctas / round)) return launch_adapter_add_small(a, sms, stream);
-    if (a.r <= 16) return launch<16>(a, cs, tiles, sms, stream);
-    if (a.r <= 32) return launch<32>(a, cs, tiles, sms, stream);
-    if (a.r <= 64) return launch<64>(a, cs, tiles, sms, stream);
-    return launch<128>(a, cs, tiles, sms, stream);
+    if (a.r <= 16) return launch<16>(a, cs, short_tiles, sms, stream);
+    if (a.r <= 32) return launch<32>(a, cs, short_tiles, sms, stream);
+    if (a.r <= 64) return launch<64>(a, cs, short_tiles, sms, stream);
+    return launch<128>(a, cs, short_tiles, sms, stream);
 }
 
 }  // namespace moe

@@ -377,7 +377,8 @@ def test_adapter_shapes(moe, r, K, N):
 
 
 @pytest.mark.parametrize("r,K,N", [(8, 8, 8), (16, 72, 56), (24, 200, 2000), (48, 2056, 1032), (64, 512, 264), (120, 1000, 8), (128, 2048, 2048)])
-@pytest.mark.parametrize("lens", [[1100], [1500, 3, 1, 900, 128, 700], [129, 2] * 100])
+@pytest.mark.parametrize("lens", [[1100], [1500, 3, 1, 900, 128, 700], [129, 2] * 100, [64, 65, 1, 40, 63, 8, 128, 9, 100, 33] * 9,
+                                  [700] * 8 + [1, 7, 31] * 6])
 def test_adapter_long_requests(moe, r, K, N, lens):
     # enough rows for the kernel of 128-row tiles, one CTA a tile or several
     check_adapter(moe, adapter_case(lens, [(i % 4) - 1 if i else 1 for i in range(len(lens))], 3, r, K, N))
@@ -399,7 +400,8 @@ def test_adapter_tiles_with_and_without_adapter_in_turn(moe, lens):
 
 
 @pytest.mark.parametrize("lens,r,K,N", [([1500, 3, 1, 900, 128, 700], 128, 2048, 2048), ([700] * 20, 64, 1032, 2056),
-                                        ([129, 2] * 150, 32, 2048, 2048), ([1] * 256, 16, 2048, 2048), ([3, 1, 5], 64, 2048, 2048)])
+                                        ([129, 2] * 150, 32, 2048, 2048), ([1] * 256, 16, 2048, 2048), ([3, 1, 5], 64, 2048, 2048),
+                                        ([130, 60, 33, 1, 77] * 16, 40, 2056, 1032)])
 def test_adapter_repeats_itself(moe, lens, r, K, N):
     # the same bits every time, also while other work keeps the memory busy
     c = adapter_case(lens, [(i % 4) - 1 if i else 1 for i in range(len(lens))], 3, r, K, N)
