@@ -505,7 +505,7 @@ cudaError_t launch_adapter_add(const AdapterArgs& a, int sms, cudaStream_t strea
     // Estimated times in ns, from sweeps over 1 to 16,384 tokens of 1 to 256 requests, ranks 16 and 64, K x N
     // 2048 x 2048 and 512 x 1024 on 152 multiprocessors. Tiles of 8 rows: 4 us, 5 ns a tile and 105 ns a MB of
     // A and B (of padded rank) that the tiles read (256 single tokens, rank 64: 17.8 us against 36.9 with tiles
-    // of 128; 4,113 tokens of 77 requests, rank 40: 30 against 23.4). Tiles of 128: the chain of one tile,
+    // of 128; 4,113 tokens of 77 requests, rank 40: 30 against 17.0). Tiles of 128: the chain of one tile,
     // shorter the more CTAs share it, times the rounds of CTAs (4,113 tokens of 16 requests, rank 64: 18.4 us
     // against 33; 16,384 of 24: 38 against 130).
     const int64_t tiles8 = adapter_tiles(a, 8), width = a.K + a.N, padded = a.r <= 16 ? 16 : a.r <= 32 ? 32 : a.r <= 64 ? 64 : 128;
