@@ -12,8 +12,8 @@
 //            sums are added at the end), columns on N. Column 2q + e of product i stands for column 8q + 2i
 //            + e of 32, so that a thread ends with eight neighbouring columns of a row: one 16-byte load of
 //            y and one store of out. Ranks up to 16 take 8 bytes a thread and one product of 16.
-// Measured, 2048 x 2048: 256 requests of one token, rank 32 10.7 us (52 MB of A and B from L2, 4.9 TB/s);
-// 4 tokens, rank 16 4.3 us, the chain of one tile.
+// Measured, 2048 x 2048: 256 requests of one token, rank 32 10.1 us (52 MB of A and B from L2, 5.1 TB/s);
+// 4 tokens, rank 16 4.2 us, the chain of one tile.
 #include "adapters.cuh"
 
 namespace moe {
@@ -57,6 +57,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_adapter_add_small(const __grid_
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, q = lane % 4;
     const int cs = static_cast<int>(ptx::cluster_size()), rank = static_cast<int>(ptx::cluster_rank());
     const int cluster = blockIdx.x / cs, n_clusters = gridDim.x / cs;
+    // A CTA's shared memory may be written by the others once that CTA has started: all arrive here, and wait
+    // before their first store to another (as before each tile's, then for the readers of the tile before).
+    if (cs > 1) ptx::cluster_arrive_all();
     // rows of h that no token fills, and columns past the rank, stay zero
     for (int i = tid; i < static_cast<int>(sizeof(h_s) / 4); i += kThreads) reinterpret_cast<uint32_t*>(h_s)[i] = 0u;
     ptx::griddep_wait();
@@ -65,7 +68,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_adapter_add_small(const __grid_
     Walk<kM> walk;
     Tile t;
     const bool check = blockIdx.x == 0 && warp == 0;
-    bool sent = false;
     for (int number = cluster; walk.find(p, number, t, check); number += n_clusters) {
         if (t.adapter < 0) {
             const int w = min(c1 * 32, p.N) / 8 - c0 * 4;  // 16-byte pieces of a row
@@ -76,7 +78,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_adapter_add_small(const __grid_
             }
             continue;
         }
-        if (sent) ptx::cluster_wait();  // all of the cluster have read the sums of the tile before
         {
             const int rb = warp % kBlocks, kw = warp / kBlocks;
             const int steps = (p.K + 31) / 32, share = cs * kSplit, me = rank * kSplit + kw;
@@ -130,6 +131,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_adapter_add_small(const __grid_
         load_b(c0 + warp * kUnroll2);
         __syncthreads();
         if (cs > 1) {  // this CTA's sum goes to every CTA of the cluster
+            ptx::cluster_wait();  // all of them have started and have read the sums of the tile before
             for (int i = tid; i < kR * kM; i += kThreads) {
                 float v = part[0][i];
 #pragma unroll
@@ -160,7 +162,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_adapter_add_small(const __grid_
             *reinterpret_cast<uint32_t*>(&h_s[1][tok][j]) = lo;
         }
         if (cs > 1) ptx::cluster_arrive_all();  // this CTA has read the cluster's sums
-        sent = cs > 1;
         __syncthreads();
 
         uint4 hi[kSteps], lo[kSteps];  // token g's h, in the order of the products' k
@@ -200,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_adapter_add_small(const __grid_
         __syncthreads();  // h is read
     }
     if (check) report(p, walk);
-    if (sent) ptx::cluster_wait();
+    if (cs > 1) ptx::cluster_wait();  // the last arrival's
 }
 
 template <int kR>
