@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kWarps * 32, kNper < 8 || (kL == 32 && kNper <
 #pragma unroll
             for (int i = 0; i < kNper; ++i) sum += fast_exp(c[i] - m);
             inv_sum = 1.0f / lanes_sum<kL>(sum);
-            smax = inv_sum;
+            if (a.bias) smax = inv_sum;  // without one, groups are compared by exp(l - m), which the sum does not divide
         }
     }
     if (a.bias) {
