@@ -167,7 +167,7 @@ __device__ __noinline__ unsigned exact_groups(const SelectArgs& a, int64_t t, co
         top = fmaxf(top, o1);
     }
     if (!a.group_top2) v2 = top;
-    const float margin = a.bias ? 2.0f * (eps_score + kEpsAdd * fabsf(top)) : 0.0f;
+    const float margin = a.bias ? 2.0f * (eps_score + kEpsAdd * fmaxf(fabsf(top), fabsf(v2))) : 0.0f;
     const bool real = g < a.n_group;
     const float thr = v2 < INFINITY ? v2 - margin : v2;  // -inf where the group has one unmasked expert or none
     uint64_t hits = 0;              // this lane's values: j, j + per, ... (at most 43 of them)
@@ -511,12 +511,25 @@ __global__ void __launch_bounds__(kWarps * 32, kNper < 8 || (kL == 32 && kNper <
         // a group's bit is that of its first lane
         unsigned keep = __ballot_sync(kFull, real && j == 0 && rank < a.topk_group) >> (sub * kL);
         if (a.bias || a.group_top2) {
-            // the last group that stays and the first that goes, by their ranks
-            const unsigned last = __ballot_sync(kFull, real && rank == a.topk_group - 1) >> (sub * kL);
-            const unsigned first = __ballot_sync(kFull, real && rank == a.topk_group) >> (sub * kL);
-            const float lo = __shfl_sync(kFull, gv, __ffs(last) - 1, kL), hi = __shfl_sync(kFull, gv, __ffs(first) - 1, kL);
-            const bool near = valid && !whole && hi > -INFINITY &&
-                              lo - hi <= 4.0f * eps_score + 2.0f * kEpsAdd * (fabsf(lo) + fabsf(hi));
+            // The lowest that a group that stays can be against the highest that one that goes can be. Both of a
+            // group's values have a score's error and a rounding of their own size, which may cancel in the sum; the
+            // sum is rounded once more. (The roundings of lo and hi themselves keep their order.)
+            const float size = !a.bias ? gv : a.group_top2 && v2 > -INFINITY ? fabsf(v1) + fabsf(v2) : fabsf(v1);
+            const bool inexact = a.bias ? fabsf(v1) < INFINITY : v1 > -INFINITY;  // a masked group and an infinite bias are exact
+            const float err = inexact ? 2.0f * (eps_score + kEpsAdd * size) : 0.0f;
+            const bool range = err < INFINITY;  // a sum that left it says nothing
+            float lo = real && rank < a.topk_group ? (range ? gv - err : -INFINITY) : INFINITY;
+            float hi = real && rank >= a.topk_group ? (range ? gv + err : INFINITY) : -INFINITY;
+            if constexpr (kL == 32) {
+                asm volatile("redux.sync.min.f32 %0, %0, 0xFFFFFFFF;" : "+f"(lo));
+                asm volatile("redux.sync.max.f32 %0, %0, 0xFFFFFFFF;" : "+f"(hi));
+            } else {
+                for (int o = per; o < kL; o <<= 1) {
+                    lo = fminf(lo, __shfl_xor_sync(kFull, lo, o));
+                    hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, o));
+                }
+            }
+            const bool near = valid && !whole && hi > -INFINITY && lo <= hi;
             auto decide = [&](int h, float eps) {
                 const unsigned stay = exact_groups<F32>(a, t0 + h, c_all + h * kE, eps);
                 if (sub == h) {

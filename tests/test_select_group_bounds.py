@@ -3,7 +3,7 @@ error bound has to send them to the FP64 decision."""
 import pytest
 import torch
 
-from test_block_ops import check_select, moe  # noqa: F401
+from test_block_ops import check_select, gen, moe, randn  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -28,3 +28,39 @@ def test_groups_without_bias_nearer_than_their_scores_errors(moe, T, E, renorm):
         l[flip * n: (flip + 1) * n, 2 - flip, 10:12] = pairs[:, 2:]
     l = l.reshape(2 * n, E).repeat((T + 2 * n - 1) // (2 * n), 1)[:T]
     check_select(moe, l, 4, score="softmax", G=4, keep=2, top2=True, renorm=renorm)
+
+
+@pytest.mark.parametrize("T,E,G,keep", [(4096, 512, 8, 4), (4096, 256, 8, 4), (3000, 64, 16, 3), (500, 1020, 17, 9)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("big", [1000.0, 3e7])
+def test_groups_whose_biases_cancel(moe, T, E, G, keep, score, big):  # noqa: F811
+    # a group's two largest values are near +big and -big: their sum is small, its FP32 rounding is not
+    g = gen(T + E)
+    bias = torch.full((G, E // G), -10 * big, device="cuda")
+    bias[:, 0], bias[:, 1] = big, -big
+    check_select(moe, randn(g, T, E), keep, bias=bias.reshape(-1), score=score, G=G, keep=keep)
+    bias[1::2, 0], bias[1::2, 1] = 0.5, -0.5  # every other group's sum is nearly exact
+    check_select(moe, randn(g, T, E), keep, bias=bias.reshape(-1), score=score, G=G, keep=keep)
+
+
+@pytest.mark.parametrize("T,E,G", [(4096, 512, 8), (4096, 256, 8), (700, 1020, 17)])
+def test_groups_whose_second_values_lie_far_below_the_first(moe, T, E, G):  # noqa: F811
+    # scores near a rounding border of score - 1000: the second largest in FP32 is not always the second largest
+    g = gen(T + E + 1)
+    bias = torch.full((G, E // G), -1000.0, device="cuda")
+    bias[:, 0] = 0.0
+    l = randn(g, T, E, std=4e-7, mean=1.2207e-4).view(T, G, E // G)
+    l[:, :, 0] = 1.0
+    check_select(moe, l.reshape(T, E), 4, bias=bias.reshape(-1), G=G, keep=4)
+
+
+def test_groups_whose_sums_leave_the_range(moe):  # noqa: F811
+    # two biases whose FP32 sum is infinite: the 64-bit sums tell the groups apart
+    E, G = 64, 8
+    bias = torch.zeros(G, E // G, device="cuda")
+    bias[2, 1], bias[2, 3] = 2e38, 2.0e38
+    bias[5, 1], bias[5, 3] = 2e38, 2.5e38
+    bias[6, 0], bias[6, 2] = 3e38, -3e38
+    g = gen(9)
+    for T in (8, 2600):
+        check_select(moe, randn(g, T, E), 2, bias=bias.reshape(-1), G=G, keep=1)
