@@ -270,8 +270,8 @@ moe_status_t moe_layer_forward_host(const moe_layer_t* L, const uint16_t* x, int
  *   gate[t * gate_ld]; gate_ld = 0 uses one row for every token.
  *   ld_*: elements between two rows. H % 8 == 0, 8 <= H <= 8192; every row starts on 16 bytes
  *   (a gate of one value per token: on its own size); residual_out may be residual and x_out may be
- *   y (the same address and row stride), no other overlap. An empty batch (T = 0) returns MOE_OK
- *   after the shape check.
+ *   y (the same address and row stride), no other overlap (other columns of one buffer are apart).
+ *   An empty batch (T = 0) returns MOE_OK after the shape check.
  * ------------------------------------------------------------------------------------------- */
 enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1 };
 
@@ -343,7 +343,8 @@ moe_status_t moe_select_experts(const moe_routing_t* R, const void* logits, int 
  *   x: bf16 [T][K]; y, out: bf16 [T][N]; ld_*: elements between two rows, every row on 16 bytes.
  *   K and N multiples of 8 in [8, 16384]; rank r a multiple of 8 in [8, 128]; adapters of smaller
  *   rank are padded with zeros. Sums are FP32; A_a x is held in 16 significant bits or more between
- *   the two products. out may be y (the same address and row stride), no other overlap.
+ *   the two products. out may be y (the same address and row stride), no other overlap (other
+ *   columns of one buffer are apart).
  *   ws: >= 256 bytes. T = 0 returns MOE_OK after the shape check.
  * ------------------------------------------------------------------------------------------- */
 typedef struct {

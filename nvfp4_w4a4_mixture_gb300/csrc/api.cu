@@ -537,12 +537,17 @@ moe_status_t moe_combine(const uint16_t* y, const float* topk_w, const float* sh
     return MOE_OK;
 }
 
-// Whether the rows [T][width bytes] at a (stride ld bytes) and at b overlap in memory.
+// Whether the T rows of width_a bytes at a (ld_a bytes apart) and those at b overlap in memory: exactly where
+// both strides are the same (columns of one buffer are apart), else by the spans from the first row to the last.
 static bool rows_overlap(const void* a, int64_t ld_a, int64_t width_a, const void* b, int64_t ld_b, int64_t width_b, int T)
 {
     if (!a || !b || T <= 0) return false;
     const char *a0 = static_cast<const char*>(a), *b0 = static_cast<const char*>(b);
-    return a0 < b0 + (T - 1) * ld_b + width_b && b0 < a0 + (T - 1) * ld_a + width_a;
+    if (a0 >= b0 + (T - 1) * ld_b + width_b || b0 >= a0 + (T - 1) * ld_a + width_a) return false;
+    if (T == 1 || ld_a != ld_b || width_a > ld_a || width_b > ld_a) return true;
+    // b's row j begins d bytes into the row j + q of a's buffer and ends in that row or the next
+    const int64_t off = b0 - a0, q = off >= 0 ? off / ld_a : -((ld_a - 1 - off) / ld_a), d = off - q * ld_a;
+    return (d < width_a && q > -T && q < T) || (d + width_b > ld_a && q + 1 > -T && q + 1 < T);
 }
 
 // One tensor of rows: base and row stride on 16 bytes, the stride at least a row (T > 1).
