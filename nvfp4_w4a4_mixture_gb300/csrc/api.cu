@@ -550,6 +550,13 @@ static bool rows_overlap(const void* a, int64_t ld_a, int64_t width_a, const voi
     return (d < width_a && q > -T && q < T) || (d + width_b > ld_a && q + 1 > -T && q + 1 < T);
 }
 
+// The same of the T rows at a and `bytes` bytes at b.
+static bool rows_overlap_bytes(const void* a, int64_t ld_a, int64_t width_a, int T, const void* b, int64_t bytes)
+{
+    return a && b && T > 0 && static_cast<const char*>(a) < static_cast<const char*>(b) + bytes &&
+           static_cast<const char*>(b) < static_cast<const char*>(a) + (T - 1) * ld_a + width_a;
+}
+
 // One tensor of rows: base and row stride on 16 bytes, the stride at least a row (T > 1).
 static moe_status_t check_rows(const char* name, const void* p, int64_t ld, int64_t width, int elem, int T)
 {
@@ -660,6 +667,8 @@ moe_status_t moe_select_experts(const moe_routing_t* R, const void* logits, int 
     if (rows_overlap(topk_ids, ob, ob, logits, ld * es, E * es, T) || rows_overlap(topk_w, ob, ob, logits, ld * es, E * es, T) ||
         rows_overlap(topk_ids, ob, ob, topk_w, ob, ob, T))
         return fail(MOE_ERR_INVALID_ARG, "topk_ids, topk_w and logits overlap");
+    if (rows_overlap_bytes(topk_ids, ob, ob, T, R->bias, 4LL * E) || rows_overlap_bytes(topk_w, ob, ob, T, R->bias, 4LL * E))
+        return fail(MOE_ERR_INVALID_ARG, "topk_ids or topk_w overlaps the bias");
     MOE_TRY(check_device());
     SelectArgs a{};
     a.T = T;
@@ -706,6 +715,10 @@ moe_status_t moe_adapter_add(const moe_adapters_t* A, const uint16_t* x, int64_t
     if (rows_overlap(out, ld_out * 2, nb, x, ld_x * 2, kb, T)) return fail(MOE_ERR_INVALID_ARG, "out overlaps x");
     if (!(out == y && (T == 1 || ld_out == ld_y)) && rows_overlap(out, ld_out * 2, nb, y, ld_y * 2, nb, T))
         return fail(MOE_ERR_INVALID_ARG, "out overlaps y without being y");
+    if (rows_overlap_bytes(out, ld_out * 2, nb, T, A->a, kb * n * r) || rows_overlap_bytes(out, ld_out * 2, nb, T, A->b, nb * n * r) ||
+        rows_overlap_bytes(out, ld_out * 2, nb, T, A->scale, 4LL * n) || rows_overlap_bytes(out, ld_out * 2, nb, T, seg_offsets, 4LL * (S + 1LL)) ||
+        rows_overlap_bytes(out, ld_out * 2, nb, T, seg_adapter, 4LL * S))
+        return fail(MOE_ERR_INVALID_ARG, "out overlaps a, b, scale, seg_offsets or seg_adapter");
     MOE_TRY(check_ws(ws, ws_bytes, sizeof(WsHeader)));
     MOE_TRY(check_device());
     AdapterArgs a{};

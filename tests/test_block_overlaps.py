@@ -39,6 +39,26 @@ def test_adapter_columns_of_one_buffer(m, no_gpu):  # noqa: F811
     assert adapt(m, y=2 * MB, ld_y=2 * N, out=2 * MB + 2 * (N - 8), ld_out=2 * N) == INVALID
 
 
+def test_outputs_on_the_small_inputs_are_refused(m):  # noqa: F811
+    # one of T * k ids or weights on one of E biases
+    for kw in (dict(bias=2 * MB), dict(bias=3 * MB + 4 * 10 * 4 - 4), dict(bias=2 * MB - 512 * 4 + 4)):
+        assert select(m, **kw) == INVALID, kw
+    last = 3 * MB + 3 * 1024 * 2 + 1024 * 2  # behind out's last row
+    for kw in (dict(a=3 * MB), dict(b=last - 16), dict(scale=last - 4), dict(off=3 * MB + 4), dict(ids=last - 4),
+               dict(off=3 * MB - 8), dict(ids=3 * MB - 4), dict(a=3 * MB - 4 * 16 * 2048 * 2 + 16)):
+        assert adapt(m, **kw) == INVALID, kw
+        assert b"overlap" in m.lib().moe_last_error_detail()
+
+
+def test_outputs_beside_the_small_inputs(m, no_gpu):  # noqa: F811
+    last = 3 * MB + 3 * 1024 * 2 + 1024 * 2
+    for kw in (dict(bias=3 * MB + 4 * 10 * 4), dict(bias=2 * MB - 512 * 4)):
+        assert passes(select(m, **kw)), kw
+    for kw in (dict(b=last), dict(scale=last), dict(off=last), dict(ids=last), dict(off=3 * MB - 12), dict(ids=3 * MB - 8),
+               dict(a=3 * MB - 4 * 16 * 2048 * 2)):
+        assert passes(adapt(m, **kw)), kw
+
+
 @pytest.mark.gpu
 def test_columns_of_one_buffer_give_the_same(moe):  # noqa: F811
     g = gen(2)
