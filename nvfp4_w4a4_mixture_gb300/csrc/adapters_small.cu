@@ -12,7 +12,7 @@
 //            sums are added at the end), columns on N. Column 2q + e of product i stands for column 8q + 2i
 //            + e of 32, so that a thread ends with eight neighbouring columns of a row: one 16-byte load of
 //            y and one store of out. Ranks up to 16 take 8 bytes a thread and one product of 16.
-// Measured, 2048 x 2048: 256 requests of one token, rank 32 10.1 us (52 MB of A and B from L2, 5.1 TB/s);
+// Measured, 2048 x 2048: 256 requests of one token, rank 32 10.3 us (52 MB of A and B from L2, 5 TB/s);
 // 4 tokens, rank 16 4.2 us, the chain of one tile.
 #include "adapters.cuh"
 
@@ -45,6 +45,12 @@ __device__ __forceinline__ uint4 load16(const uint16_t* p, bool in)
     return in ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
 }
 
+// y may be out: not through the path of data that the kernel does not change
+__device__ __forceinline__ uint4 load16_y(const uint16_t* p, bool in)
+{
+    return in ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
+}
+
 template <int kR>
 __global__ void __launch_bounds__(kThreads, 2) k_adapter_add_small(const __grid_constant__ AdapterArgs p)
 {
@@ -74,7 +80,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_adapter_add_small(const __grid_
             for (int i = tid; i < w * t.rows; i += kThreads) {
                 const int64_t row = t.row + i / w;
                 const int col = c0 * 32 + i % w * 8;
-                *reinterpret_cast<uint4*>(p.out + row * p.ld_out + col) = load16(p.y + row * p.ld_y + col, true);
+                *reinterpret_cast<uint4*>(p.out + row * p.ld_out + col) = load16_y(p.y + row * p.ld_y + col, true);
             }
             continue;
         }
@@ -125,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_adapter_add_small(const __grid_
                     }
                 }
                 const int col = (c + u) * 32 + q * 8;
-                yv[u] = load16(p.y + (t.row + g) * p.ld_y + col, c + u < c1 && col < p.N && g < t.rows);
+                yv[u] = load16_y(p.y + (t.row + g) * p.ld_y + col, c + u < c1 && col < p.N && g < t.rows);
             }
         };
         load_b(c0 + warp * kUnroll2);
