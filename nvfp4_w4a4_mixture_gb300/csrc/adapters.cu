@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ptx::tc_fence_before();
                         } else {
 #pragma unroll
-                            for (int c = 0; c < 64; ++c) v[c] = 0u;
+                            for (int c = 0; c < 64; ++c) v[c] = 0x80000000u;  // -0: what leaves y's sign of zero as it is
                         }
                         const uint32_t yb = ptx::smem_u32(smem) + s * S::kStage;
                         uint4 y[8];

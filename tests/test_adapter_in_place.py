@@ -1,4 +1,5 @@
-"""GPU: adapters added in place again and again, each call reading what the one before it has just written."""
+"""GPU: adapters added in place again and again, each call reading what the one before it has just written, and rows
+without an adapter, which are y's values in every kernel, the sign of a zero included."""
 import pytest
 import torch
 
@@ -20,3 +21,20 @@ def test_in_place_calls_in_a_row(moe, lens, r, K, N):  # noqa: F811
         moe.moe_adapter_add(y=y, out=y, **c)
     moe.moe_read_device_status()
     assert torch.equal(a, y)
+
+
+@pytest.mark.parametrize("lens,r,K,N", [([1] * 40, 16, 256, 256), ([5000, 9], 64, 2048, 2048), ([3000, 3000], 64, 2048, 2048),
+                                        ([40, 130, 7, 64] * 25, 40, 1032, 2056)])
+def test_rows_without_adapter_keep_their_values(moe, lens, r, K, N):  # noqa: F811
+    c = adapter_case(lens, [-1 if i % 2 == 0 else 0 for i in range(len(lens))], 1, r, K, N)
+    c["y"][::3], c["y"][1::7, ::5] = -0.0, float("nan")
+    off = c["seg_offsets"].tolist()
+    for out in (None, c["y"].clone()):
+        y = c["y"] if out is None else out
+        want = y.clone()
+        got = moe.moe_adapter_add(**dict(c, y=y), out=out)
+        for i in range(0, len(lens), 2):
+            rows = slice(off[i], off[i + 1])
+            real = ~want[rows].isnan()
+            assert torch.equal(got[rows].isnan(), ~real)
+            assert torch.equal(got[rows].view(torch.int16)[real], want[rows].view(torch.int16)[real])
