@@ -22,6 +22,7 @@
 #include <cfloat>
 
 #include "block.cuh"
+#include "fp64.cuh"
 #include "topk.cuh"
 
 namespace moe {
@@ -56,13 +57,6 @@ __device__ __forceinline__ float fast_exp(float x)
     return r;
 }
 
-__device__ __forceinline__ float fast_rcp(float x)
-{
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
 __device__ __forceinline__ float warp_max(float v)
 {
 #pragma unroll
@@ -75,43 +69,6 @@ __device__ __forceinline__ float warp_sum(float v)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
     return v;
-}
-
-// FP64 runs at 1/64 of the FP32 rate here (a warp instruction takes some 58 cycles), so the exponential
-// and the reciprocal are as short as 52 bits allow: the table-driven exponential of Tang (ACM TOMS 15,
-// 1989), x = (n / 32) ln 2 + r with |r| <= ln 2 / 64, exp(x) = 2^(n / 32) (1 + r + ... + r^6 / 720), and two
-// Newton steps from the FP32 reciprocal. Both are off by about an ulp; with the library's functions a token that
-// is ranked again took 2.8 us.
-__device__ const double kExp2[32] = {  // 2^(j / 32)
-    0x1.0000000000000p+0, 0x1.059b0d3158574p+0, 0x1.0b5586cf9890fp+0, 0x1.11301d0125b51p+0,
-    0x1.172b83c7d517bp+0, 0x1.1d4873168b9aap+0, 0x1.2387a6e756238p+0, 0x1.29e9df51fdee1p+0,
-    0x1.306fe0a31b715p+0, 0x1.371a7373aa9cbp+0, 0x1.3dea64c123422p+0, 0x1.44e086061892dp+0,
-    0x1.4bfdad5362a27p+0, 0x1.5342b569d4f82p+0, 0x1.5ab07dd485429p+0, 0x1.6247eb03a5585p+0,
-    0x1.6a09e667f3bcdp+0, 0x1.71f75e8ec5f74p+0, 0x1.7a11473eb0187p+0, 0x1.82589994cce13p+0,
-    0x1.8ace5422aa0dbp+0, 0x1.93737b0cdc5e5p+0, 0x1.9c49182a3f090p+0, 0x1.a5503b23e255dp+0,
-    0x1.ae89f995ad3adp+0, 0x1.b7f76f2fb5e47p+0, 0x1.c199bdd85529cp+0, 0x1.cb720dcef9069p+0,
-    0x1.d5818dcfba487p+0, 0x1.dfc97337b9b5fp+0, 0x1.ea4afa2a490dap+0, 0x1.f50765b6e4540p+0};
-
-__device__ __forceinline__ double exp64(double x)
-{
-    if (!(fabs(x) < 700.0)) return exp(x);
-    const int n = __double2int_rn(x * 0x1.71547652b82fep+5);
-    const double r = fma(n, -0x1.473de6af278edp-39, fma(n, -0x1.62e42fef00000p-6, x));  // the longer part of ln 2 / 32 is exact times n
-    double p = fma(r, 1.0 / 720, 1.0 / 120);
-    p = fma(r, p, 1.0 / 24);
-    p = fma(r, p, 1.0 / 6);
-    p = fma(r, p, 0.5);
-    p = fma(r, p, 1.0);
-    p = fma(r, p, 1.0) * kExp2[n & 31];
-    return __hiloint2double(__double2hiint(p) + ((n >> 5) << 20), __double2loint(p));
-}
-
-__device__ __forceinline__ double rcp64(double d)
-{
-    if (!(d < 1e30)) return 1.0 / d;
-    double r = fast_rcp(static_cast<float>(d));
-    r = fma(r, fma(-d, r, 1.0), r);
-    return fma(r, fma(-d, r, 1.0), r);
 }
 
 // Scores in FP64. m: the row's largest logit (softmax); scale: 1 / its softmax sum, or 1 where only the
