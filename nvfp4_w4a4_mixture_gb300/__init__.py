@@ -8,12 +8,13 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import os
+import sysconfig
 
 import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libmoe_nvfp4.so")
-CALLS_PATH = os.path.join(_HERE, "_lib", "_calls.so")
+CALLS_PATH = os.path.join(_HERE, "_lib", "_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 EPI_F32, EPI_BF16, EPI_SWIGLU_NVFP4 = 0, 1, 2
 SCHED_AUTO, SCHED_ACT_ON_M, SCHED_WEIGHTS_ON_M, SCHED_WIDE, SCHED_WIDE_ROWS = 0, 0x100, 0x200, 0x400, 0x800
@@ -78,10 +79,14 @@ _calls = None  # the C marshalling of the block calls (csrc/calls.c), where it w
 
 def _load_calls(L):
     global _calls
+    _calls = None
     if os.path.exists(CALLS_PATH):
         loader = importlib.machinery.ExtensionFileLoader("_calls", CALLS_PATH)
-        mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_calls", loader))
-        loader.exec_module(mod)
+        try:
+            mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_calls", loader))
+            loader.exec_module(mod)
+        except ImportError:  # the same calls go through ctypes
+            return
         mod.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (L.moe_norm_residual, L.moe_select_experts, L.moe_adapter_add)),
                  torch.bfloat16, torch.float32, torch.int32)
         _calls = mod

@@ -16,7 +16,8 @@ SRC_DIR = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_lib")
 OBJ_DIR = os.path.join(OUT_DIR, "obj")
 LIB = os.path.join(OUT_DIR, "libmoe_nvfp4.so")
-CALLS_SRC, CALLS = os.path.join(SRC_DIR, "calls.c"), os.path.join(OUT_DIR, "_calls.so")
+CALLS_SRC = os.path.join(SRC_DIR, "calls.c")
+CALLS = os.path.join(OUT_DIR, "_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
