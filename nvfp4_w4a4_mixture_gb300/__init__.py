@@ -432,23 +432,28 @@ def moe_layer_forward_profiled(layer, x, events, residual=None, out=None, ws=Non
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
+_INT_MAX = 0x7FFFFFFF  # of a count in the C calls
+
+
 def _refuse(t, name, dtype, shape):
     if t.dtype != dtype or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor of %s, got %s on %s" % (name, dtype, t.dtype, t.device))
+    if shape[0] > _INT_MAX:
+        raise ValueError("%s: %d rows, more than %d" % (name, shape[0], _INT_MAX))
     raise ValueError("%s must have shape %s and be contiguous (rows may be strided where that is allowed), got %s with strides %s"
                      % (name, tuple(shape), tuple(t.shape), t.stride()))
 
 
 def _whole(t, name, dtype, shape):
     """The data pointer of a contiguous CUDA tensor of that type and shape (an int or None, as ctypes takes it)."""
-    if t.dtype is not dtype or not t.is_cuda or t.shape != shape or not t.is_contiguous():
+    if t.dtype is not dtype or not t.is_cuda or t.shape != shape or not t.is_contiguous() or shape[0] > _INT_MAX:
         _refuse(t, name, dtype, shape)
     return t.data_ptr()
 
 
 def _rows(t, name, dtype, shape):
     """(data pointer, elements between two rows) of a CUDA tensor of that type and shape [T, n] whose rows are contiguous."""
-    if t.dtype is dtype and t.is_cuda and t.shape == shape:
+    if t.dtype is dtype and t.is_cuda and t.shape == shape and shape[0] <= _INT_MAX:
         if t.is_contiguous():
             return t.data_ptr(), shape[1]
         if shape[1] == 1 or t.stride(1) == 1:

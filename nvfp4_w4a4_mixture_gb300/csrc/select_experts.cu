@@ -639,7 +639,7 @@ template <int kL, int kNper, bool F32>
 cudaError_t launch(const SelectArgs& a, bool vec, cudaStream_t stream)
 {
     constexpr int per_cta = kWarps * (32 / kL);
-    const dim3 grid((a.T + per_cta - 1) / per_cta), block(kWarps * 32);
+    const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(a.T) + per_cta - 1) / per_cta)), block(kWarps * 32);
     if constexpr (kNper >= 4) {
         if (vec) return launch_pdl(k_select_experts<kL, kNper, F32, true>, grid, block, 0, stream, a);
     }
