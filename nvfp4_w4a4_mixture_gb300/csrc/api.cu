@@ -628,7 +628,7 @@ moe_status_t moe_norm_residual(const moe_norm_t* N, const uint16_t* y, int64_t l
     a.w_pre = N->w_pre;
     a.eps = N->eps;
     a.w_offset = N->w_offset;
-    a.res_scale = N->residual_scale;
+    a.res_scale = residual ? N->residual_scale : 0.0f;  // a term that is left out, whatever its scale
     a.gate = N->gate;
     a.gate_f32 = gs == 4;
     a.gate_per_channel = N->gate_per_channel != 0;
