@@ -426,8 +426,9 @@ moe_status_t moe_layer_workspace_view(const moe_layer_t* L, int T, moe_layer_vie
  *   for a token block's intermediate then gives up after wait_limit_us microseconds (0: the
  *   default, 1 s) and needs ready_extra more completions than exist (0: the real count), so
  *   with ready_extra > 0 every down tile of moe_layer_forward times out; the launch stops, frees
- *   its tensor memory and records MOE_ERR_DEVICE_TIMEOUT for moe_read_device_status(). Another
- *   call with (0, 0) restores normal operation. The values are written into the workspace header
+ *   its tensor memory and records MOE_ERR_DEVICE_TIMEOUT for moe_read_device_status(). In
+ *   moe_adapter_add (requests that go to its tensor-memory kernel) the wait for A x does the same.
+ *   Another call with (0, 0) restores normal operation. The values are written into the workspace header
  *   in stream order (a one-thread kernel on `stream`).
  * ------------------------------------------------------------------------------------------- */
 moe_status_t moe_set_wait_test_hook(void* ws, unsigned wait_limit_us, int ready_extra, moe_stream_t stream);

@@ -740,6 +740,7 @@ moe_status_t moe_adapter_add(const moe_adapters_t* A, const uint16_t* x, int64_t
     a.out = out;
     a.ld_out = T > 1 ? ld_out : N;
     a.status = &static_cast<WsHeader*>(ws)->status;
+    a.hooks = static_cast<const WsHeader*>(ws);
     MOE_CUDA(launch_adapter_add(a, device_sm_count(), static_cast<cudaStream_t>(stream)), "adapter launch");
     return MOE_OK;
 }

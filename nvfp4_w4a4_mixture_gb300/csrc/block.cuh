@@ -71,6 +71,7 @@ struct AdapterArgs {
     uint16_t* out;
     int64_t ld_out;
     int* status;
+    const WsHeader* hooks;    // the workspace header whose test_* fields a wait reads
     int zero;                 // 0, which kernels do not know
 };
 cudaError_t launch_adapter_add(const AdapterArgs& a, int sms, cudaStream_t stream);

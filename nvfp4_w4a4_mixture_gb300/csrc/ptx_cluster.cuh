@@ -129,6 +129,15 @@ __device__ __forceinline__ bool mbar_wait_near(uint64_t* bar, uint32_t parity)
     }
 }
 
+// mbar_wait with a limit in microseconds (0: kWaitLimitNs).
+__device__ __forceinline__ bool mbar_wait_us(uint64_t* bar, uint32_t parity, unsigned us)
+{
+    const uint64_t t0 = globaltimer(), limit = us ? static_cast<uint64_t>(us) * 1000u : kWaitLimitNs;
+    while (!mbar_try_wait(bar, parity))
+        if (globaltimer() - t0 > limit) return false;
+    return true;
+}
+
 // Warp-wide: true in one lane, the same at every call with all lanes.
 __device__ __forceinline__ bool elect_one()
 {
