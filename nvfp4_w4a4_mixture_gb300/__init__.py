@@ -200,6 +200,23 @@ def _ws(nbytes):
     return w
 
 
+_adapter_ws = {}
+
+
+def _adapter_workspace():
+    """moe_adapter_add's workspace where the caller gives none: its header is all that the call uses, so it is never
+    replaced by a larger one, which would lose its report and leave captured calls with memory that was given back."""
+    dev = torch.cuda.current_device()
+    w = _adapter_ws.get(dev)
+    if w is None:
+        w = Workspace(4096)
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream().synchronize()  # the header is zero for every stream from here on
+            _adapter_ws[dev] = w
+        # a capture zeroes the header at each replay: its workspace belongs to the graph, and its report is lost
+    return w
+
+
 def moe_set_wait_test_hook(ws, wait_limit_us, ready_extra):
     """Test hook: the expert GEMMs' wait for a token block's intermediate gives up after
     wait_limit_us (0: default) and needs ready_extra more completions (0: none); (0, 0) restores."""
@@ -207,7 +224,12 @@ def moe_set_wait_test_hook(ws, wait_limit_us, ready_extra):
 
 
 def moe_read_device_status(ws=None):
-    ws = ws or _ws(4096)
+    """Raises what the calls on the workspace have reported since the last reading (None: the default workspaces)."""
+    if ws is None:
+        w = _adapter_ws.get(torch.cuda.current_device())
+        if w is not None:
+            _check(lib().moe_read_device_status(w.ptr, _stream()))
+        ws = _ws(4096)
     _check(lib().moe_read_device_status(ws.ptr, _stream()))
 
 
@@ -546,7 +568,7 @@ def moe_adapter_add(x, y, a, b, scale, seg_offsets, seg_adapter, out=None, ws=No
     """y + scale[i] * (x A_i^T) B_i^T per request, i its adapter (-1: y alone). x bf16 [T, K]; y bf16 [T, N];
     a bf16 [n, r, K]; b bf16 [n, N, r]; scale fp32 [n]; request s has the rows seg_offsets[s] ..
     seg_offsets[s + 1] (int32 [S + 1]) and the adapter seg_adapter[s] (int32 [S]). out: optional, may be y.
-    x, y and out may have strided rows."""
+    x, y and out may have strided rows. Requests that break the rules are reported by moe_read_device_status(ws)."""
     if out is None:
         out = torch.empty(y.shape, dtype=_BF16, device=y.device)
     if _lib is None:
@@ -554,7 +576,7 @@ def moe_adapter_add(x, y, a, b, scale, seg_offsets, seg_adapter, out=None, ws=No
     status = -1
     if x.is_cuda:
         if ws is None:
-            ws = _ws(4096)
+            ws = _adapter_workspace()
         if _calls is not None:
             status = _calls.adapter_add(x, y, a, b, scale, seg_offsets, seg_adapter, out, ws.address, ws.nbytes, _stream())
     if status < 0:
