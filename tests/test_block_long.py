@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from test_block_ops import BF, adapter_case, gen, moe, randn  # noqa: F401
+from test_block_ops import BF, adapter_case, check_adapter, gen, moe, randn  # noqa: F401
 from test_block_refusals import FakeTensor, m  # noqa: F401
 
 
@@ -88,3 +88,10 @@ def test_norms_of_a_long_batch(moe):  # noqa: F811
     for rows in (slice(0, 400), slice(262144 - 200, 262144 + 200), slice(T - 400, T)):  # 262,144 rows are 2^31 elements
         want = moe.moe_norm_residual(y[rows], r[rows], w_post=w, w_pre=w)
         assert torch.equal(got[0][rows], want[0]) and torch.equal(got[1][rows], want[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,r,K,N", [([5, 1], 128, 16384, 16384), ([700, 300], 128, 16384, 1024), ([5000], 64, 1024, 16384),
+                                        ([70, 50, 33] * 27, 40, 16384, 520)])
+def test_adapters_of_the_largest_widths(moe, lens, r, K, N):  # noqa: F811
+    check_adapter(moe, adapter_case(lens, [i % 2 for i in range(len(lens))], 2, r, K, N))
