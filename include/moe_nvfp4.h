@@ -307,8 +307,11 @@ moe_status_t moe_norm_residual(const moe_norm_t* N, const uint16_t* y, int64_t l
  *   with such a logit, or whose c is -inf or NaN, is masked: it adds nothing to its group's value
  *   (a group of masked experts alone comes last) and is chosen only after all others of the groups
  *   that stay (lowest id first), with weight 0.
- *   ids are those of exact arithmetic: values are compared in FP32 with a bound on their error, and
- *   a token with two values nearer than that is decided again in FP64.
+ *   ids are those of 64-bit arithmetic: values are compared in FP32 with a bound on their error, and
+ *   a token with two values nearer than that is decided again in FP64. Values that differ by less
+ *   than the rounding there (some 1e-15 of the largest) may go either way, the same way at every
+ *   call; equal ones (sigmoid scores of logits past 37 are all 1) count as equal. Without a bias the
+ *   logits order the experts, exactly.
  *   logits: logits_dtype (MOE_DTYPE_*) [T][E], rows ld >= E elements apart, naturally aligned;
  *   topk_ids: int32 [T][k]; topk_w: FP32 [T][k]. 1 <= E <= 1024, 1 <= k <= 32, 1 <= n_group <= 32
  *   dividing E, 1 <= topk_group <= n_group, k <= topk_group * (E / n_group). T = 0 returns MOE_OK

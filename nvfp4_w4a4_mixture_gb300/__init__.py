@@ -219,7 +219,8 @@ def _adapter_workspace():
 
 def moe_set_wait_test_hook(ws, wait_limit_us, ready_extra):
     """Test hook: the expert GEMMs' wait for a token block's intermediate gives up after
-    wait_limit_us (0: default) and needs ready_extra more completions (0: none); (0, 0) restores."""
+    wait_limit_us (0: default) and needs ready_extra more completions (0: none); with more than none,
+    moe_adapter_add's wait for A x (long requests) runs out too. (0, 0) restores."""
     _check(lib().moe_set_wait_test_hook(ws.ptr, int(wait_limit_us), int(ready_extra), _stream()))
 
 

@@ -13,8 +13,8 @@
 // quarter each) take phase 2's slices in turn: they read an accumulator, add y from the ring's buffer
 // and store rows.
 // Bounded by memory where the batch fills the multiprocessors (16,384 tokens of 24 requests, rank 64,
-// 2048 x 2048: 37.5 us, 5.5 TB/s, 82 % of what a copy reaches), else by the chain of one tile (4,113
-// tokens of 77 requests, rank 40, 2056 x 1032: 17.0 us, 141 CTAs).
+// 2048 x 2048: 38.0 us, 5.4 TB/s, 81 % of what a copy reaches), else by the chain of one tile (4,113
+// tokens of 77 requests, rank 40, 2056 x 1032: 17.1 us, 141 CTAs).
 // Rows of a tile beyond its request's end hold whatever the buffers held; rows do not mix, and those
 // are not stored. The zero fill of TMA pads K, N and the rank.
 #include "adapters.cuh"
@@ -395,7 +395,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         // y has to be in all lanes' registers before the stage goes back, or its next fill may be read: the
                         // arrival's address takes a zero from the loaded values, one that the compiler cannot know. (A fence
-                        // would wait for the rows that were stored a slice ago, too.)
+                        // would wait for the rows that were stored a slice ago, too.) Without it, 1 % of runs had 16-byte
+                        // pieces of the stage's next fill.
                         const uint32_t zero = __reduce_or_sync(0xFFFFFFFFu, seen) & static_cast<uint32_t>(p.zero);
                         if (lane == 0) {
                             ptx::mbar_arrive(&st.empty[s + zero]);

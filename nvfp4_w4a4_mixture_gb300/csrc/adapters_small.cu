@@ -12,8 +12,8 @@
 //            sums are added at the end), columns on N. Column 2q + e of product i stands for column 8q + 2i
 //            + e of 32, so that a thread ends with eight neighbouring columns of a row: one 16-byte load of
 //            y and one store of out. Ranks up to 16 take 8 bytes a thread and one product of 16.
-// Measured, 2048 x 2048: 256 requests of one token, rank 32 10.3 us (52 MB of A and B from L2, 5 TB/s);
-// 4 tokens, rank 16 4.2 us, the chain of one tile.
+// Measured, 2048 x 2048: 256 requests of one token, rank 32 10.2 us (52 MB of A and B from L2, 5 TB/s);
+// 4 tokens, rank 16 4.3 us, the chain of one tile.
 #include "adapters.cuh"
 
 namespace moe {

@@ -10,15 +10,16 @@
 //   choice   the lane maxima are sorted across the lanes; the (k + 1)-th is a lower bound of the
 //            (k + 1)-th largest value, and the few values that reach it are compacted into a list
 //            and ranked by (c descending, id ascending)
-//   exact    where two neighbours of the ranking, or the last group that stays and the first that
-//            goes, are nearer than their errors, the candidates are ranked again in FP64
-//            (exact_ranking, exact_groups). Only the values that can matter are computed again
+//   exact    where two neighbours of the ranking, or a group that stays and one that goes, are nearer
+//            than their errors, the candidates or the groups are ranked again in FP64 (exact_ranking,
+//            exact_groups). Only the values that can matter are computed again
 //   others   rows with fewer unmasked experts than k, more candidates than the list holds (many equal
 //            logits) or logits of +inf (whole_row)
-// The weights are computed from the chosen logits alone.
+// The weights are computed from the chosen logits alone, in FP32 as they are returned (off by an ulp or two: 7e-8 of
+// their norm over 16,384 tokens, where one rounding from FP64 gives 3e-8).
 // Bounded by instruction issue (70 % of the slots): the steps across lanes cost what they cost for one
-// token or for two. Measured: 16,384 x 512, bias and 4 of 8 groups 26.0 us (1.34 TB/s; 1,145 warp
-// instructions a token), without both 12.4; 12,365 x 160, 3 of 8 groups 8.5; 2048 x 512 3.1; 4 x 512 3.0.
+// token or for two. Measured: 16,384 x 512, bias and 4 of 8 groups 24.7 to 26.0 us by the set of logits (1.4
+// TB/s; 1,162 warp instructions a token), without both 12.4; 12,365 x 160, 3 of 8 groups 8.5; 2048 x 512 3.1; 4 x 512 3.0.
 #include <cfloat>
 
 #include "block.cuh"
@@ -38,7 +39,7 @@ constexpr unsigned kFull = 0xFFFFFFFFu;
 // 8e-8 in all), the sum and rcp.approx add 2^-24 and 2^-23: 2.6e-7, taken as 6e-7. Softmax: a term's
 // own error is at most 2.6e-7 of the largest; the sum of up to 1024 terms, 37 roundings deep, is off
 // by 3.3e-6, a factor that all scores of the row share: two of them compare within 3.8e-6, two pairs
-// within 7.6e-6, taken as 2 and 4 times 2.5e-6.
+// within 7.6e-6, taken as 2 and 4 times 2.5e-6 (for groups without a bias too, which share no factor).
 constexpr float kEpsSigmoid = 6e-7f, kEpsSoftmax = 2.5e-6f, kEpsAdd = 6e-8f;
 
 __device__ __forceinline__ bool ahead(double c, int e, double d, int f) { return c > d || (c == d && e < f); }
@@ -127,7 +128,8 @@ __device__ __noinline__ unsigned exact_groups(const SelectArgs& a, int64_t t, co
     const float margin = a.bias ? 2.0f * (eps_score + kEpsAdd * fmaxf(fabsf(top), fabsf(v2))) : 0.0f;
     const bool real = g < a.n_group;
     const float thr = v2 < INFINITY ? v2 - margin : v2;  // -inf where the group has one unmasked expert or none
-    uint64_t hits = 0;              // this lane's values: j, j + per, ... (at most 43 of them)
+    // this lane's values: j, j + per, ...; fewer than 64, since size <= 1024 / n_group and per > 16 / n_group
+    uint64_t hits = 0;
     if (real)
         for (int i = 0; (i << lg) + j < size; ++i) {
             const float v = c_s[g * size + (i << lg) + j];
@@ -556,7 +558,8 @@ __global__ void __launch_bounds__(kWarps * 32, kNper < 8 || (kL == 32 && kNper <
         C = 0;
         mine = 0;
     }
-    // Straight-line stores: as a loop over a lane's bits, nvcc 13.0 ran the body once for lanes without any.
+    // Straight-line stores: a loop over a lane's bits was 1 us faster for 16,384 x 512, but where a lane has two slots it
+    // left candidates of lanes without a bit in the list; why was not found.
     Cand* list = cand + pos;
 #pragma unroll
     for (int i = 0; i < kNper; ++i)
