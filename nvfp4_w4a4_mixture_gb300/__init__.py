@@ -553,6 +553,8 @@ def moe_select_experts(logits, k, bias=None, score=SCORE_SOFTMAX, n_group=1, top
         status = _calls.select_experts(logits, k, bias, score, n_group, topk_group, group_score, renormalize, scale, ids, w,
                                        _stream())
     if status < 0:
+        if any(not -_INT_MAX <= v <= _INT_MAX for v in (k, score, n_group, topk_group, group_score)):
+            raise ValueError("k, score, n_group, topk_group and group_score are ints of 32 bits")
         T, E = logits.shape
         lt = logits.dtype
         l_ptr, l_ld = _rows(logits, "logits", _F32 if lt is _F32 else _BF16, (T, E))

@@ -66,7 +66,12 @@ static PyObject* leave(void)
 }
 
 /* numbers among the arguments; an error of their conversion is looked for once */
-static long as_int(PyObject* v) { return PyLong_AsLong(v); }
+static int as_int(PyObject* v)
+{
+    const long i = PyLong_AsLong(v);
+    if (i != (int)i) PyErr_SetString(PyExc_OverflowError, "an int of more than 32 bits");
+    return (int)i;
+}
 static float as_float(PyObject* v) { return (float)PyFloat_AsDouble(v); }
 
 /* norm_residual(y, residual, w_post, w_pre, gate, residual_scale, eps, w_offset, residual_out, x_out, stream) */
@@ -138,7 +143,7 @@ static PyObject* select_experts(PyObject* self, PyObject* const* a, Py_ssize_t n
     lt = dtype_of(a[0]);
     if (lt < 0 || lt > 1 || !whole(a[0], 2, rows, &l)) return leave();
     d.E = (int)rows[1];
-    d.k = (int)as_int(a[1]);
+    d.k = as_int(a[1]);
     out[0] = rows[0];
     out[1] = d.k;
     if (d.k < 1 || dtype_of(a[9]) != 2 || !whole(a[9], 2, out, &ids) || dtype_of(a[10]) != 1 || !whole(a[10], 2, out, &w)) return leave();
@@ -147,10 +152,10 @@ static PyObject* select_experts(PyObject* self, PyObject* const* a, Py_ssize_t n
         if (dtype_of(a[2]) != 1 || !whole(a[2], 1, cols, &p)) return leave();
         d.bias = p;
     }
-    d.score = (int)as_int(a[3]);
-    d.n_group = (int)as_int(a[4]);
-    d.topk_group = (int)as_int(a[5]);
-    d.group_score = (int)as_int(a[6]);
+    d.score = as_int(a[3]);
+    d.n_group = as_int(a[4]);
+    d.topk_group = as_int(a[5]);
+    d.group_score = as_int(a[6]);
     d.renormalize = PyObject_IsTrue(a[7]);
     d.scale = as_float(a[8]);
     p = PyLong_AsVoidPtr(a[11]);
