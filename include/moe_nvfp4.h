@@ -273,7 +273,7 @@ moe_status_t moe_layer_forward_host(const moe_layer_t* L, const uint16_t* x, int
  *   y (the same address and row stride), no other overlap (other columns of one buffer are apart).
  *   An empty batch (T = 0) returns MOE_OK after the shape check.
  * ------------------------------------------------------------------------------------------- */
-enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1 };
+enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1, MOE_DTYPE_E4M3 = 2 };
 
 typedef struct {
     int H;
@@ -361,6 +361,118 @@ moe_status_t moe_adapter_add(const moe_adapters_t* A, const uint16_t* x, int64_t
                              const int32_t* seg_offsets, const int32_t* seg_adapter, int S, const uint16_t* y,
                              int64_t ld_y, uint16_t* out, int64_t ld_out, void* ws, size_t ws_bytes,
                              moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * The attention half of a block, around a paged cache of keys and values.
+ *
+ * moe_kv_cache_t: n_pages pages of page_size slots (a power of two, at most 65,536), each slot with n_kv heads of D
+ *   elements (D = 64, 128 or 256), keys and values apart, in bf16 or E4M3. Element c of head h of a page's slot is at
+ *   page * ld_page + slot * ld_slot + h * ld_head + c (elements, the same for k and v; every head starts on 16 bytes).
+ *   k_scale, v_scale (E4M3): FP32 [n_kv], a value is code * scale; NULL: 1.
+ *
+ * moe_requests_t: the T rows of a batch are the requests' new tokens one request after the other: request s has the
+ *   rows [seg_offsets[s], seg_offsets[s+1]) (none, one or many) and kv_len[s] tokens with them, so its row i is at
+ *   position kv_len[s] - n + i. Position p is in slot p % page_size of page pages[s * ld_pages + p / page_size].
+ *   seg_offsets[0] = 0, non-decreasing, seg_offsets[S] <= T: rows behind the last request are left as they were.
+ *   A row at a negative position (kv_len < n, for example an idle slot of a batch with kv_len 0) has no place in the
+ *   cache. What breaks these rules (offsets out of order or past T, kv_len < 0 or past max_pages * page_size) is
+ *   skipped, its rows left as they were; moe_read_device_status reports it as MOE_ERR_INVALID_ARG. A page outside
+ *   [0, n_pages) is reported likewise; nothing is written there, and its tokens read as zeros.
+ *   All of it is read on the device: a captured call follows what the tables hold when it is replayed.
+ * ------------------------------------------------------------------------------------------- */
+typedef struct {
+    int dtype;              /* MOE_DTYPE_BF16 or MOE_DTYPE_E4M3 */
+    int n_pages, page_size, n_kv, D;
+    void *k, *v;
+    int64_t ld_page, ld_slot, ld_head;
+    const float *k_scale, *v_scale; /* nullable, FP32 [n_kv] (E4M3) */
+} moe_kv_cache_t;
+
+typedef struct {
+    int S, max_pages;
+    const int32_t* seg_offsets; /* [S+1] */
+    const int32_t* kv_len;      /* [S] */
+    const int32_t* pages;       /* [S] rows of max_pages ids, ld_pages elements apart */
+    int64_t ld_pages;
+} moe_requests_t;
+
+/* ---------------------------------------------------------------------------------------------
+ * moe_cache_append -- what lies between the projection to queries, keys and values and the attention, in one launch:
+ *   the norm of every query and key head, the rotation by the token's position, and the append of keys and values
+ *   to the cache. Per row at position p and head (q with w_q, k with w_k):
+ *     u   = x * rsqrt(mean_c(x_c^2) + eps) * (w_offset + w)      (u = x when w is NULL)
+ *     the rot first elements are turned in pairs (a, b) = (u_i, u_{i + rot/2}), or (u_2i, u_2i+1) with interleaved:
+ *     (a cos - b sin, a sin + b cos), angle p * inv_freq[i], i < rot/2; the others stay
+ *   in FP32, rounded once: q_out = bf16, keys to the cache's type; values go there as they are. E4M3: the nearest code
+ *   of x / scale, saturating at 448. Angles are exact to 2^-30 turns at any position.
+ *   q: bf16 [T][n_q][D], k and v: bf16 [T][n_kv][D]; ld_*: elements between two tokens, heads contiguous, every row on
+ *   16 bytes (the three may be columns of one buffer). q_out: bf16 [T][n_q][D], may be q (the same address and row
+ *   stride), no other overlap. n_q = 0: keys and values alone (q and q_out NULL). rot: a multiple of 16 in [0, D].
+ *   1 <= n_kv <= 1024, n_q <= 1024. Two rows with one place in the cache (a page shared by requests that both write
+ *   to it) leave either's values there.
+ *   ws: >= 256 bytes (status word). T = 0 returns MOE_OK after the shape check.
+ * ------------------------------------------------------------------------------------------- */
+typedef struct {
+    int n_q, rot, interleaved;
+    const float* inv_freq;  /* FP32 [rot / 2], finite; NULL exactly when rot is 0 */
+    const uint16_t* w_q;    /* nullable, bf16 [D] */
+    const uint16_t* w_k;    /* nullable, bf16 [D] */
+    float eps;              /* >= 0 */
+    float w_offset;
+} moe_rotary_t;
+
+moe_status_t moe_cache_append(const moe_kv_cache_t* C, const moe_requests_t* R, const moe_rotary_t* P, const uint16_t* q,
+                              int64_t ld_q, const uint16_t* k, int64_t ld_k, const uint16_t* v, int64_t ld_v, int T,
+                              uint16_t* q_out, int64_t ld_q_out, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * moe_paged_attention -- attention of a few new tokens of every request (a decode step, a verify window) over its
+ *   cache, the new tokens themselves among it. Row at position p, query head j, its key head h = j / (n_q / n_kv):
+ *     out = sum_t softmax_t(scale * q . k_t) v_t    over 0 <= t <= p, with a window over p - window < t <= p
+ *     lse = log sum_t exp(scale * q . k_t)          (natural logarithm)
+ *   A row that sees nothing (a negative position) has out = 0 and lse = -inf. Sums are FP32; the weights are held in 16
+ *   significant bits or more (bf16 cache) or 11 (E4M3) for the second product. What lies behind a request's
+ *   last token or outside a row's window takes no part, whatever its bits.
+ *   q, out: bf16 [T][n_q][D], ld_*: elements between two tokens, every row on 16 bytes; out may be q (the same
+ *   address and row stride), no other overlap. lse: nullable, FP32 [T][n_q]. n_q a multiple of n_kv, n_q / n_kv <= 64.
+ *   max_new in [1, 16]: the most rows of a request; a request of more is skipped and reported. window: 0 for none.
+ *   The cache's length is split over the multiprocessors, the parts joined in a second launch in a fixed order.
+ *   ws: >= moe_attention_workspace_bytes(S, n_q, n_kv, D, max_new). T = 0 returns MOE_OK after the shape check.
+ * ------------------------------------------------------------------------------------------- */
+typedef struct {
+    int n_q, max_new, window;
+    float scale;            /* finite */
+} moe_attention_t;
+
+moe_status_t moe_paged_attention(const moe_kv_cache_t* C, const moe_requests_t* R, const moe_attention_t* A,
+                                 const uint16_t* q, int64_t ld_q, int T, uint16_t* out, int64_t ld_out, float* lse, void* ws,
+                                 size_t ws_bytes, moe_stream_t stream);
+
+/* Workspace bytes for moe_paged_attention with these sizes on the current device; 0 for sizes that it refuses. */
+size_t moe_attention_workspace_bytes(int S, int n_q, int n_kv, int D, int max_new);
+
+/* ---------------------------------------------------------------------------------------------
+ * moe_quantize_fp8 -- FP8 encoding of activations with a scale for each 128 elements of a row:
+ *   scale[t][b] = amax_b / 448 (1 where amax is 0), code = E4M3 nearest-even of x / scale; each step is rounded to FP32
+ *   (results are bit-exact). A block with a NaN has a scale and codes of NaN; one with an infinity has the scale infinity,
+ *   codes of NaN for its infinities and 0 for the others.
+ *   x: bf16 [T][K], rows ld_x elements apart, every row on 16 bytes; codes: E4M3 [T][K]; scale: FP32 [T][ceil(K / 128)].
+ *   K a multiple of 16 in [16, 65536]; the last block of a row may be short. T = 0 returns MOE_OK after the shape check.
+ * ------------------------------------------------------------------------------------------- */
+moe_status_t moe_quantize_fp8(const uint16_t* x, int64_t ld_x, int T, int K, uint8_t* codes, float* scale,
+                              moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * moe_gemm_fp8 -- matrix product in FP8 with a scale for each block of 128, for the projections beside the NVFP4 experts:
+ *   out[t][n] = sum_b a_scale[t][b] b_scale[n / 128][b] sum_{k in block b} a[t][k] b[n][k]
+ *   a: E4M3 [T][K], a_scale: FP32 [T][ceil(K / 128)] (moe_quantize_fp8's outputs); b: E4M3 [N][K], b_scale: FP32
+ *   [ceil(N / 128)][ceil(K / 128)]. A block's products are summed in FP32 by the tensor cores, the blocks' sums are
+ *   scaled and added in FP32. out: out_dtype (MOE_DTYPE_BF16 or MOE_DTYPE_F32) [T][N], rows ld_out elements apart, every
+ *   row on 16 bytes; it overlaps no input. K a multiple of 16 in [16, 65536], N a multiple of 8 in [8, 1048576]; the
+ *   last blocks may be short. ws: >= 256 bytes (status word). T = 0 returns MOE_OK after the shape check.
+ * ------------------------------------------------------------------------------------------- */
+moe_status_t moe_gemm_fp8(const uint8_t* a, const float* a_scale, const uint8_t* b, const float* b_scale, int T, int N, int K,
+                          void* out, int out_dtype, int64_t ld_out, void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------------
  * moe_route_topk_noalloc -- moe_route_topk for callers that cannot give the library scratch

@@ -19,7 +19,7 @@ CALLS_PATH = os.path.join(_HERE, "_lib", "_calls" + sysconfig.get_config_var("EX
 EPI_F32, EPI_BF16, EPI_SWIGLU_NVFP4 = 0, 1, 2
 SCHED_AUTO, SCHED_ACT_ON_M, SCHED_WEIGHTS_ON_M, SCHED_WIDE, SCHED_WIDE_ROWS = 0, 0x100, 0x200, 0x400, 0x800
 SCHED_WEIGHTS_RESIDENT = 0x1000
-DTYPE_BF16, DTYPE_F32 = 0, 1
+DTYPE_BF16, DTYPE_F32, DTYPE_E4M3 = 0, 1, 2
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 GROUP_MAX, GROUP_TOP2 = 0, 1
 
@@ -29,6 +29,7 @@ ENTRY_POINTS = (
     "moe_read_device_status", "moe_status_string", "moe_last_error_detail", "moe_route_topk_noalloc",
     "moe_layer_forward_host", "moe_workspace_bytes_host", "moe_layer_workspace_view",
     "moe_set_wait_test_hook", "moe_norm_residual", "moe_select_experts", "moe_adapter_add",
+    "moe_cache_append", "moe_paged_attention", "moe_attention_workspace_bytes", "moe_quantize_fp8", "moe_gemm_fp8",
 )
 
 
@@ -71,6 +72,26 @@ class RoutingDesc(ctypes.Structure):
 class AdaptersDesc(ctypes.Structure):
     _fields_ = [("n", ctypes.c_int), ("r", ctypes.c_int), ("K", ctypes.c_int), ("N", ctypes.c_int),
                 ("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
+class KvCacheDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("n_kv", ctypes.c_int),
+                ("D", ctypes.c_int), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("ld_page", ctypes.c_int64),
+                ("ld_slot", ctypes.c_int64), ("ld_head", ctypes.c_int64), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class RequestsDesc(ctypes.Structure):
+    _fields_ = [("S", ctypes.c_int), ("max_pages", ctypes.c_int), ("seg_offsets", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("pages", ctypes.c_void_p), ("ld_pages", ctypes.c_int64)]
+
+
+class RotaryDesc(ctypes.Structure):
+    _fields_ = [("n_q", ctypes.c_int), ("rot", ctypes.c_int), ("interleaved", ctypes.c_int), ("inv_freq", ctypes.c_void_p),
+                ("w_q", ctypes.c_void_p), ("w_k", ctypes.c_void_p), ("eps", ctypes.c_float), ("w_offset", ctypes.c_float)]
+
+
+class AttentionDesc(ctypes.Structure):
+    _fields_ = [("n_q", ctypes.c_int), ("max_new", ctypes.c_int), ("window", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
 _lib = None
@@ -144,6 +165,17 @@ def lib():
         L.moe_select_experts.argtypes = [ctypes.POINTER(RoutingDesc), vp, i32, i64, i32, vp, vp, vp]
         L.moe_adapter_add.restype = i32
         L.moe_adapter_add.argtypes = [ctypes.POINTER(AdaptersDesc), vp, i64, i32, vp, vp, i32, vp, i64, vp, i64, vp, sz, vp]
+        cache, requests = ctypes.POINTER(KvCacheDesc), ctypes.POINTER(RequestsDesc)
+        L.moe_cache_append.restype = i32
+        L.moe_cache_append.argtypes = [cache, requests, ctypes.POINTER(RotaryDesc), vp, i64, vp, i64, vp, i64, i32, vp, i64, vp, sz, vp]
+        L.moe_paged_attention.restype = i32
+        L.moe_paged_attention.argtypes = [cache, requests, ctypes.POINTER(AttentionDesc), vp, i64, i32, vp, i64, vp, vp, sz, vp]
+        L.moe_attention_workspace_bytes.restype = sz
+        L.moe_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+        L.moe_quantize_fp8.restype = i32
+        L.moe_quantize_fp8.argtypes = [vp, i64, i32, i32, vp, vp, vp]
+        L.moe_gemm_fp8.restype = i32
+        L.moe_gemm_fp8.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, i32, i64, vp, sz, vp]
         _load_calls(L)
         _lib = L
     return _lib
@@ -227,9 +259,10 @@ def moe_set_wait_test_hook(ws, wait_limit_us, ready_extra):
 def moe_read_device_status(ws=None):
     """Raises what the calls on the workspace have reported since the last reading (None: the default workspaces)."""
     if ws is None:
-        w = _adapter_ws.get(torch.cuda.current_device())
-        if w is not None:
-            _check(lib().moe_read_device_status(w.ptr, _stream()))
+        dev = torch.cuda.current_device()
+        for w in [_adapter_ws.get(dev)] + [w for key, w in _attention_ws.items() if key[0] == dev]:
+            if w is not None:
+                _check(lib().moe_read_device_status(w.ptr, _stream()))
         ws = _ws(4096)
     _check(lib().moe_read_device_status(ws.ptr, _stream()))
 
@@ -596,4 +629,162 @@ def moe_adapter_add(x, y, a, b, scale, seg_offsets, seg_adapter, out=None, ws=No
                                        ws.address, ws.nbytes, _stream())
     if status:
         _check(status)
+    return out
+
+
+_E4M3 = torch.float8_e4m3fn
+
+
+def moe_attention_workspace_bytes(S, n_q, n_kv, D, max_new):
+    return int(lib().moe_attention_workspace_bytes(S, n_q, n_kv, D, max_new))
+
+
+def _heads(t, name, dtype, shape):
+    """(data pointer, elements between two tokens) of a CUDA tensor [T, n, D] whose tokens' heads lie side by side."""
+    if t.dtype is dtype and t.is_cuda and t.shape == shape and shape[0] <= _INT_MAX:
+        s = t.stride()
+        if (shape[2] == 1 or s[2] == 1) and (shape[1] == 1 or s[1] == shape[2]):
+            return t.data_ptr(), s[0]
+    _refuse(t, name, dtype, shape)
+
+
+def _cache_desc(k_cache, v_cache, k_scale, v_scale):
+    shape = k_cache.shape
+    if len(shape) != 4:
+        raise ValueError("k_cache must have shape [n_pages, page_size, n_kv, D], got %s" % (tuple(shape),))
+    dt = k_cache.dtype
+    if dt is not _BF16 and dt is not _E4M3:
+        raise TypeError("k_cache must be bf16 or float8_e4m3fn, got %s" % dt)
+    if v_cache.dtype is not dt or v_cache.shape != shape or v_cache.stride() != k_cache.stride():
+        raise ValueError("v_cache must have k_cache's type, shape and strides")
+    if not k_cache.is_cuda or not v_cache.is_cuda:
+        raise TypeError("k_cache and v_cache must be CUDA tensors")
+    s = k_cache.stride()
+    if s[3] != 1 or max(shape) > _INT_MAX:
+        raise ValueError("the elements of a cached head must lie side by side, fewer than 2^31 of each dimension")
+    n_kv = shape[2]
+    return KvCacheDesc(DTYPE_BF16 if dt is _BF16 else DTYPE_E4M3, shape[0], shape[1], n_kv, shape[3], k_cache.data_ptr(), v_cache.data_ptr(),
+                       s[0], s[1], s[2], None if k_scale is None else _whole(k_scale, "k_scale", _F32, (n_kv,)),
+                       None if v_scale is None else _whole(v_scale, "v_scale", _F32, (n_kv,)))
+
+
+def _requests_desc(seg_offsets, kv_len, pages):
+    S = kv_len.shape[0]
+    if len(pages.shape) != 2:
+        raise ValueError("pages must have shape [S, max_pages], got %s" % (tuple(pages.shape),))
+    p_ptr, p_ld = _rows(pages, "pages", _I32, (S, pages.shape[1]))
+    return RequestsDesc(S, pages.shape[1], _whole(seg_offsets, "seg_offsets", _I32, (S + 1,)), _whole(kv_len, "kv_len", _I32, (S,)), p_ptr, p_ld)
+
+
+def moe_cache_append(q, k, v, k_cache, v_cache, seg_offsets, kv_len, pages, inv_freq=None, interleaved=False, w_q=None,
+                     w_k=None, eps=1e-6, w_offset=0.0, k_scale=None, v_scale=None, out=None, ws=None):
+    """Norm (w_q, w_k) and rotation (inv_freq) of new tokens' queries and keys, and the append of keys and values to a
+    paged cache; returns the queries (None without q).
+
+    q: bf16 [T, n_q, D] or None; k, v: bf16 [T, n_kv, D] (tokens may be strided: columns of one buffer); k_cache,
+    v_cache: bf16 or float8_e4m3fn [n_pages, page_size, n_kv, D], strided as they like, heads contiguous; request s has
+    the rows seg_offsets[s] .. seg_offsets[s + 1] (int32 [S + 1]), with them kv_len[s] tokens (int32 [S]) in the pages
+    pages[s] (int32 [S, max_pages]). inv_freq: fp32 [rot / 2]; w_q, w_k: bf16 [D]; k_scale, v_scale: fp32 [n_kv] of an
+    8-bit cache. out: optional, may be q. Requests that break the rules are reported by moe_read_device_status(ws)."""
+    if _lib is None:
+        lib()
+    T, n_kv, D = k.shape
+    k_ptr, k_ld = _heads(k, "k", _BF16, (T, n_kv, D))
+    v_ptr, v_ld = _heads(v, "v", _BF16, (T, n_kv, D))
+    n_q, q_ptr, q_ld, o_ptr, o_ld = 0, None, 0, None, 0
+    if q is not None:
+        n_q = q.shape[1]
+        q_ptr, q_ld = _heads(q, "q", _BF16, (T, n_q, D))
+        if out is None:
+            out = torch.empty(T, n_q, D, dtype=_BF16, device=q.device)
+        o_ptr, o_ld = _heads(out, "out", _BF16, (T, n_q, D))
+    elif out is not None:
+        raise ValueError("out without q")
+    if k_cache.shape[2:] != (n_kv, D):
+        raise ValueError("k_cache of %s for k of %s" % (tuple(k_cache.shape), tuple(k.shape)))
+    half = 0 if inv_freq is None else inv_freq.shape[0]
+    if half > D:
+        raise ValueError("inv_freq: %d values for D = %d" % (half, D))
+    d = RotaryDesc(n_q, 2 * half, 1 if interleaved else 0, None if inv_freq is None else _whole(inv_freq, "inv_freq", _F32, (half,)),
+                   None if w_q is None else _whole(w_q, "w_q", _BF16, (D,)), None if w_k is None else _whole(w_k, "w_k", _BF16, (D,)),
+                   eps, w_offset)
+    if ws is None:
+        ws = _adapter_workspace()
+    _check(lib().moe_cache_append(_cache_desc(k_cache, v_cache, k_scale, v_scale), _requests_desc(seg_offsets, kv_len, pages), d, q_ptr,
+                                  q_ld, k_ptr, k_ld, v_ptr, v_ld, T, o_ptr, o_ld, ws.address, ws.nbytes, _stream()))
+    return out
+
+
+_attention_ws = {}
+
+
+def _attention_workspace(nbytes):
+    """moe_paged_attention's workspace where the caller gives none: one for each stream, since calls on two streams run
+    at the same time. A capture's belongs to its graph (the memory is the graph's, its report is lost)."""
+    stream = _stream()
+    if torch.cuda.is_current_stream_capturing():
+        return Workspace(nbytes)
+    key = torch.cuda.current_device(), stream
+    w = _attention_ws.get(key)
+    if w is None or w.nbytes < nbytes:
+        old, w = w, Workspace(nbytes)
+        if old is not None:  # what its calls have reported stays readable
+            w.tensor[:4].copy_(old.tensor[:4])
+        _attention_ws[key] = w
+    return w
+
+
+def moe_paged_attention(q, k_cache, v_cache, seg_offsets, kv_len, pages, max_new=1, scale=None, window=0, k_scale=None,
+                        v_scale=None, out=None, lse=None, ws=None):
+    """Attention of the requests' new tokens (at most max_new <= 16 each) over the paged cache that holds them, causal,
+    with a window over the last `window` tokens (0: all): bf16 [T, n_q, D]. Arguments as in moe_cache_append; n_q a
+    multiple of n_kv; scale: 1 / sqrt(D) by default; lse: optional fp32 [T, n_q] for the logarithm of the sums. out:
+    optional, may be q. A row that sees nothing gets 0 (lse: -inf)."""
+    if _lib is None:
+        lib()
+    T, n_q, D = q.shape
+    n_kv = k_cache.shape[2]
+    if k_cache.shape[3] != D:
+        raise ValueError("k_cache of %s for q of %s" % (tuple(k_cache.shape), tuple(q.shape)))
+    q_ptr, q_ld = _heads(q, "q", _BF16, (T, n_q, D))
+    if out is None:
+        out = torch.empty(T, n_q, D, dtype=_BF16, device=q.device)
+    o_ptr, o_ld = _heads(out, "out", _BF16, (T, n_q, D))
+    r = _requests_desc(seg_offsets, kv_len, pages)
+    if ws is None:
+        ws = _attention_workspace(lib().moe_attention_workspace_bytes(r.S, n_q, n_kv, D, max_new))
+    _check(lib().moe_paged_attention(_cache_desc(k_cache, v_cache, k_scale, v_scale), r,
+                                     AttentionDesc(n_q, max_new, window, D ** -0.5 if scale is None else scale), q_ptr, q_ld, T, o_ptr, o_ld,
+                                     None if lse is None else _whole(lse, "lse", _F32, (T, n_q)), ws.address, ws.nbytes, _stream()))
+    return out
+
+
+def moe_quantize_fp8(x, out=None):
+    """x bf16 [T, K] (rows may be strided) -> (codes float8_e4m3fn [T, K], scales fp32 [T, ceil(K / 128)]): a scale for each
+    128 elements of a row. out: optional (codes, scales)."""
+    T, K = x.shape
+    if out is None:
+        out = torch.empty(T, K, dtype=_E4M3, device=x.device), torch.empty(T, (K + 127) // 128, dtype=_F32, device=x.device)
+    x_ptr, x_ld = _rows(x, "x", _BF16, (T, K))
+    _check(lib().moe_quantize_fp8(x_ptr, x_ld, T, K, _whole(out[0], "codes", _E4M3, (T, K)),
+                                  _whole(out[1], "scales", _F32, (T, (K + 127) // 128)), _stream()))
+    return out
+
+
+def moe_gemm_fp8(a, a_scale, b, b_scale, out=None, dtype=torch.bfloat16, ws=None):
+    """a [T, K] times b [N, K] transposed, both float8_e4m3fn with a scale for each block of 128: a_scale fp32
+    [T, ceil(K / 128)] (moe_quantize_fp8's), b_scale fp32 [ceil(N / 128), ceil(K / 128)]. out: optional bf16 or fp32 [T, N], rows
+    may be strided; dtype: the type of one that is allocated."""
+    T, K = a.shape
+    N = b.shape[0]
+    if out is None:
+        out = torch.empty(T, N, dtype=dtype, device=a.device)
+    f32 = out.dtype is _F32
+    o_ptr, o_ld = _rows(out, "out", _F32 if f32 else _BF16, (T, N))
+    if ws is None:
+        ws = _adapter_workspace()
+    kb = (K + 127) // 128
+    _check(lib().moe_gemm_fp8(_whole(a, "a", _E4M3, (T, K)), _whole(a_scale, "a_scale", _F32, (T, kb)), _whole(b, "b", _E4M3, (N, K)),
+                              _whole(b_scale, "b_scale", _F32, ((N + 127) // 128, kb)), T, N, K, o_ptr, DTYPE_F32 if f32 else DTYPE_BF16,
+                              o_ld, ws.address, ws.nbytes, _stream()))
     return out

@@ -12,15 +12,15 @@
 
 #include "../../include/moe_nvfp4.h"
 
+#include "api.cuh"
+#include "attention.cuh"
 #include "block.cuh"
 #include "kernels.cuh"
 
 namespace moe {
 
-namespace {
-
-thread_local std::string g_detail;
-constexpr int kLayerStageEvents = 6;
+static thread_local std::string g_detail;
+static constexpr int kLayerStageEvents = 6;
 
 moe_status_t fail(moe_status_t s, const char* fmt, ...)
 {
@@ -58,6 +58,8 @@ moe_status_t check_device()
     }
     return ok ? MOE_OK : fail(MOE_ERR_UNSUPPORTED_DEVICE, "device is not sm_103");
 }
+
+namespace {
 
 struct WsLayout {
     size_t hdr, amax_slots, topk_ids, topk_w, shared_g, logits, x_codes, x_sf, offsets, perm_src, src_perm, row_token,
@@ -133,6 +135,8 @@ moe_status_t check_layer_shape(int H, int E, int k, int I)
     return MOE_OK;
 }
 
+}  // namespace
+
 moe_status_t check_ws(const void* ws, size_t ws_bytes, size_t need)
 {
     if (!ws) return fail(MOE_ERR_INVALID_ARG, "workspace is NULL");
@@ -140,20 +144,6 @@ moe_status_t check_ws(const void* ws, size_t ws_bytes, size_t need)
     if (ws_bytes < need) return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", ws_bytes, need);
     return MOE_OK;
 }
-
-#define MOE_TRY(x)                              \
-    do {                                        \
-        moe_status_t s_ = (x);                  \
-        if (s_ != MOE_OK) return s_;            \
-    } while (0)
-
-#define MOE_CUDA(x, what)                       \
-    do {                                        \
-        cudaError_t e_ = (x);                   \
-        if (e_ != cudaSuccess) return cuda_fail(e_, what); \
-    } while (0)
-
-}  // namespace
 
 void set_last_error_detail(const char* msg) { g_detail = msg ? msg : ""; }
 
@@ -163,6 +153,35 @@ int device_sm_count()
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     return sms > 0 ? sms : 1;
+}
+
+// Whether the T rows of width_a bytes at a (ld_a bytes apart) and those at b overlap in memory: exactly where
+// both strides are the same (columns of one buffer are apart), else by the spans from the first row to the last.
+bool rows_overlap(const void* a, int64_t ld_a, int64_t width_a, const void* b, int64_t ld_b, int64_t width_b, int T)
+{
+    if (!a || !b || T <= 0) return false;
+    const char *a0 = static_cast<const char*>(a), *b0 = static_cast<const char*>(b);
+    if (a0 >= b0 + (T - 1) * ld_b + width_b || b0 >= a0 + (T - 1) * ld_a + width_a) return false;
+    if (T == 1 || ld_a != ld_b || width_a > ld_a || width_b > ld_a) return true;
+    // b's row j begins d bytes into the row j + q of a's buffer and ends in that row or the next
+    const int64_t off = b0 - a0, q = off >= 0 ? off / ld_a : -((ld_a - 1 - off) / ld_a), d = off - q * ld_a;
+    return (d < width_a && q > -T && q < T) || (d + width_b > ld_a && q + 1 > -T && q + 1 < T);
+}
+
+// The same of the T rows at a and `bytes` bytes at b.
+bool rows_overlap_bytes(const void* a, int64_t ld_a, int64_t width_a, int T, const void* b, int64_t bytes)
+{
+    return a && b && T > 0 && static_cast<const char*>(a) < static_cast<const char*>(b) + bytes &&
+           static_cast<const char*>(b) < static_cast<const char*>(a) + (T - 1) * ld_a + width_a;
+}
+
+// One tensor of rows: base and row stride on 16 bytes, the stride at least a row (T > 1).
+moe_status_t check_rows(const char* name, const void* p, int64_t ld, int64_t width, int elem, int T)
+{
+    if (T > 1 && ld < width) return fail(MOE_ERR_INVALID_ARG, "%s: row stride %lld < row length %lld", name, (long long)ld, (long long)width);
+    if (!aligned(p, 16) || (T > 1 && ld * elem % 16))
+        return fail(MOE_ERR_MISALIGNED, "%s %p with row stride %lld: every row must start on 16 bytes", name, p, (long long)ld);
+    return MOE_OK;
 }
 
 static PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder()
@@ -300,6 +319,10 @@ moe_status_t moe_read_device_status(void* ws, moe_stream_t stream)
     if (status & kDevTimeoutAdapter) return fail(MOE_ERR_DEVICE_TIMEOUT, "device status 0x%x: adapter wait timed out", status);
     if (status & kDevBadSegment)
         return fail(MOE_ERR_INVALID_ARG, "device status 0x%x: seg_offsets or seg_adapter outside its range", status);
+    if (status & kDevTimeoutGemmFp8) return fail(MOE_ERR_DEVICE_TIMEOUT, "device status 0x%x: FP8 GEMM wait timed out", status);
+    if (status & kDevBadRequest)
+        return fail(MOE_ERR_INVALID_ARG, "device status 0x%x: a request's seg_offsets or kv_len outside its range", status);
+    if (status & kDevBadPage) return fail(MOE_ERR_INVALID_ARG, "device status 0x%x: page outside [0, n_pages)", status);
     if (status & kDevBadExpertId) return fail(MOE_ERR_INVALID_ARG, "device status 0x%x: expert id outside [0, E)", status);
     return MOE_OK;
 }
@@ -534,35 +557,6 @@ moe_status_t moe_combine(const uint16_t* y, const float* topk_w, const float* sh
     MOE_TRY(check_device());
     MOE_CUDA(launch_combine(y, topk_w, shared_g, src_perm, T, k, H, residual, out, nullptr, static_cast<cudaStream_t>(stream)),
              "combine launch");
-    return MOE_OK;
-}
-
-// Whether the T rows of width_a bytes at a (ld_a bytes apart) and those at b overlap in memory: exactly where
-// both strides are the same (columns of one buffer are apart), else by the spans from the first row to the last.
-static bool rows_overlap(const void* a, int64_t ld_a, int64_t width_a, const void* b, int64_t ld_b, int64_t width_b, int T)
-{
-    if (!a || !b || T <= 0) return false;
-    const char *a0 = static_cast<const char*>(a), *b0 = static_cast<const char*>(b);
-    if (a0 >= b0 + (T - 1) * ld_b + width_b || b0 >= a0 + (T - 1) * ld_a + width_a) return false;
-    if (T == 1 || ld_a != ld_b || width_a > ld_a || width_b > ld_a) return true;
-    // b's row j begins d bytes into the row j + q of a's buffer and ends in that row or the next
-    const int64_t off = b0 - a0, q = off >= 0 ? off / ld_a : -((ld_a - 1 - off) / ld_a), d = off - q * ld_a;
-    return (d < width_a && q > -T && q < T) || (d + width_b > ld_a && q + 1 > -T && q + 1 < T);
-}
-
-// The same of the T rows at a and `bytes` bytes at b.
-static bool rows_overlap_bytes(const void* a, int64_t ld_a, int64_t width_a, int T, const void* b, int64_t bytes)
-{
-    return a && b && T > 0 && static_cast<const char*>(a) < static_cast<const char*>(b) + bytes &&
-           static_cast<const char*>(b) < static_cast<const char*>(a) + (T - 1) * ld_a + width_a;
-}
-
-// One tensor of rows: base and row stride on 16 bytes, the stride at least a row (T > 1).
-static moe_status_t check_rows(const char* name, const void* p, int64_t ld, int64_t width, int elem, int T)
-{
-    if (T > 1 && ld < width) return fail(MOE_ERR_INVALID_ARG, "%s: row stride %lld < row length %lld", name, (long long)ld, (long long)width);
-    if (!aligned(p, 16) || (T > 1 && ld * elem % 16))
-        return fail(MOE_ERR_MISALIGNED, "%s %p with row stride %lld: every row must start on 16 bytes", name, p, (long long)ld);
     return MOE_OK;
 }
 

@@ -1,0 +1,96 @@
+// attention.cuh -- internal launchers of the attention half of a block: appends to a paged cache with norm and rotation,
+// attention over that cache, FP8 encoding and products (not part of the C ABI).
+#pragma once
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "kernels.cuh"
+
+namespace moe {
+
+// Device status bits of these calls (the workspace header's status word).
+enum : int {
+    kDevBadRequest = 64,       // seg_offsets or kv_len outside its range
+    kDevBadPage = 128,         // a page id outside [0, n_pages)
+    kDevTimeoutGemmFp8 = 256,  // a bounded wait of the FP8 GEMM ran out
+};
+
+struct KvCache {
+    void *k, *v;
+    bool e4m3;
+    int n_pages, page_log2, n_kv, D;
+    int64_t ld_page, ld_slot, ld_head;  // elements
+    const float *k_scale, *v_scale;     // nullable
+};
+
+struct Requests {
+    int S;
+    const int32_t *seg_offsets, *kv_len, *pages;
+    int64_t ld_pages;
+    int64_t max_len;  // max_pages * page_size
+};
+
+struct Request {
+    int beg, n, len;  // first row, rows (0: broken or empty), tokens with them
+};
+
+// Request s of a batch of T rows. bad: it breaks the rules (then it has no rows).
+__device__ __forceinline__ Request load_request(const Requests& r, int s, int T, int max_new, bool& bad)
+{
+    const int beg = __ldg(r.seg_offsets + s), end = __ldg(r.seg_offsets + s + 1), len = __ldg(r.kv_len + s);
+    bad = beg < 0 || beg > end || end > T || (s == 0 && beg != 0) || len < 0 || len > r.max_len || end - beg > max_new;
+    return Request{beg, bad ? 0 : end - beg, len};
+}
+
+// ---- cache_append.cu
+struct AppendArgs {
+    KvCache c;
+    Requests r;
+    int T, n_q, rot;
+    bool interleaved;
+    const float* inv_freq;
+    const uint16_t *w_q, *w_k;  // nullable
+    float eps, w_offset;
+    const uint16_t *q, *k, *v;
+    int64_t ld_q, ld_k, ld_v;
+    uint16_t* q_out;
+    int64_t ld_q_out;
+    int* status;
+};
+cudaError_t launch_cache_append(const AppendArgs& a, int sms, cudaStream_t stream);
+
+// ---- paged_attention.cu
+struct AttentionArgs {
+    KvCache c;
+    Requests r;
+    int T, n_q, group, max_new, window;
+    float scale;
+    const uint16_t* q;
+    int64_t ld_q;
+    uint16_t* out;
+    int64_t ld_out;
+    float* lse;       // nullable
+    int64_t* prefix;  // [S + 1] units before each request (workspace)
+    float* part;      // partial sums (workspace)
+    float* part_ml;   // their maxima and weights (workspace)
+    int* status;
+};
+size_t attention_workspace_bytes(int S, int n_q, int n_kv, int D, int max_new, int sms);
+cudaError_t launch_paged_attention(AttentionArgs a, void* ws, int sms, cudaStream_t stream);
+
+// ---- quantize_fp8.cu
+cudaError_t launch_quantize_fp8(const uint16_t* x, int64_t ld_x, int T, int K, uint8_t* codes, float* scale, int sms, cudaStream_t stream);
+
+// ---- gemm_fp8.cu
+struct GemmFp8Args {
+    int T, N, K;
+    const uint8_t *a, *b;
+    const float *a_scale, *b_scale;
+    void* out;
+    bool out_f32;
+    int64_t ld_out;
+    int* status;
+};
+cudaError_t launch_gemm_fp8(const GemmFp8Args& a, int sms, cudaStream_t stream);
+
+}  // namespace moe

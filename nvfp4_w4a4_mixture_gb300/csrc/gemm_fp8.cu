@@ -1,0 +1,506 @@
+// gemm_fp8.cu -- FP8 matrix product with a scale for each block of 128:
+//   out[t][n] = sum_b sa[t][b] sb[n / 128][b] sum_{k in b} a[t][k] b[n][k]
+// tcgen05.mma kind::f8f6f4 sums a block's 128 products in tensor memory (four MMAs of K = 32); the scales are FP32 and
+// differ from block to block, so a block's sum leaves tensor memory and is scaled and added in registers, while the next
+// block's MMAs run into another buffer. Two kernels, by the number of tiles:
+//   k_gemm_fp8       128 tokens x 256 outputs a tile: a lane is a token, its scale one number a block. CTAs stay and
+//                    walk the tiles; two groups of four warps take 128 outputs each.
+//   k_gemm_fp8_few   128 outputs x 16, 32 or 64 tokens a tile (weights on the MMA's M side): few tokens then read each
+//                    weight once without padding; a cluster of CTAs shares a tile's blocks along K and adds the parts
+//                    through distributed shared memory, in the order of their ranks.
+// TMA fills the ragged ends of K, T and N with zeros.
+#include "attention.cuh"
+#include "ptx_cluster.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kSmemMax = 227 * 1024;
+
+// D(tmem, f32) (+)= A(smem, e4m3) * B(smem, e4m3)^T, K = 32
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n"
+        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor, kind::f8f6f4: D f32 [4,6) = 1, A and B E4M3 (format 0), both K-major, N >> 3 at [17,23), M >> 4 at [24,29).
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N)
+{
+    return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// Warp-wide: this warp's 32 lanes x 32 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+
+// Two FP32 sums by one instruction: acc += v * s.
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) { return static_cast<uint64_t>(hi) << 32 | lo; }
+__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t v, uint64_t s) { asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(s)); }
+__device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+
+// ------------------------------------------------------------------------------------------------
+// many tokens
+// ------------------------------------------------------------------------------------------------
+constexpr int kBigM = 128, kBigN = 256, kBigStages = 4, kBigThreads = 320, kEpiWarps = 8;
+constexpr int kBigA = kBigM * 128, kBigStage = kBigA + kBigN * 128;
+
+struct BigTail {
+    uint64_t full[kBigStages], empty[kBigStages], acc_full[2], acc_empty[2], drain;
+    uint32_t tmem;
+    int abort;
+};
+constexpr size_t kBigSmem = 1024 + static_cast<size_t>(kBigStages) * kBigStage + sizeof(BigTail);
+static_assert(kBigSmem <= kSmemMax, "shared memory");
+
+template <bool kF32>
+__global__ void __launch_bounds__(kBigThreads, 1)
+    k_gemm_fp8(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const __grid_constant__ GemmFp8Args p,
+               int n_tiles_n, int n_tiles)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    BigTail& st = *reinterpret_cast<BigTail*>(smem + kBigStages * kBigStage);
+    const int tid = threadIdx.x, warp = __reduce_max_sync(0xFFFFFFFFu, tid / 32), lane = tid % 32;
+    const int nk = (p.K + 127) / 128;
+    if (tid == 0) {
+        for (int s = 0; s < kBigStages; ++s) {
+            ptx::mbar_init(&st.full[s], 1);
+            ptx::mbar_init(&st.empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(&st.acc_full[b], 1);
+            ptx::mbar_init(&st.acc_empty[b], kEpiWarps);
+        }
+        ptx::mbar_init(&st.drain, 1);
+        st.abort = 0;
+        ptx::fence_mbar_init();
+        ptx::prefetch_tmap(&map_a);
+        ptx::prefetch_tmap(&map_b);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(&st.tmem, 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = st.tmem;
+    auto fail = [&]() {
+        if (atomicExch(&st.abort, 1) == 0) record_status(p.status, kDevTimeoutGemmFp8);
+    };
+    auto all = [&](bool got) { return __all_sync(0xFFFFFFFFu, got) != 0; };
+
+    if (warp == 0) {
+        const bool leader = ptx::elect_one();
+        int s = 0;
+        uint32_t ph = 0, fills = 0;
+        bool ok = true;
+        for (int tile = blockIdx.x; ok && tile < n_tiles; tile += gridDim.x) {
+            const int tm = tile / n_tiles_n, tn = tile % n_tiles_n;
+            for (int kb = 0; kb < nk; ++kb) {
+                ok = all(ptx::mbar_wait_near(&st.empty[s], ph ^ 1));
+                if (!ok) break;
+                uint8_t* b = smem + s * kBigStage;
+                if (leader) {
+                    ptx::mbar_arrive_expect_tx(&st.full[s], kBigStage);
+                    ptx::tma_load_3d(b, &map_a, &st.full[s], kb * 128, tm * kBigM, 0);
+                    ptx::tma_load_3d(b + kBigA, &map_b, &st.full[s], kb * 128, tn * kBigN, 0);
+                }
+                ++fills;
+                if (++s == kBigStages) { s = 0; ph ^= 1; }
+            }
+        }
+        if (!ok) fail();
+        if (leader && !ptx::ring_drain(st.full, kBigStages, fills)) fail();
+    } else if (warp == 1) {
+        constexpr uint32_t idesc = idesc_e4m3(kBigM, kBigN);
+        const uint64_t da = ptx::sdesc_sw128(ptx::smem_u32(smem)), db = ptx::sdesc_sw128(ptx::smem_u32(smem + kBigA));
+        const bool leader = ptx::elect_one();
+        int s = 0;
+        uint32_t ph = 0, it = 0;
+        bool ok = true;
+        for (int tile = blockIdx.x; ok && tile < n_tiles; tile += gridDim.x)
+            for (int kb = 0; kb < nk; ++kb, ++it) {
+                const uint32_t buf = it & 1;
+                ok = all(ptx::mbar_wait_near(&st.full[s], ph)) && all(ptx::mbar_wait_near(&st.acc_empty[buf], ((it >> 1) & 1) ^ 1));
+                if (!ok) break;
+                ptx::tc_fence_after();
+                const uint64_t so = static_cast<uint64_t>(s) * (kBigStage >> 4);
+                if (leader) {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) mma_e4m3(tmem + buf * kBigN, da + so + kk * 2, db + so + kk * 2, idesc, kk > 0);
+                    ptx::tc_commit(&st.empty[s]);
+                    ptx::tc_commit(&st.acc_full[buf]);
+                }
+                if (++s == kBigStages) { s = 0; ph ^= 1; }
+            }
+        if (!ok) {
+            fail();
+            if (leader) ptx::tc_commit(&st.drain);  // what was issued ends before the tensor memory goes
+            ptx::mbar_wait(&st.drain, 0);
+        }
+    } else {
+        const int ew = warp - 2, grp = ew / 4, q = warp & 3;
+        const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16) + grp * 128;
+        uint32_t it = 0;
+        bool ok = true;
+        for (int tile = blockIdx.x; ok && tile < n_tiles; tile += gridDim.x) {
+            const int tm = tile / n_tiles_n, tn = tile % n_tiles_n;
+            const int row = tm * kBigM + q * 32 + lane, col = tn * kBigN + grp * 128;
+            const float* sa = p.a_scale + static_cast<int64_t>(min(row, p.T - 1)) * nk;
+            const float* sb = p.b_scale + static_cast<int64_t>(min(col, p.N - 1) / 128) * nk;
+            uint64_t acc[64];
+#pragma unroll
+            for (int i = 0; i < 64; ++i) acc[i] = 0;
+            float f = __ldg(sa) * __ldg(sb);
+            for (int kb = 0; kb < nk; ++kb, ++it) {
+                const uint32_t buf = it & 1;
+                const uint32_t fb = __float_as_uint(f);
+                const uint64_t ff = pair(fb, fb);
+                if (kb + 1 < nk) f = __ldg(sa + kb + 1) * __ldg(sb + kb + 1);
+                ok = all(ptx::mbar_wait_near(&st.acc_full[buf], (it >> 1) & 1));
+                if (!ok) break;
+                ptx::tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t v[32];
+                    tmem_ld32(tq + buf * kBigN + c * 32, v);
+                    ptx::tmem_ld_wait();
+                    if (c == 3) {
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(&st.acc_empty[buf]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) fma2(acc[c * 16 + i], pair(v[2 * i], v[2 * i + 1]), ff);
+                }
+            }
+            if (!ok) break;
+            if (row < p.T) {
+                const int64_t at = static_cast<int64_t>(row) * p.ld_out + col;
+                if constexpr (kF32) {
+                    float* out = static_cast<float*>(p.out) + at;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (col + 4 * i < p.N)
+                            *reinterpret_cast<float4*>(out + 4 * i) = make_float4(lo_of(acc[2 * i]), hi_of(acc[2 * i]), lo_of(acc[2 * i + 1]), hi_of(acc[2 * i + 1]));
+                } else {
+                    uint16_t* out = static_cast<uint16_t*>(p.out) + at;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (col + 8 * i < p.N) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) w[x] = pack_bf16x2(lo_of(acc[4 * i + x]), hi_of(acc[4 * i + x]));
+                            *reinterpret_cast<uint4*>(out + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                }
+            }
+        }
+        if (!ok) fail();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (warp == 1) {
+        __syncwarp();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------------------------------------------
+// few tokens
+// ------------------------------------------------------------------------------------------------
+constexpr int kFewM = 128, kFewThreads = 192, kFewBufs = 4, kChunk = 8;  // kChunk: blocks whose token scales are staged together
+
+template <int kN>
+struct Few {
+    static constexpr int kA = kFewM * 128, kStage = kA + kN * 128;
+    static constexpr int kPart = kN * kFewM * 4;      // the parts of this CTA's share of the tokens
+    static constexpr int kScales = 2 * kChunk * kN * 4;
+    static constexpr int kStages = kN == 64 ? 6 : 5;
+    static constexpr uint32_t kCols = kFewBufs * kN;
+};
+template <int kStages>
+struct FewTail {
+    uint64_t full[kStages], empty[kStages], acc_full[kFewBufs], acc_empty[kFewBufs], drain;
+    uint32_t tmem;
+    int abort;
+};
+template <int kN>
+constexpr size_t few_smem()
+{
+    using S = Few<kN>;
+    constexpr size_t n = 1024 + static_cast<size_t>(S::kStages) * S::kStage + S::kPart + S::kScales + sizeof(FewTail<S::kStages>);
+    static_assert(n <= kSmemMax, "shared memory");
+    return n;
+}
+
+template <int kN, bool kF32>
+__global__ void __launch_bounds__(kFewThreads)
+    k_gemm_fp8_few(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const __grid_constant__ GemmFp8Args p,
+                   int n_tiles_t)
+{
+    using S = Few<kN>;
+    constexpr int kStages = S::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float* const part = reinterpret_cast<float*>(smem + kStages * S::kStage);  // [rank][token of the share][128]
+    float* const scales = part + S::kPart / 4;                                 // [2][kChunk][kN]
+    FewTail<kStages>& st = *reinterpret_cast<FewTail<kStages>*>(scales + S::kScales / 4);
+    const int tid = threadIdx.x, warp = __reduce_max_sync(0xFFFFFFFFu, tid / 32), lane = tid % 32;
+    const int cs = static_cast<int>(ptx::cluster_size()), rank = static_cast<int>(ptx::cluster_rank());
+    const int tile = blockIdx.x / cs, tt = tile % n_tiles_t, tn = tile / n_tiles_t;
+    const int nk = (p.K + 127) / 128, k0 = static_cast<int>(static_cast<int64_t>(nk) * rank / cs), k1 = static_cast<int>(static_cast<int64_t>(nk) * (rank + 1) / cs);
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            ptx::mbar_init(&st.full[s], 1);
+            ptx::mbar_init(&st.empty[s], 1);
+        }
+        for (int b = 0; b < kFewBufs; ++b) {
+            ptx::mbar_init(&st.acc_full[b], 1);
+            ptx::mbar_init(&st.acc_empty[b], 4);
+        }
+        ptx::mbar_init(&st.drain, 1);
+        st.abort = 0;
+        ptx::fence_mbar_init();
+        ptx::prefetch_tmap(&map_a);
+        ptx::prefetch_tmap(&map_b);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(&st.tmem, S::kCols);
+        ptx::tmem_relinquish();
+    }
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (cs > 1) ptx::cluster_arrive_all();  // waited for before the first store to another CTA
+    ptx::tc_fence_after();
+    const uint32_t tmem = st.tmem;
+    auto fail = [&]() {
+        if (atomicExch(&st.abort, 1) == 0) record_status(p.status, kDevTimeoutGemmFp8);
+    };
+    auto all = [&](bool got) { return __all_sync(0xFFFFFFFFu, got) != 0; };
+    bool good = true;
+    float acc[kN];
+
+    if (warp == 0) {
+        const bool leader = ptx::elect_one();
+        int s = 0;
+        uint32_t ph = 0, fills = 0;
+        bool ok = true;
+        for (int kb = k0; kb < k1; ++kb) {
+            ok = all(ptx::mbar_wait_near(&st.empty[s], ph ^ 1));
+            if (!ok) break;
+            uint8_t* b = smem + s * S::kStage;
+            if (leader) {
+                ptx::mbar_arrive_expect_tx(&st.full[s], S::kStage);
+                ptx::tma_load_3d(b, &map_b, &st.full[s], kb * 128, tn * kFewM, 0);
+                ptx::tma_load_3d(b + S::kA, &map_a, &st.full[s], kb * 128, tt * kN, 0);
+            }
+            ++fills;
+            if (++s == kStages) { s = 0; ph ^= 1; }
+        }
+        if (!ok) fail();
+        if (leader && !ptx::ring_drain(st.full, kStages, fills)) fail();
+    } else if (warp == 1) {
+        constexpr uint32_t idesc = idesc_e4m3(kFewM, kN);
+        const uint64_t dw = ptx::sdesc_sw128(ptx::smem_u32(smem)), dx = ptx::sdesc_sw128(ptx::smem_u32(smem + S::kA));
+        const bool leader = ptx::elect_one();
+        int s = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int kb = k0; kb < k1; ++kb) {
+            const uint32_t it = kb - k0, buf = it % kFewBufs;
+            ok = all(ptx::mbar_wait_near(&st.full[s], ph)) && all(ptx::mbar_wait_near(&st.acc_empty[buf], ((it / kFewBufs) & 1) ^ 1));
+            if (!ok) break;
+            ptx::tc_fence_after();
+            const uint64_t so = static_cast<uint64_t>(s) * (S::kStage >> 4);
+            if (leader) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) mma_e4m3(tmem + buf * kN, dw + so + kk * 2, dx + so + kk * 2, idesc, kk > 0);
+                ptx::tc_commit(&st.empty[s]);
+                ptx::tc_commit(&st.acc_full[buf]);
+            }
+            if (++s == kStages) { s = 0; ph ^= 1; }
+        }
+        if (!ok) {
+            fail();
+            if (leader) ptx::tc_commit(&st.drain);  // what was issued ends before the tensor memory goes
+            ptx::mbar_wait(&st.drain, 0);
+        }
+    } else {
+        const int q = warp & 3, et = tid - 64;
+        const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) acc[i] = 0.0f;
+        const float* sb = p.b_scale + static_cast<int64_t>(tn) * nk;
+        for (int kb = k0; kb < k1; ++kb) {
+            const uint32_t it = kb - k0, buf = it % kFewBufs;
+            float* const sc = scales + (it / kChunk & 1) * kChunk * kN;
+            if (it % kChunk == 0) {  // the products of both scales for the next blocks (the other half may still be read)
+                for (int i = et; i < kChunk * kN; i += 128) {
+                    const int t = tt * kN + i / kChunk, b = kb + i % kChunk;
+                    sc[i % kChunk * kN + i / kChunk] = t < p.T && b < k1 ? __ldg(p.a_scale + static_cast<int64_t>(t) * nk + b) * __ldg(sb + b) : 0.0f;
+                }
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+            }
+            good = all(ptx::mbar_wait_near(&st.acc_full[buf], (it / kFewBufs) & 1));
+            if (!good) break;
+            ptx::tc_fence_after();
+            const float4* s4 = reinterpret_cast<const float4*>(sc + it % kChunk * kN);
+#pragma unroll
+            for (int c = 0; c < kN; c += 16) {
+                uint32_t v[16];
+                ptx::tmem_ld16(tq + buf * kN + c, v);
+                ptx::tmem_ld_wait();
+                if (c + 16 == kN) {
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&st.acc_empty[buf]);
+                }
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                    const float4 f = s4[(c + i) / 4];
+                    acc[c + i] = fmaf(__uint_as_float(v[i]), f.x, acc[c + i]);
+                    acc[c + i + 1] = fmaf(__uint_as_float(v[i + 1]), f.y, acc[c + i + 1]);
+                    acc[c + i + 2] = fmaf(__uint_as_float(v[i + 2]), f.z, acc[c + i + 2]);
+                    acc[c + i + 3] = fmaf(__uint_as_float(v[i + 3]), f.w, acc[c + i + 3]);
+                }
+            }
+        }
+        if (!good) fail();
+    }
+    __syncwarp();
+    const int share = kN / cs;  // tokens whose parts this CTA adds
+    const int row = (warp & 3) * 32 + lane, n = tn * kFewM + row;
+    auto store = [&](int c, float v) {
+        const int t = tt * kN + c;
+        if (t >= p.T || n >= p.N) return;
+        const int64_t at = static_cast<int64_t>(t) * p.ld_out + n;
+        if constexpr (kF32) static_cast<float*>(p.out)[at] = v;
+        else static_cast<uint16_t*>(p.out)[at] = static_cast<uint16_t>(pack_bf16x2(v, 0.0f));
+    };
+    if (cs > 1) {
+        ptx::cluster_wait();
+        if (warp >= 2) {
+#pragma unroll
+            for (int c = 0; c < kN; ++c) {
+                const uint32_t to = ptx::cluster_addr(part + (rank * share + c % share) * kFewM + row, c / share);
+                ptx::cluster_store(to, acc[c]);
+            }
+        }
+        ptx::cluster_sync();
+        if (warp >= 2 && !*reinterpret_cast<volatile int*>(&st.abort))
+            for (int c = 0; c < share; ++c) {
+                float v = 0.0f;
+                for (int r = 0; r < cs; ++r) v += part[(r * share + c) * kFewM + row];
+                store(rank * share + c, v);
+            }
+    } else if (warp >= 2 && good) {
+#pragma unroll
+        for (int c = 0; c < kN; ++c) store(c, acc[c]);
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (warp == 1) {
+        __syncwarp();
+        ptx::tmem_dealloc(tmem, S::kCols);
+    }
+}
+
+bool maps(const GemmFp8Args& p, CUtensorMap* a, CUtensorMap* b, uint32_t rows_a, uint32_t rows_b)
+{
+    return encode_tmap_3d_u8(a, p.a, p.K, p.T, 1, 128, rows_a) == CUDA_SUCCESS && encode_tmap_3d_u8(b, p.b, p.K, p.N, 1, 128, rows_b) == CUDA_SUCCESS;
+}
+
+template <bool kF32>
+cudaError_t launch_big(const GemmFp8Args& p, int sms, cudaStream_t stream)
+{
+    static bool set = false;
+    if (!set) {
+        cudaError_t e = cudaFuncSetAttribute(k_gemm_fp8<kF32>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kBigSmem));
+        if (e != cudaSuccess) return e;
+        set = true;
+    }
+    CUtensorMap a, b;
+    if (!maps(p, &a, &b, kBigM, kBigN)) return cudaErrorInvalidValue;
+    const int tn = (p.N + kBigN - 1) / kBigN, tm = (p.T + kBigM - 1) / kBigM;
+    const int64_t tiles = static_cast<int64_t>(tn) * tm;
+    if (tiles > 0x7FFFFFFF - 65536) return cudaErrorInvalidValue;
+    return launch_pdl(k_gemm_fp8<kF32>, dim3(tiles < sms ? static_cast<int>(tiles) : sms), dim3(kBigThreads), kBigSmem, stream, a, b, p, tn,
+                      static_cast<int>(tiles));
+}
+
+template <int kN, bool kF32>
+cudaError_t launch_few(const GemmFp8Args& p, int sms, cudaStream_t stream)
+{
+    static bool set = false;
+    if (!set) {
+        cudaError_t e = cudaFuncSetAttribute(k_gemm_fp8_few<kN, kF32>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(few_smem<kN>()));
+        if (e != cudaSuccess) return e;
+        set = true;
+    }
+    CUtensorMap a, b;
+    if (!maps(p, &a, &b, kN, kFewM)) return cudaErrorInvalidValue;
+    const int tt = (p.T + kN - 1) / kN, tn = (p.N + kFewM - 1) / kFewM, nk = (p.K + 127) / 128;
+    const int64_t tiles = static_cast<int64_t>(tt) * tn;
+    int cs = 1;
+    while (cs < 8 && tiles * cs * 2 <= sms && cs * 2 <= nk) cs *= 2;
+    if (tiles * cs > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * cs));
+    cfg.blockDim = dim3(kFewThreads);
+    cfg.dynamicSmemBytes = few_smem<kN>();
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cs;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, k_gemm_fp8_few<kN, kF32>, a, b, p, tt);
+}
+
+template <bool kF32>
+cudaError_t launch(const GemmFp8Args& p, int sms, cudaStream_t stream)
+{
+    const int64_t big = static_cast<int64_t>((p.T + kBigM - 1) / kBigM) * ((p.N + kBigN - 1) / kBigN);
+    if (p.T > 64 && big >= sms / 2) return launch_big<kF32>(p, sms, stream);
+    if (p.T <= 16) return launch_few<16, kF32>(p, sms, stream);
+    if (p.T <= 32) return launch_few<32, kF32>(p, sms, stream);
+    return launch_few<64, kF32>(p, sms, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_fp8(const GemmFp8Args& p, int sms, cudaStream_t stream)
+{
+    return p.out_f32 ? launch<true>(p, sms, stream) : launch<false>(p, sms, stream);
+}
+
+}  // namespace moe
