@@ -320,6 +320,7 @@ moe_status_t moe_read_device_status(void* ws, moe_stream_t stream)
     if (status & kDevBadSegment)
         return fail(MOE_ERR_INVALID_ARG, "device status 0x%x: seg_offsets or seg_adapter outside its range", status);
     if (status & kDevTimeoutGemmFp8) return fail(MOE_ERR_DEVICE_TIMEOUT, "device status 0x%x: FP8 GEMM wait timed out", status);
+    if (status & kDevTimeoutAttention) return fail(MOE_ERR_DEVICE_TIMEOUT, "device status 0x%x: attention wait timed out", status);
     if (status & kDevBadRequest)
         return fail(MOE_ERR_INVALID_ARG, "device status 0x%x: a request's seg_offsets or kv_len outside its range", status);
     if (status & kDevBadPage) return fail(MOE_ERR_INVALID_ARG, "device status 0x%x: page outside [0, n_pages)", status);

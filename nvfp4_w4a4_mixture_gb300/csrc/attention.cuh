@@ -13,6 +13,7 @@ enum : int {
     kDevBadRequest = 64,       // seg_offsets or kv_len outside its range
     kDevBadPage = 128,         // a page id outside [0, n_pages)
     kDevTimeoutGemmFp8 = 256,  // a bounded wait of the FP8 GEMM ran out
+    kDevTimeoutAttention = 512,  // a bounded wait of the attention ran out
 };
 
 struct KvCache {
@@ -40,6 +41,24 @@ __device__ __forceinline__ Request load_request(const Requests& r, int s, int T,
     const int beg = __ldg(r.seg_offsets + s), end = __ldg(r.seg_offsets + s + 1), len = __ldg(r.kv_len + s);
     bad = beg < 0 || beg > end || end > T || (s == 0 && beg != 0) || len < 0 || len > r.max_len || end - beg > max_new;
     return Request{beg, bad ? 0 : end - beg, len};
+}
+
+// The last request whose rows begin at or before row t (-1: none). Warp-wide; lanes look at 32 offsets at a time.
+__device__ __forceinline__ int find_request(const int32_t* off, int S, int t)
+{
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = S + 1;  // off[lo] <= t, once that was seen for lo = 0
+    bool first = true;
+    while (first || hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, i = lo + lane * step;
+        const unsigned m = __ballot_sync(0xFFFFFFFFu, i < hi && __ldg(off + min(i, S)) <= t);
+        const int k = __popc(m);
+        if (first && k == 0) return -1;
+        first = false;
+        lo += (max(k, 1) - 1) * step;
+        hi = min(lo + step, hi);
+    }
+    return lo;
 }
 
 // ---- cache_append.cu
@@ -70,7 +89,7 @@ struct AttentionArgs {
     uint16_t* out;
     int64_t ld_out;
     float* lse;       // nullable
-    int64_t* prefix;  // [S + 1] units before each request (workspace)
+    int64_t* prefix;  // [S + 3] units before each request, their number, and how they are cut (workspace)
     float* part;      // partial sums (workspace)
     float* part_ml;   // their maxima and weights (workspace)
     int* status;

@@ -12,24 +12,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// The last request whose rows begin at or before row t (-1: none). Warp-wide; lanes look at 32 offsets at a time.
-__device__ __forceinline__ int find_request(const int32_t* off, int S, int t)
-{
-    const int lane = threadIdx.x & 31;
-    int lo = 0, hi = S + 1;  // off[lo] <= t, once that was seen for lo = 0
-    bool first = true;
-    while (first || hi - lo > 1) {
-        const int step = (hi - lo + 31) / 32, i = lo + lane * step;
-        const unsigned m = __ballot_sync(0xFFFFFFFFu, i < hi && __ldg(off + min(i, S)) <= t);
-        const int k = __popc(m);
-        if (first && k == 0) return -1;
-        first = false;
-        lo += (max(k, 1) - 1) * step;
-        hi = min(lo + step, hi);
-    }
-    return lo;
-}
-
 __device__ __forceinline__ float bf16_at(const uint4& v, int i)
 {
     const uint32_t w = i / 2 == 0 ? v.x : i / 2 == 1 ? v.y : i / 2 == 2 ? v.z : v.w;
