@@ -193,8 +193,7 @@ moe_status_t moe_paged_attention(const moe_kv_cache_t* C, const moe_requests_t* 
     if (T == 0) return MOE_OK;  // an empty batch: nothing is read or written, the pointers may be NULL
     MOE_TRY(check_cache_memory(C));
     MOE_TRY(check_requests(R, C->page_size, T, &a.r));
-    // the join has a CTA for each request and key head, and each 16 rows of them
-    if (static_cast<int64_t>(R->S) * C->n_kv * 64 > 0x7FFFFFFF) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "S=%d requests of n_kv=%d heads: too many", R->S, C->n_kv);
+    if (static_cast<int64_t>(T) * A->n_q > 0x7FFFFF00) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "T=%d rows of n_q=%d heads: 2^31 or more", T, A->n_q);
     if (!q || !out) return fail(MOE_ERR_INVALID_ARG, "NULL tensor pointer");
     const int64_t w = static_cast<int64_t>(A->n_q) * C->D;
     MOE_TRY(check_rows("q", q, ld_q, w, 2, T));

@@ -94,6 +94,17 @@ struct AttentionArgs {
     float* part_ml;   // their maxima and weights (workspace)
     int* status;
 };
+namespace attention {
+// the rows of a unit in eights: what max_new tokens of a key head's queries need, at most eight
+inline int row_eights(int group, int max_new)
+{
+    const int rows = group * max_new;
+    return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : rows <= 32 ? 4 : 8;
+}
+
+// most CTAs of the main launch: each has two places for partial sums
+inline int ctas_most(int sms) { return sms * 4; }
+}  // namespace attention
 size_t attention_workspace_bytes(int S, int n_q, int n_kv, int D, int max_new, int sms);
 cudaError_t launch_paged_attention(AttentionArgs a, void* ws, int sms, cudaStream_t stream);
 

@@ -1,0 +1,898 @@
+// paged_attention.cuh -- attention of a few new tokens of every request over a paged cache:
+//   out = sum_t softmax_t(scale q . k_t) v_t over the tokens that a row sees, in one pass over keys and values
+// with the running maximum m and sum l of the softmax: o <- o 2^(m - m') + 2^(s - m') v.
+//
+// Work: a unit is 64 cached tokens of one key head against up to kRows rows (new tokens x query heads of that key
+// head). The units of all requests, in order, are cut into equal runs, one a CTA, so ragged lengths balance by
+// themselves. A (request, head) whose units lie in one run is finished there; of the others every run leaves o, m and l
+// in the workspace, and a second launch adds them in the order of the runs.
+// A CTA streams K and V through a ring in shared memory: two warps load (cp.async of 16 bytes a lane, addresses from
+// the page table, which is read a unit ahead; a token behind the end is filled with zeros). Of a unit each of the four
+// others takes 16 tokens of K Q^T, they exchange maxima and weights through shared memory, and each takes a quarter of
+// the columns of V^T P^T: K and V are read from shared memory once, and the accumulators need no join. mma.sync
+// with the tokens (and V's columns) on its M side: rows are padded to eight, not sixteen. The products are 4 flops a
+// byte and row, for 8 rows 32 flops a byte, which the memory bounds long before.
+// bf16 cache: the weights are two bf16 values (16 bits); E4M3 cache: codes become FP16 (exact), the weights are FP16
+// and q is scaled to FP16's range by a power of two a row (exact where q is not 2^-30 of the row's largest).
+#pragma once
+#include "attention.cuh"
+#include "ptx_cluster.cuh"
+
+namespace moe {
+
+namespace attention {
+
+constexpr int kWarps = 4, kGroup = 32 * kWarps;  // a group of warps that computes
+constexpr int kLoaders = 2, kLoad = 64 / kLoaders;  // warps that load, a warp's tokens of a unit
+constexpr int kTile = 64;                        // tokens of a unit, 16 a warp
+constexpr int kMinUnits = 1;                     // a run costs at least so many units
+constexpr int kExtra = 2;                        // what the begin and the end of a (request, head) cost, in units
+
+// kRG: groups, kNR: a group's rows in eights
+template <int kD, bool kE4M3, int kRG, int kNR>
+struct Shape {
+    static constexpr int kThreads = kRG * kGroup + kLoaders * 32;
+    static constexpr int kRows = 8 * kRG * kNR;
+    static constexpr int kRowBytes = kD * (kE4M3 ? 1 : 2);       // of a cached token's head
+    static constexpr int kStage = 2 * kTile * kRowBytes;         // K, V
+    static constexpr int kQ = kRows * kD * 2;
+    static constexpr int kP = kRows * kTile * 2 * (kE4M3 ? 1 : 2);
+    static constexpr int kFixed = kQ + kP + kRows * (2 * kWarps * 4 + 8) + 512;
+    // as many CTAs an SM as hold three stages each, and as the registers of so many rows allow: one to four
+    static constexpr int kByRegs = kRG == 4 ? 1 : kRG >= 2 ? 2 : 3;
+    // (a multiprocessor's 228 KB less 1 KB a CTA, and 10 KB in which the join's CTAs can wait)
+    static constexpr int most(int ctas) { return (218 / ctas - 1) * 1024; }
+    static constexpr int by_smem(int ctas) { return ctas == 1 || (most(ctas) - kFixed) / kStage >= 3 ? ctas : by_smem(ctas - 1); }
+    static constexpr int kCtas = by_smem(kByRegs);
+    static constexpr int kFit = (most(kCtas) - kFixed) / kStage;
+    static constexpr int kStages = kFit > 6 ? 6 : kFit;
+    static constexpr int kSmem = kFixed + kStages * kStage;
+    static_assert(kStages >= 2 && kSmem <= most(kCtas), "shared memory");
+};
+
+// ---- the cut into runs of equal cost. A (request, head) of n units costs kExtra + n, its unit i lying at offset kExtra + i:
+// a border inside the extra part is one before its first unit.
+__host__ __device__ __forceinline__ int runs_of(int64_t total, int ctas)
+{
+    const int64_t n = (total + kMinUnits - 1) / kMinUnits;
+    return n < ctas ? static_cast<int>(n) : ctas;
+}
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)  // of numbers that mostly fit 32 bits
+{
+    return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
+struct Cut {
+    int64_t q, r;  // runs 0 .. r - 1 have q + 1 units, the others q
+    __device__ int64_t first(int64_t c) const { return c * q + (c < r ? c : r); }
+    __device__ int run(int64_t u) const { return static_cast<int>(u < r * (q + 1) ? quotient(u, q + 1) : r + quotient(u - r * (q + 1), q)); }
+};
+
+struct Span {
+    int beg, n, len, start, tiles, segs;  // rows; tokens; first token seen; units along the tokens; (head, row block) pairs
+    __device__ int64_t cost() const { return static_cast<int64_t>(tiles + (tiles ? kExtra : 0)) * segs; }
+};
+
+template <int kRows>
+__device__ __forceinline__ Span span_of(const AttentionArgs& p, int s, bool& bad)
+{
+    const Request r = load_request(p.r, s, p.T, p.max_new, bad);
+    Span a{r.beg, r.n, r.len, 0, 0, 0};
+    if (r.n == 0) return a;
+    if (p.window > 0) {
+        const int64_t first = static_cast<int64_t>(r.len) - r.n - p.window + 1;
+        a.start = first > 0 ? static_cast<int>(first) : 0;
+    }
+    a.tiles = max(1, static_cast<int>((static_cast<int64_t>(r.len) - a.start + kTile - 1) / kTile));  // a request that sees nothing has a unit, too
+    a.segs = p.c.n_kv * ((r.n * p.group + kRows - 1) / kRows);
+    return a;
+}
+
+// A place in the order of units.
+template <int kRows>
+struct Cursor {
+    Span a;
+    int s, seg, tile;
+    // The next unit (there is one).
+    __device__ void next(const AttentionArgs& p)
+    {
+        if (++tile < a.tiles) return;
+        tile = 0;
+        if (++seg < a.segs) return;
+        seg = 0;
+        bool bad;
+        do a = span_of<kRows>(p, ++s, bad);
+        while (a.segs == 0);
+    }
+};
+
+// ---- warp-level matrix products and their operands
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// Two 8 x 8 blocks of 16-bit values, stored transposed: lanes 0 .. 7 and 8 .. 15 give the rows' addresses.
+__device__ __forceinline__ void stsm2t(uint32_t addr, uint32_t a, uint32_t b)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x2.trans.shared.b16 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+template <bool kF16>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    if constexpr (kF16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Four E4M3 codes as FP16 values, exactly: the lower two and the upper two.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t v, uint32_t& lo, uint32_t& hi)
+{
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}\n"
+        : "=r"(lo), "=r"(hi)
+        : "r"(v));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float f16_to_f32(uint32_t bits16)
+{
+    float f;
+    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.f32.f16 %0, t;\n\t}\n" : "=f"(f) : "r"(bits16));
+    return f;
+}
+// 2^x, the hardware's (2 units in the last place); 0 for -inf
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// 16-byte piece c of row r, so that eight rows' equal pieces lie in different banks
+template <int kRowBytes>
+__device__ __forceinline__ uint32_t piece(int r, int c)
+{
+    if constexpr (kRowBytes == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+    else return r * kRowBytes + ((c ^ (r & 7)) << 4);
+}
+// the same for E4M3 keys, which are read four pieces of two rows at a time
+template <int kRowBytes>
+__device__ __forceinline__ uint32_t piece_k8(int r, int c)
+{
+    if constexpr (kRowBytes == 64) return r * 64 + (c << 4);
+    else return r * kRowBytes + ((c ^ ((r & 1) << 2)) << 4);
+}
+
+// The elements of a word (four bytes or two halves) that are no finite numbers: their top bits.
+template <bool kE4M3>
+__device__ __forceinline__ uint32_t odd_mask(uint32_t w)
+{
+    if constexpr (kE4M3) return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // 0x7F: NaN
+    else return (((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u);                // an exponent of all ones
+}
+
+template <int kD, bool kE4M3, int kRG, int kNR>
+__global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD, kE4M3, kRG, kNR>::kCtas) k_paged_attention(const __grid_constant__ AttentionArgs p)
+{
+    using S = Shape<kD, kE4M3, kRG, kNR>;
+    constexpr int kThreads = S::kThreads, kCompute = kRG * kGroup;
+    constexpr int kRows = S::kRows, kRB = S::kRowBytes, kChunks = kRB / 16, kStages = S::kStages;
+    constexpr int kQB = kD * 2;             // bytes of a row of q
+    constexpr int kMT = kD / 64;             // 16-column tiles of a warp's quarter of the columns
+    constexpr int kKS = kD / 16;             // steps of Q K^T
+    constexpr bool kQReg = kNR * kKS <= 8;  // q's fragments stay in registers
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t* const ring = smem;
+    uint8_t* const qs = smem + kStages * S::kStage;
+    uint8_t* const ps = qs + S::kQ;         // weights: [kRows][64] 16-bit, bf16: the high parts, then the low ones
+    float* const wmax = reinterpret_cast<float*>(ps + S::kP);  // [kRows][kWarps]
+    float* const wsum = wmax + kRows * kWarps;                 // [kRows][kWarps]
+    float* const qscale = wsum + kRows * kWarps;               // [kRows] (E4M3) what the row of q was divided by
+    int* const row_pos = reinterpret_cast<int*>(qscale + kRows);  // [kRows] the row's position
+    int64_t* const found = reinterpret_cast<int64_t*>(row_pos + kRows);  // a sum a warp, then what the search found
+    Cursor<kRows>* const start = reinterpret_cast<Cursor<kRows>*>(found + 20);
+    uint64_t* const full = reinterpret_cast<uint64_t*>(found + 30);  // [kStages]
+    uint64_t* const empty = full + kStages;                            // [kStages]
+    int* const abort = reinterpret_cast<int*>(empty + kStages);
+    const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid / 32, 0), lane = tid % 32, g = lane / 4, t4 = lane % 4;
+    const uint32_t ring_a = ptx::smem_u32(ring), qs_a = ptx::smem_u32(qs), ps_a = ptx::smem_u32(ps);
+
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            ptx::mbar_init(full + s, kLoaders * 32);  // the loading lanes
+            ptx::mbar_init(empty + s, kRG * kWarps);
+        }
+        *abort = 0;
+        ptx::fence_mbar_init();
+    }
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+
+    // ---- this CTA's run: the units before each request, a block of requests a thread
+    const int block = (p.r.S + kThreads - 1) / kThreads, sb = min(p.r.S, tid * block), se = min(p.r.S, sb + block);
+    int64_t mine = 0;
+    for (int s = sb; s < se; ++s) {
+        bool bad;
+        mine += span_of<kRows>(p, s, bad).cost();
+        if (bad && blockIdx.x == 0) record_status(p.status, kDevBadRequest);
+    }
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) found[warp] = incl;
+    __syncthreads();
+    int64_t before = incl - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += found[w];
+        total += found[w];
+    }
+    const int runs = runs_of(total, gridDim.x);
+    Cut cut{0, 0};
+    if (runs) {
+        cut.q = quotient(total, runs);
+        cut.r = total - cut.q * runs;
+    }
+    if (blockIdx.x == 0) {  // for the join
+        int64_t u = before;
+        for (int s = sb; s < se; ++s) {
+            bool bad;
+            p.prefix[s] = u;
+            u += span_of<kRows>(p, s, bad).cost();
+        }
+        if (tid == 0) {
+            p.prefix[p.r.S] = total;
+            p.prefix[p.r.S + 1] = cut.q;
+            p.prefix[p.r.S + 2] = cut.r;
+        }
+    }
+    if (static_cast<int>(blockIdx.x) >= runs) return;
+    // its first unit, and the place of both borders in the order of units
+    const int64_t border[2] = {cut.first(blockIdx.x), cut.first(blockIdx.x + 1)};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        if (border[e] < before || border[e] >= before + mine) continue;
+        int64_t u = border[e] - before;
+        Cursor<kRows> c;
+        for (c.s = sb;; ++c.s) {
+            bool bad;
+            c.a = span_of<kRows>(p, c.s, bad);
+            if (u < c.a.cost()) break;
+            u -= c.a.cost();
+        }
+        const int each = c.a.tiles + kExtra;
+        c.seg = static_cast<int>(quotient(u, each));
+        c.tile = max(0, static_cast<int>(u - static_cast<int64_t>(c.seg) * each) - kExtra);
+        start[e] = c;
+    }
+    __syncthreads();
+    Cursor<kRows> cu = start[0];
+    // the units between the borders
+    int count;
+    {
+        const bool to_end = border[1] == total;
+        const Cursor<kRows> end = start[1];
+        const int last_s = to_end ? p.r.S : end.s;
+        int64_t n = -(static_cast<int64_t>(cu.seg) * cu.a.tiles + cu.tile) + (to_end ? 0 : static_cast<int64_t>(end.seg) * end.a.tiles + end.tile);
+        for (int s = cu.s; s < last_s; ++s) {
+            bool bad;
+            const Span a = s == cu.s ? cu.a : span_of<kRows>(p, s, bad);
+            n += static_cast<int64_t>(a.tiles) * a.segs;
+        }
+        count = static_cast<int>(n);
+    }
+    // A bounded wait (a waiting warp takes no issue slots). After one that ran out there are no more: the rest runs on
+    // whatever is there, to its end.
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (*reinterpret_cast<volatile int*>(abort) == 0 && !ptx::mbar_wait(bar, parity)) {
+            *reinterpret_cast<volatile int*>(abort) = 1;
+            record_status(p.status, kDevTimeoutAttention);
+        }
+    };
+
+    if (warp >= kRG * kWarps) {
+        // ---- loads: a warp kLoad tokens of a unit, four lanes a token; page ids come a unit ahead
+        const int lw = warp - kRG * kWarps;
+        const int64_t v_from_k = static_cast<const char*>(p.c.v) - static_cast<const char*>(p.c.k);
+        const uint32_t k_even = lw * kLoad * kRB + (kE4M3 ? piece_k8<kRB>(g, t4) : piece<kRB>(g, t4)), k_odd = k_even ^ 64;
+        const uint32_t v_even = (kTile + lw * kLoad) * kRB + piece<kRB>(g, t4), v_odd = v_even ^ 64;
+        const int mask = (1 << p.c.page_log2) - 1;
+        int page = 0, pos = 0;  // of the token lane % kLoad
+        bool in = false;
+        int64_t head_off = 0;
+        auto fetch = [&]() {
+            pos = cu.a.start + cu.tile * kTile + lw * kLoad + lane % kLoad;
+            head_off = (cu.seg % p.c.n_kv) * p.c.ld_head;
+            in = pos < cu.a.len && pos >= 0;
+            if (in) page = __ldg(p.r.pages + cu.s * p.r.ld_pages + (pos >> p.c.page_log2));
+        };
+        fetch();
+        int s = 0;
+        uint32_t ph = 1;
+        for (int j = 0; j < count; ++j) {
+            if (in && static_cast<unsigned>(page) >= static_cast<unsigned>(p.c.n_pages)) {
+                in = false;
+                record_status(p.status, kDevBadPage);
+            }
+            const int64_t mine = in ? (page * p.c.ld_page + (pos & mask) * p.c.ld_slot + head_off) * (kE4M3 ? 1 : 2) : -1;
+            if (j + 1 < count) {
+                cu.next(p);
+                fetch();
+            }
+            wait(empty + s, ph);
+            uint8_t* const to = ring + s * S::kStage;
+#pragma unroll
+            for (int b = 0; b < kLoad / 8; ++b) {
+                const int64_t off = __shfl_sync(0xFFFFFFFFu, mine, b * 8 + g);
+                const bool there = off >= 0;
+                const char* const k = static_cast<const char*>(p.c.k) + (there ? off + t4 * 16 : 0);
+                const char* const v = k + v_from_k;
+#pragma unroll
+                for (int i = 0; i < kChunks / 4; ++i) {
+                    ptx::cp_async_16(to + b * 8 * kRB + (i & 1 ? k_odd : k_even) + i / 2 * 128, k + i * 64, there);
+                    ptx::cp_async_16(to + b * 8 * kRB + (i & 1 ? v_odd : v_even) + i / 2 * 128, v + i * 64, there);
+                }
+            }
+            ptx::cp_async_arrive_noinc(full + s);
+            if (++s == kStages) { s = 0; ph ^= 1; }
+        }
+        ptx::cp_async_commit();
+        ptx::cp_async_wait<0>();
+        return;
+    }
+
+    // group rg, its warp gw, thread gt; its rows are the eights rg, rg + kRG, ..
+    const int rg = warp / kWarps, gw = warp % kWarps, gt = tid % kGroup;
+    auto base_of = [&](int nr) { return (nr * kRG + rg) * 8; };
+    auto sync = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + rg), "n"(kGroup) : "memory"); };  // of the group
+    auto sync_all = [] { asm volatile("bar.sync 8, %0;" ::"n"(kCompute) : "memory"); };           // of all groups
+    auto any_of = [](bool v) {
+        uint32_t r;
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t"
+            "setp.ne.u32 q, %1, 0;\n\t"
+            "bar.red.or.pred p, 8, %2, q;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}\n"
+            : "=r"(r)
+            : "r"(static_cast<uint32_t>(v)), "n"(kCompute)
+            : "memory");
+        return r != 0;
+    };
+
+    float o[kMT][kNR][4], m[kNR][2], l[kNR][2];  // rows 8 nr + 2 t4, + 1; columns of v by g
+    uint32_t qf[kQReg ? kNR : 1][kQReg ? kKS : 1][2];
+    uint32_t stage_off = 0;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool opens = true;
+    int h = 0, row0 = 0, rows = 0, live = 0, first_row = 0, last_row = 0;
+    float factor = 0.0f;
+    bool active = false;  // this group has rows
+
+    for (int j = 0; j < count; ++j) {
+        if (opens) {
+            // ---- the rows' queries
+            h = cu.seg % p.c.n_kv;
+            row0 = cu.seg / p.c.n_kv * kRows;
+            rows = min(kRows, cu.a.n * p.group - row0);
+            live = (rows + 7) / 8;
+            first_row = cu.a.len - cu.a.n + row0 / p.group;
+            last_row = cu.a.len - cu.a.n + (row0 + rows - 1) / p.group;
+            factor = p.scale * 1.44269504088896340736f * (kE4M3 && p.c.k_scale ? __ldg(p.c.k_scale + h) : 1.0f);
+            active = rg < live;
+            constexpr int kQC = kD / 8;
+#pragma unroll 4
+            for (int i = gt; i < 8 * kNR * kQC; i += kGroup) {
+                const int r = base_of(i / kQC / 8) + i / kQC % 8, c = i % kQC, at = (row0 + r) / p.group;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (r < rows) v = __ldg(reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(cu.a.beg + at) * p.ld_q + (h * p.group + (row0 + r) - at * p.group) * kD + c * 8));
+                if (c == 0) row_pos[r] = cu.a.len - cu.a.n + at;
+                if constexpr (!kE4M3) {
+                    *reinterpret_cast<uint4*>(qs + piece<kQB>(r, c)) = v;
+                } else {
+                    // FP16 with the row's largest in [2^14, 2^15), columns in the order in which the keys' bytes come:
+                    // column 16 x + k of a block of 64 is element 16 t + 4 x + e, t and e as the fragments have them
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t big = 0;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) big = max(big, max((w[x] << 16) & 0x7FFF0000u, w[x] & 0x7FFF0000u));
+#pragma unroll
+                    for (int x = kQC / 2; x > 0; x >>= 1) big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, x));
+                    const int shift = big ? max(-110, min(100, 14 + 127 - static_cast<int>(big >> 23))) : 0;
+                    const float by = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
+                    if (c == 0) qscale[r] = __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int d = c * 8 + 2 * x, rem = d % 64, k = rem % 4 / 2 * 8 + rem / 16 * 2;
+                        const int col = d / 64 * 64 + rem % 16 / 4 * 16 + k;
+                        *reinterpret_cast<uint32_t*>(qs + piece<kQB>(r, col / 8) + col % 8 * 2) =
+                            pack_f16x2(__uint_as_float(w[x] << 16) * by, __uint_as_float(w[x] & 0xFFFF0000u) * by);
+                    }
+                }
+            }
+            sync();  // (of a group without rows, too)
+            if constexpr (kQReg) {
+#pragma unroll
+                for (int nr = 0; nr < kNR; ++nr)
+#pragma unroll
+                    for (int ks = 0; ks < kKS; ks += 2) {
+                        uint32_t b[4];
+                        ldsm4(qs_a + piece<kQB>(base_of(nr) + (lane & 7), 2 * ks + (lane >> 3)), b);
+                        qf[nr][ks][0] = b[0];
+                        qf[nr][ks][1] = b[1];
+                        qf[nr][ks + 1][0] = b[2];
+                        qf[nr][ks + 1][1] = b[3];
+                    }
+            }
+#pragma unroll
+            for (int nr = 0; nr < kNR; ++nr) {
+                m[nr][0] = m[nr][1] = -INFINITY;
+                l[nr][0] = l[nr][1] = 0.0f;
+#pragma unroll
+                for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) o[mt][nr][x] = 0.0f;
+            }
+            opens = false;
+        }
+
+        wait(full + stage, phase);
+        const uint32_t ks_a = ring_a + stage_off, vs_a = ks_a + kTile * kRB;
+        const int pos0 = cu.a.start + cu.tile * kTile;
+        // some row does not see some token (rows further down see later ones)
+        const bool edge = pos0 + kTile - 1 > first_row || (p.window > 0 && static_cast<int64_t>(pos0) + p.window <= last_row);
+        auto sees = [&](int at, int pos) { return pos <= at && (p.window <= 0 || static_cast<int64_t>(pos) + p.window > at); };
+        if (active) {
+        // ---- S^T = K Q^T of this warp's 16 tokens, two chains of sums
+        float sc[kNR][4], sc2[kNR][4];
+#pragma unroll
+        for (int nr = 0; nr < kNR; ++nr)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) sc[nr][x] = sc2[nr][x] = 0.0f;
+        // q's fragments of steps ks and ks + 1
+        auto q_frag = [&](int nr, int ks, uint32_t (&b)[4]) {
+            if constexpr (kQReg) {
+                b[0] = qf[nr][ks][0];
+                b[1] = qf[nr][ks][1];
+                b[2] = qf[nr][ks + 1][0];
+                b[3] = qf[nr][ks + 1][1];
+            } else {
+                ldsm4(qs_a + piece<kQB>(base_of(nr) + (lane & 7), 2 * ks + (lane >> 3)), b);
+            }
+        };
+        if constexpr (!kE4M3) {
+#pragma unroll
+            for (int ks = 0; ks < kKS; ks += 2) {
+                uint32_t a[4], a2[4];
+                ldsm4(ks_a + piece<kRB>(gw * 16 + (lane & 15), 2 * ks + (lane >> 4)), a);
+                ldsm4(ks_a + piece<kRB>(gw * 16 + (lane & 15), 2 * ks + 2 + (lane >> 4)), a2);
+#pragma unroll
+                for (int nr = 0; nr < kNR; ++nr) {
+                        uint32_t b[4];
+                        q_frag(nr, ks, b);
+                        mma<false>(sc[nr], a[0], a[1], a[2], a[3], b[0], b[1]);
+                        mma<false>(sc2[nr], a2[0], a2[1], a2[2], a2[3], b[2], b[3]);
+                    }
+            }
+        } else {
+#pragma unroll
+            for (int blk = 0; blk < kD / 64; ++blk) {
+                uint32_t w[2][4];
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(w[y][0]), "=r"(w[y][1]), "=r"(w[y][2]), "=r"(w[y][3])
+                                 : "r"(ks_a + piece_k8<kRB>(gw * 16 + y * 8 + g, 4 * blk + t4))
+                                 : "memory");
+#pragma unroll
+                for (int x = 0; x < 4; x += 2) {
+                    uint32_t a[2][4];
+#pragma unroll
+                    for (int z = 0; z < 2; ++z)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) e4m3x4_to_f16(w[y][x + z], a[z][y], a[z][2 + y]);
+#pragma unroll
+                    for (int nr = 0; nr < kNR; ++nr) {
+                            uint32_t b[4];
+                            q_frag(nr, 4 * blk + x, b);
+                            mma<true>(sc[nr], a[0][0], a[0][1], a[0][2], a[0][3], b[0], b[1]);
+                            mma<true>(sc2[nr], a[1][0], a[1][1], a[1][2], a[1][3], b[2], b[3]);
+                        }
+                }
+            }
+        }
+
+        // ---- scores in powers of two, masks, maxima
+#pragma unroll
+        for (int nr = 0; nr < kNR; ++nr) {
+                const float2 by = kE4M3 ? *reinterpret_cast<const float2*>(qscale + base_of(nr) + 2 * t4) : make_float2(1.0f, 1.0f);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) sc[nr][x] = (sc[nr][x] + sc2[nr][x]) * (kE4M3 ? factor * (x & 1 ? by.y : by.x) : factor);
+                if (edge) {
+                    const int2 at = *reinterpret_cast<const int2*>(row_pos + base_of(nr) + 2 * t4);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        if (!sees(x & 1 ? at.y : at.x, pos0 + gw * 16 + g + x / 2 * 8)) sc[nr][x] = -INFINITY;
+                }
+                float u = fmaxf(sc[nr][0], sc[nr][2]), v = fmaxf(sc[nr][1], sc[nr][3]);
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) {
+                    u = fmaxf(u, __shfl_xor_sync(0xFFFFFFFFu, u, x));
+                    v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, x));
+                }
+                if (g == 0) {
+                    wmax[(base_of(nr) + 2 * t4) * kWarps + gw] = u;
+                    wmax[(base_of(nr) + 2 * t4 + 1) * kWarps + gw] = v;
+                }
+            }
+        sync();  // the maxima are there, and every warp is done with the weights of the unit before
+
+        // ---- weights
+        bool moved = false;
+        float alpha[kNR][2];
+#pragma unroll
+        for (int nr = 0; nr < kNR; ++nr) {
+                float by[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float4 w = *reinterpret_cast<const float4*>(wmax + (base_of(nr) + 2 * t4 + x) * kWarps);
+                    const float to = fmaxf(fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w)), m[nr][x]);
+                    moved |= to > m[nr][x];
+                    by[x] = to == -INFINITY ? 0.0f : to;  // a row that has seen nothing yet
+                    alpha[nr][x] = exp2_fast(m[nr][x] - by[x]);
+                    m[nr][x] = to;
+                }
+#pragma unroll
+                for (int x = 0; x < 4; ++x) sc[nr][x] = exp2_fast(sc[nr][x] - by[x & 1]);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) l[nr][x] = l[nr][x] * alpha[nr][x] + (sc[nr][x] + sc[nr][x + 2]);
+                // rows of 64 tokens: this warp's 16 are pieces 2 warp and 2 warp + 1
+                const uint32_t at = ps_a + piece<128>(base_of(nr) + (lane & 7), 2 * gw + ((lane >> 3) & 1));
+                if constexpr (kE4M3) {
+                    stsm2t(at, pack_f16x2(sc[nr][0], sc[nr][1]), pack_f16x2(sc[nr][2], sc[nr][3]));
+                } else {
+                    uint32_t high[2], low[2];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        high[x] = pack_bf16x2(sc[nr][2 * x], sc[nr][2 * x + 1]);
+                        low[x] = pack_bf16x2(sc[nr][2 * x] - __uint_as_float(high[x] << 16), sc[nr][2 * x + 1] - __uint_as_float(high[x] & 0xFFFF0000u));
+                    }
+                    stsm2t(at, high[0], high[1]);
+                    stsm2t(at + kRows * kTile * 2, low[0], low[1]);
+                }
+            }
+        if (__any_sync(0xFFFFFFFFu, moved)) {
+#pragma unroll
+            for (int nr = 0; nr < kNR; ++nr) {
+#pragma unroll
+                    for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) o[mt][nr][x] *= alpha[nr][x & 1];
+                }
+        }
+
+        }
+
+        // an accumulator's column of v: x / 2 is the lower or upper eight of a tile (E4M3: the even or odd columns)
+        auto column = [&](int mt, int x) {
+            return gw * (kD / 4) + mt * 16 + (kE4M3 ? 2 * g + x / 2 : g + x / 2 * 8);
+        };
+        if (edge && cu.a.n > 1) {
+            // A token that only some rows see may hold infinities or NaN, and a weight of 0 times them is no 0: such
+            // elements are added by the rows that see them, one by one, and taken out of the unit.
+            uint8_t* const vs = ring + stage_off + kTile * kRB;
+            bool odd = false;
+            for (int i = tid; i < kTile * kRB / 16; i += kCompute) {
+                const uint4 w = *reinterpret_cast<const uint4*>(vs + i * 16);
+                odd |= (odd_mask<kE4M3>(w.x) | odd_mask<kE4M3>(w.y) | odd_mask<kE4M3>(w.z) | odd_mask<kE4M3>(w.w)) != 0;
+            }
+            if (any_of(odd)) {  // (the weights are there)
+#pragma unroll 1
+                for (int tok = 0; tok < (active ? kTile : 0); ++tok) {
+                    const int pos = pos0 + tok;
+#pragma unroll
+                    for (int nr = 0; nr < kNR; ++nr)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const int r = base_of(nr) + 2 * t4 + y;
+                            if (!sees(row_pos[r], pos)) continue;
+                            const uint8_t* pp = ps + piece<128>(r, tok / 8) + tok % 8 * 2;
+                            float wt;
+                            if constexpr (kE4M3) wt = f16_to_f32(*reinterpret_cast<const uint16_t*>(pp));
+                            else wt = bf16_to_f32(*reinterpret_cast<const uint16_t*>(pp)) + bf16_to_f32(*reinterpret_cast<const uint16_t*>(pp + kRows * kTile * 2));
+#pragma unroll
+                            for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+                                for (int x = y; x < 4; x += 2) {
+                                    const int d = column(mt, x);
+                                    if constexpr (kE4M3) {
+                                        const uint32_t b = vs[piece<kRB>(tok, d / 16) + d % 16];
+                                        if ((b & 0x7Fu) == 0x7Fu) o[mt][nr][x] += wt * NAN;
+                                    } else {
+                                        const uint32_t b = *reinterpret_cast<const uint16_t*>(vs + piece<kRB>(tok, d / 8) + d % 8 * 2);
+                                        if ((b & 0x7F80u) == 0x7F80u) o[mt][nr][x] += wt * bf16_to_f32(b);
+                                    }
+                                }
+                        }
+                }
+                sync_all();
+                for (int i = tid; i < kTile * kRB / 4; i += kCompute) {
+                    uint32_t* const w = reinterpret_cast<uint32_t*>(vs) + i;
+                    const uint32_t odds = odd_mask<kE4M3>(*w);
+                    // the elements of the marked top bits, as whole bytes or halves
+                    if (odds) *w &= ~(kE4M3 ? (odds >> 7) * 0xFFu : (odds >> 15) * 0xFFFFu);
+                }
+                sync_all();
+            }
+        } else if (active) {
+            sync();  // the weights are there
+        }
+
+        if (active) {
+        // ---- O^T += V^T P^T, this warp's quarter of the columns, 32 tokens at a time
+#pragma unroll 1
+        for (int kk = 0; kk < kTile / 16; kk += 2) {
+            uint32_t b[kNR][4], bl[kE4M3 ? 1 : kNR][4];
+#pragma unroll
+            for (int nr = 0; nr < kNR; ++nr) {
+                    const uint32_t at = ps_a + piece<128>(base_of(nr) + (lane & 7), 2 * kk + (lane >> 3));
+                    ldsm4(at, b[nr]);
+                    if constexpr (!kE4M3) ldsm4(at + kRows * kTile * 2, bl[nr]);
+                }
+#pragma unroll
+            for (int mt = 0; mt < kMT; ++mt) {
+                uint32_t a[2][4];  // of both steps
+                if constexpr (!kE4M3) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        ldsm4t(vs_a + piece<kRB>((kk + x) * 16 + (lane & 7) + (lane >> 4) * 8, gw * (kD / 32) + 2 * mt + ((lane >> 3) & 1)), a[x]);
+                } else {
+                    // a piece is 16 columns: the transposed load gives the bytes of two columns of two tokens
+                    uint32_t w[4];
+                    ldsm4t(vs_a + piece<kRB>(kk * 16 + lane, gw * (kD / 64) + mt), w);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        e4m3x4_to_f16(__byte_perm(w[x], 0, 0x3120), a[x / 2][x % 2 * 2], a[x / 2][x % 2 * 2 + 1]);
+                    }
+                }
+#pragma unroll
+                for (int nr = 0; nr < kNR; ++nr) {
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            mma<kE4M3>(o[mt][nr], a[x][0], a[x][1], a[x][2], a[x][3], b[nr][2 * x], b[nr][2 * x + 1]);
+                            if constexpr (!kE4M3) mma<false>(o[mt][nr], a[x][0], a[x][1], a[x][2], a[x][3], bl[nr][2 * x], bl[nr][2 * x + 1]);
+                        }
+                    }
+            }
+        }
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(empty + stage);
+        stage_off += S::kStage;
+        if (++stage == kStages) {
+            stage = 0;
+            stage_off = 0;
+            phase ^= 1;
+        }
+
+        // ---- the end of a (request, head): finished here, or a part of it
+        const bool last = j == count - 1, closes = cu.tile == cu.a.tiles - 1;
+        if ((last || closes) && active) {
+#pragma unroll
+            for (int nr = 0; nr < kNR; ++nr)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float v = l[nr][x];
+#pragma unroll
+                    for (int y = 4; y < 32; y <<= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, y);
+                    if (g == 0) wsum[(base_of(nr) + 2 * t4 + x) * kWarps + gw] = v;
+                }
+            sync();
+            const bool whole = closes && cu.tile <= j;  // its first unit is in this run as well
+            // a part: slot 0 where the (request, head) holds the run's first unit, else 1
+            const int64_t part = blockIdx.x * 2 + (cu.tile >= j ? 0 : 1);
+#pragma unroll
+            for (int nr = 0; nr < kNR; ++nr)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int r = base_of(nr) + 2 * t4 + x;
+                    const float4 w = *reinterpret_cast<const float4*>(wsum + r * kWarps);
+                    const float sum = (w.x + w.y) + (w.z + w.w);
+                    if (r >= rows) continue;
+                    if (whole) {
+                        const int at = (row0 + r) / p.group, head = h * p.group + (row0 + r) - at * p.group;
+                        const int64_t t = cu.a.beg + at;
+                        float by = sum == 0.0f ? 0.0f : 1.0f / sum;
+                        if (kE4M3 && p.c.v_scale) by *= __ldg(p.c.v_scale + h);
+                        uint16_t* const to = p.out + t * p.ld_out + head * kD;
+                        if (p.lse && gw == 0 && g == 0)
+                            p.lse[t * p.n_q + head] = sum == 0.0f ? -INFINITY : (m[nr][x] + log2f(sum)) * 0.69314718055994530942f;
+#pragma unroll
+                        for (int mt = 0; mt < kMT; ++mt) {
+                            const uint32_t b = pack_bf16x2(o[mt][nr][x] * by, o[mt][nr][x + 2] * by);
+                            if constexpr (kE4M3) {
+                                *reinterpret_cast<uint32_t*>(to + column(mt, 0)) = b;
+                            } else {
+                                to[column(mt, 0)] = static_cast<uint16_t>(b);
+                                to[column(mt, 2)] = static_cast<uint16_t>(b >> 16);
+                            }
+                        }
+                    } else {
+                        float* const to = p.part + (part * kRows + r) * kD;
+                        if (gw == 0 && g == 0) *reinterpret_cast<float2*>(p.part_ml + (part * kRows + r) * 2) = make_float2(m[nr][x], sum);
+#pragma unroll
+                        for (int mt = 0; mt < kMT; ++mt) {
+                            if constexpr (kE4M3) {
+                                *reinterpret_cast<float2*>(to + column(mt, 0)) = make_float2(o[mt][nr][x], o[mt][nr][x + 2]);
+                            } else {
+                                to[column(mt, 0)] = o[mt][nr][x];
+                                to[column(mt, 2)] = o[mt][nr][x + 2];
+                            }
+                        }
+                    }
+                }
+        }
+        opens = closes;
+        if (!last) cu.next(p);
+    }
+}
+
+// ---- the join: a row's parts, in the order of the runs, by the CTA's eight warps (or, of many rows, by one)
+constexpr int kJoinWarps = 8;
+
+template <int kD, bool kE4M3, int kRG, int kNR>
+__global__ void __launch_bounds__(kJoinWarps * 32) k_attention_join(const __grid_constant__ AttentionArgs p, int row_a_warp)
+{
+    constexpr int kRows = 8 * kRG * kNR, kV = kD / 32;  // columns a lane: lane * kV ..
+    __shared__ float sm_o[kJoinWarps][kD], sm_ml[kJoinWarps][2];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int row = row_a_warp ? static_cast<int>(blockIdx.x) * kJoinWarps + warp : static_cast<int>(blockIdx.x);
+    // (the tables were there before the main launch began)
+    const int t = row / p.n_q, head = row - t * p.n_q, s = t < p.T ? find_request(p.r.seg_offsets, p.r.S, t) : -1;
+    Span a{};
+    bool bad = true;
+    if (s >= 0 && s < p.r.S) a = span_of<kRows>(p, s, bad);
+    const bool mine = a.segs != 0 && t < a.beg + a.n;
+    const int h = head / p.group, in_seg = (t - a.beg) * p.group + head % p.group, r = in_seg % kRows;
+    const int seg = in_seg / kRows * p.c.n_kv + h;
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    if (!mine) return;  // the same in all warps of a row
+    const int64_t u0 = p.prefix[s] + static_cast<int64_t>(seg) * (a.tiles + kExtra);
+    const Cut cut{p.prefix[p.r.S + 1], p.prefix[p.r.S + 2]};
+    const int c0 = cut.run(u0 + kExtra), n = cut.run(u0 + kExtra + a.tiles - 1) - c0 + 1;
+    if (n == 1) return;  // finished by its run
+    const bool from_start = cut.first(c0) >= u0;
+    auto slot_of = [&](int x) { return static_cast<int64_t>(c0 + x) * 2 + (x == 0 && !from_start ? 1 : 0); };
+
+    float mx = -INFINITY, sum = 0.0f, o[kV];
+#pragma unroll
+    for (int i = 0; i < kV; ++i) o[i] = 0.0f;
+    const int per = (n + kJoinWarps - 1) / kJoinWarps;
+    const int b = row_a_warp ? 0 : min(n, warp * per), e = row_a_warp ? n : min(n, b + per);
+    for (int i0 = b; i0 < e; i0 += 32) {
+        const int i = i0 + lane;
+        float2 ml = make_float2(-INFINITY, 0.0f);
+        if (i < e) ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + (slot_of(i) * kRows + r) * 2));
+        float top = ml.x;
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+        const float to = fmaxf(mx, top), by = to == -INFINITY ? 0.0f : to;
+        const float keep = exp2_fast(mx - by), w = exp2_fast(ml.x - by);
+        mx = to;
+        float part = w * ml.y;
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, x);
+        sum = sum * keep + part;
+#pragma unroll
+        for (int x = 0; x < kV; ++x) o[x] *= keep;
+        const int in = min(32, e - i0);
+        for (int x0 = 0; x0 < in; x0 += 8) {  // eight parts' loads in flight
+            float v[8][kV];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const float* from = p.part + (slot_of(i0 + x0 + x) * kRows + r) * kD + lane * kV;
+#pragma unroll
+                for (int y = 0; y < kV; ++y) v[x][y] = 0.0f;
+                if (x0 + x < in) {
+                    if constexpr (kV == 2) {
+                        *reinterpret_cast<float2*>(v[x]) = __ldcg(reinterpret_cast<const float2*>(from));
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < kV; y += 4) *reinterpret_cast<float4*>(v[x] + y) = __ldcg(reinterpret_cast<const float4*>(from + y));
+                    }
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const float wx = __shfl_sync(0xFFFFFFFFu, w, x0 + x);
+#pragma unroll
+                for (int y = 0; y < kV; ++y) o[y] += wx * v[x][y];
+            }
+        }
+    }
+    if (!row_a_warp) {
+#pragma unroll
+        for (int x = 0; x < kV; ++x) sm_o[warp][lane * kV + x] = o[x];
+        if (lane == 0) {
+            sm_ml[warp][0] = mx;
+            sm_ml[warp][1] = sum;
+        }
+        __syncthreads();
+        if (warp) return;
+        mx = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) mx = fmaxf(mx, sm_ml[w][0]);
+        const float by = mx == -INFINITY ? 0.0f : mx;
+        sum = 0.0f;
+#pragma unroll
+        for (int x = 0; x < kV; ++x) o[x] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+            const float f = exp2_fast(sm_ml[w][0] - by);
+            sum += f * sm_ml[w][1];
+#pragma unroll
+            for (int x = 0; x < kV; ++x) o[x] += f * sm_o[w][lane * kV + x];
+        }
+    }
+    float by = sum == 0.0f ? 0.0f : 1.0f / sum;
+    if (kE4M3 && p.c.v_scale) by *= __ldg(p.c.v_scale + h);
+    uint16_t* const to = p.out + static_cast<int64_t>(t) * p.ld_out + head * kD + lane * kV;
+#pragma unroll
+    for (int x = 0; x < kV; x += 2) *reinterpret_cast<uint32_t*>(to + x) = pack_bf16x2(o[x] * by, o[x + 1] * by);
+    if (p.lse && lane == 0) p.lse[row] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994530942f;
+}
+
+template <int kD, bool kE4M3, int kRG, int kNR>
+cudaError_t launch(const AttentionArgs& a, int sms, cudaStream_t stream)
+{
+    using S = Shape<kD, kE4M3, kRG, kNR>;
+    static bool set = false;
+    if (!set) {
+        cudaError_t e = cudaFuncSetAttribute(k_paged_attention<kD, kE4M3, kRG, kNR>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+        if (e != cudaSuccess) return e;
+        set = true;
+    }
+    const int ctas = sms * S::kCtas;
+    cudaError_t e = launch_pdl(k_paged_attention<kD, kE4M3, kRG, kNR>, dim3(ctas), dim3(S::kThreads), S::kSmem, stream, a);
+    if (e != cudaSuccess) return e;
+    // few rows: a CTA each (a long request's many parts are added by eight warps), else a warp each
+    const int64_t n = static_cast<int64_t>(a.T) * a.n_q;
+    const int row_a_warp = n > 512;
+    return launch_pdl(k_attention_join<kD, kE4M3, kRG, kNR>, dim3(static_cast<unsigned>(row_a_warp ? (n + kJoinWarps - 1) / kJoinWarps : n)),
+                      dim3(kJoinWarps * 32), 0, stream, a, row_a_warp);
+}
+
+template <int kD, bool kE4M3>
+cudaError_t launch_head_size(const AttentionArgs& a, int sms, cudaStream_t stream)
+{
+    switch (row_eights(a.group, a.max_new)) {
+    case 1: return launch<kD, kE4M3, 1, 1>(a, sms, stream);
+    case 2: return launch<kD, kE4M3, 2, 1>(a, sms, stream);
+    case 3: return launch<kD, kE4M3, 3, 1>(a, sms, stream);
+    case 4: return launch<kD, kE4M3, 2, 2>(a, sms, stream);
+    default: return launch<kD, kE4M3, 4, 2>(a, sms, stream);
+    }
+}
+
+}  // namespace attention
+}  // namespace moe

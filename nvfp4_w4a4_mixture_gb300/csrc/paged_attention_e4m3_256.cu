@@ -1,0 +1,10 @@
+// The attention kernels of a cache in e4m3 with heads of 256.
+#include "paged_attention.cuh"
+
+namespace moe {
+namespace attention {
+
+template cudaError_t launch_head_size<256, true>(const AttentionArgs&, int, cudaStream_t);
+
+}  // namespace attention
+}  // namespace moe
