@@ -110,6 +110,8 @@ def _load_calls(L):
             return
         mod.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (L.moe_norm_residual, L.moe_select_experts, L.moe_adapter_add)),
                  torch.bfloat16, torch.float32, torch.int32)
+        mod.bind_attention(*(ctypes.cast(f, ctypes.c_void_p).value for f in (L.moe_cache_append, L.moe_paged_attention, L.moe_quantize_fp8,
+                                                                             L.moe_gemm_fp8)), torch.float8_e4m3fn)
         _calls = mod
 
 
@@ -236,8 +238,9 @@ _adapter_ws = {}
 
 
 def _adapter_workspace():
-    """moe_adapter_add's workspace where the caller gives none: its header is all that the call uses, so it is never
-    replaced by a larger one, which would lose its report and leave captured calls with memory that was given back."""
+    """The workspace of moe_adapter_add, moe_cache_append and moe_gemm_fp8 where the caller gives none: its header is all that
+    they use, so it is never replaced by a larger one, which would lose its report and leave captured calls with memory
+    that was given back."""
     dev = torch.cuda.current_device()
     w = _adapter_ws.get(dev)
     if w is None:
@@ -688,6 +691,25 @@ def moe_cache_append(q, k, v, k_cache, v_cache, seg_offsets, kv_len, pages, inv_
     8-bit cache. out: optional, may be q. Requests that break the rules are reported by moe_read_device_status(ws)."""
     if _lib is None:
         lib()
+    if q is not None and out is None:
+        out = torch.empty(q.shape, dtype=_BF16, device=q.device)
+    status = -1
+    if k.is_cuda:
+        if ws is None:
+            ws = _adapter_workspace()
+        if _calls is not None:
+            status = _calls.cache_append(q, k, v, k_cache, v_cache, k_scale, v_scale, seg_offsets, kv_len, pages, inv_freq, interleaved,
+                                         w_q, w_k, eps, w_offset, out, ws.address, ws.nbytes, _stream())
+    if status < 0:
+        status = _cache_append(q, k, v, k_cache, v_cache, seg_offsets, kv_len, pages, inv_freq, interleaved, w_q, w_k, eps, w_offset,
+                               k_scale, v_scale, out, ws)
+    if status:
+        _check(status)
+    return out
+
+
+def _cache_append(q, k, v, k_cache, v_cache, seg_offsets, kv_len, pages, inv_freq, interleaved, w_q, w_k, eps, w_offset, k_scale,
+                  v_scale, out, ws):
     T, n_kv, D = k.shape
     k_ptr, k_ld = _heads(k, "k", _BF16, (T, n_kv, D))
     v_ptr, v_ld = _heads(v, "v", _BF16, (T, n_kv, D))
@@ -695,8 +717,6 @@ def moe_cache_append(q, k, v, k_cache, v_cache, seg_offsets, kv_len, pages, inv_
     if q is not None:
         n_q = q.shape[1]
         q_ptr, q_ld = _heads(q, "q", _BF16, (T, n_q, D))
-        if out is None:
-            out = torch.empty(T, n_q, D, dtype=_BF16, device=q.device)
         o_ptr, o_ld = _heads(out, "out", _BF16, (T, n_q, D))
     elif out is not None:
         raise ValueError("out without q")
@@ -708,23 +728,22 @@ def moe_cache_append(q, k, v, k_cache, v_cache, seg_offsets, kv_len, pages, inv_
     d = RotaryDesc(n_q, 2 * half, 1 if interleaved else 0, None if inv_freq is None else _whole(inv_freq, "inv_freq", _F32, (half,)),
                    None if w_q is None else _whole(w_q, "w_q", _BF16, (D,)), None if w_k is None else _whole(w_k, "w_k", _BF16, (D,)),
                    eps, w_offset)
-    if ws is None:
-        ws = _adapter_workspace()
-    _check(lib().moe_cache_append(_cache_desc(k_cache, v_cache, k_scale, v_scale), _requests_desc(seg_offsets, kv_len, pages), d, q_ptr,
-                                  q_ld, k_ptr, k_ld, v_ptr, v_ld, T, o_ptr, o_ld, ws.address, ws.nbytes, _stream()))
-    return out
+    return lib().moe_cache_append(_cache_desc(k_cache, v_cache, k_scale, v_scale), _requests_desc(seg_offsets, kv_len, pages), d, q_ptr,
+                                  q_ld, k_ptr, k_ld, v_ptr, v_ld, T, o_ptr, o_ld, ws.address, ws.nbytes, _stream())
 
 
 _attention_ws = {}
 
 
-def _attention_workspace(nbytes):
+def _attention_workspace(S, n_q, n_kv, D, max_new):
     """moe_paged_attention's workspace where the caller gives none: one for each stream, since calls on two streams run
     at the same time. A capture's belongs to its graph (the memory is the graph's, its report is lost)."""
-    stream = _stream()
+    if not isinstance(max_new, int) or not 0 <= max_new <= _INT_MAX:
+        raise ValueError("max_new is an int of 32 bits")
+    nbytes = _lib.moe_attention_workspace_bytes(S, n_q, n_kv, D, max_new)
     if torch.cuda.is_current_stream_capturing():
         return Workspace(nbytes)
-    key = torch.cuda.current_device(), stream
+    key = torch.cuda.current_device(), _stream()
     w = _attention_ws.get(key)
     if w is None or w.nbytes < nbytes:
         old, w = w, Workspace(nbytes)
@@ -742,20 +761,30 @@ def moe_paged_attention(q, k_cache, v_cache, seg_offsets, kv_len, pages, max_new
     optional, may be q. A row that sees nothing gets 0 (lse: -inf)."""
     if _lib is None:
         lib()
-    T, n_q, D = q.shape
-    n_kv = k_cache.shape[2]
-    if k_cache.shape[3] != D:
-        raise ValueError("k_cache of %s for q of %s" % (tuple(k_cache.shape), tuple(q.shape)))
-    q_ptr, q_ld = _heads(q, "q", _BF16, (T, n_q, D))
     if out is None:
-        out = torch.empty(T, n_q, D, dtype=_BF16, device=q.device)
-    o_ptr, o_ld = _heads(out, "out", _BF16, (T, n_q, D))
-    r = _requests_desc(seg_offsets, kv_len, pages)
-    if ws is None:
-        ws = _attention_workspace(lib().moe_attention_workspace_bytes(r.S, n_q, n_kv, D, max_new))
-    _check(lib().moe_paged_attention(_cache_desc(k_cache, v_cache, k_scale, v_scale), r,
-                                     AttentionDesc(n_q, max_new, window, D ** -0.5 if scale is None else scale), q_ptr, q_ld, T, o_ptr, o_ld,
-                                     None if lse is None else _whole(lse, "lse", _F32, (T, n_q)), ws.address, ws.nbytes, _stream()))
+        out = torch.empty(q.shape, dtype=_BF16, device=q.device)
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    status = -1
+    if q.is_cuda:
+        if ws is None:
+            ws = _attention_workspace(kv_len.shape[0], q.shape[1], k_cache.shape[2], k_cache.shape[3], max_new)
+        if _calls is not None:
+            status = _calls.paged_attention(q, k_cache, v_cache, k_scale, v_scale, seg_offsets, kv_len, pages, max_new, scale, window, out,
+                                            lse, ws.address, ws.nbytes, _stream())
+    if status < 0:
+        T, n_q, D = q.shape
+        if k_cache.shape[3:] != (D,):
+            raise ValueError("k_cache of %s for q of %s" % (tuple(k_cache.shape), tuple(q.shape)))
+        if any(not -_INT_MAX <= v <= _INT_MAX for v in (max_new, window)):
+            raise ValueError("max_new and window are ints of 32 bits")
+        q_ptr, q_ld = _heads(q, "q", _BF16, (T, n_q, D))
+        o_ptr, o_ld = _heads(out, "out", _BF16, (T, n_q, D))
+        status = lib().moe_paged_attention(_cache_desc(k_cache, v_cache, k_scale, v_scale), _requests_desc(seg_offsets, kv_len, pages),
+                                           AttentionDesc(n_q, max_new, window, scale), q_ptr, q_ld, T, o_ptr, o_ld,
+                                           None if lse is None else _whole(lse, "lse", _F32, (T, n_q)), ws.address, ws.nbytes, _stream())
+    if status:
+        _check(status)
     return out
 
 
@@ -765,26 +794,47 @@ def moe_quantize_fp8(x, out=None):
     T, K = x.shape
     if out is None:
         out = torch.empty(T, K, dtype=_E4M3, device=x.device), torch.empty(T, (K + 127) // 128, dtype=_F32, device=x.device)
-    x_ptr, x_ld = _rows(x, "x", _BF16, (T, K))
-    _check(lib().moe_quantize_fp8(x_ptr, x_ld, T, K, _whole(out[0], "codes", _E4M3, (T, K)),
-                                  _whole(out[1], "scales", _F32, (T, (K + 127) // 128)), _stream()))
+    if _lib is None:
+        lib()
+    status = -1
+    if _calls is not None and x.is_cuda:
+        status = _calls.quantize_fp8(x, out[0], out[1], _stream())
+    if status < 0:
+        status = _quantize_fp8(x, out)
+    if status:
+        _check(status)
     return out
+
+
+def _quantize_fp8(x, out):
+    T, K = x.shape
+    x_ptr, x_ld = _rows(x, "x", _BF16, (T, K))
+    return lib().moe_quantize_fp8(x_ptr, x_ld, T, K, _whole(out[0], "codes", _E4M3, (T, K)),
+                                  _whole(out[1], "scales", _F32, (T, (K + 127) // 128)), _stream())
 
 
 def moe_gemm_fp8(a, a_scale, b, b_scale, out=None, dtype=torch.bfloat16, ws=None):
     """a [T, K] times b [N, K] transposed, both float8_e4m3fn with a scale for each block of 128: a_scale fp32
     [T, ceil(K / 128)] (moe_quantize_fp8's), b_scale fp32 [ceil(N / 128), ceil(K / 128)]. out: optional bf16 or fp32 [T, N], rows
     may be strided; dtype: the type of one that is allocated."""
-    T, K = a.shape
-    N = b.shape[0]
+    if _lib is None:
+        lib()
     if out is None:
-        out = torch.empty(T, N, dtype=dtype, device=a.device)
-    f32 = out.dtype is _F32
-    o_ptr, o_ld = _rows(out, "out", _F32 if f32 else _BF16, (T, N))
-    if ws is None:
-        ws = _adapter_workspace()
-    kb = (K + 127) // 128
-    _check(lib().moe_gemm_fp8(_whole(a, "a", _E4M3, (T, K)), _whole(a_scale, "a_scale", _F32, (T, kb)), _whole(b, "b", _E4M3, (N, K)),
-                              _whole(b_scale, "b_scale", _F32, ((N + 127) // 128, kb)), T, N, K, o_ptr, DTYPE_F32 if f32 else DTYPE_BF16,
-                              o_ld, ws.address, ws.nbytes, _stream()))
+        out = torch.empty(a.shape[0], b.shape[0], dtype=dtype, device=a.device)
+    status = -1
+    if a.is_cuda:
+        if ws is None:
+            ws = _adapter_workspace()
+        if _calls is not None:
+            status = _calls.gemm_fp8(a, a_scale, b, b_scale, out, ws.address, ws.nbytes, _stream())
+    if status < 0:
+        T, K = a.shape
+        N, kb, f32 = b.shape[0], (K + 127) // 128, out.dtype is _F32
+        a_ptr, as_ptr = _whole(a, "a", _E4M3, (T, K)), _whole(a_scale, "a_scale", _F32, (T, kb))
+        b_ptr, bs_ptr = _whole(b, "b", _E4M3, (N, K)), _whole(b_scale, "b_scale", _F32, ((N + 127) // 128, kb))
+        o_ptr, o_ld = _rows(out, "out", _F32 if f32 else _BF16, (T, N))
+        status = lib().moe_gemm_fp8(a_ptr, as_ptr, b_ptr, bs_ptr, T, N, K, o_ptr, DTYPE_F32 if f32 else DTYPE_BF16, o_ld, ws.address,
+                                    ws.nbytes, _stream())
+    if status:
+        _check(status)
     return out

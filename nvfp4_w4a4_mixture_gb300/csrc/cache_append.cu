@@ -1,8 +1,9 @@
 // cache_append.cu -- norm, rotation by position and append to the paged cache, one launch:
 //   u = x rsqrt(mean(x^2) + eps) (off + w);  (a, b) -> (a cos - b sin, a sin + b cos), angle p inv_freq[i]
-// A head of D elements is in the registers of D / 8 lanes (16 bytes each) from its load to its store: the norm's sum and
-// the rotation's partner come by shuffles. The angle is a 64-bit fraction of a turn: inv_freq / 2 pi in 2^-64 turns
-// (one FP64 product, off by 2^-54 of it), times the position modulo 2^64, which drops whole turns exactly, so the
+// A warp takes the heads of one token (of few tokens, some of them), 256 elements a pass: a head of D elements is in the
+// registers of D / 8 lanes (16 bytes each) from its load to its store, the norm's sum and the rotation's partner come by
+// shuffles. The angle is a 64-bit fraction of a turn: inv_freq / 2 pi in 2^-64
+// turns (one FP64 product, off by 2^-54 of it), times the position modulo 2^64, which drops whole turns exactly, so the
 // angle of position 2^20 is as good as that of position 1; sine and cosine of what is left are FP32's.
 #include "attention.cuh"
 
@@ -10,144 +11,229 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kWarps = 4;
 
-__device__ __forceinline__ float bf16_at(const uint4& v, int i)
+// ---- two FP32 values an instruction
+__device__ __forceinline__ uint64_t pair(float lo, float hi) { return static_cast<uint64_t>(__float_as_uint(hi)) << 32 | __float_as_uint(lo); }
+__device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
 {
-    const uint32_t w = i / 2 == 0 ? v.x : i / 2 == 1 ? v.y : i / 2 == 2 ? v.z : v.w;
-    return i % 2 ? __uint_as_float(w & 0xFFFF0000u) : __uint_as_float(w << 16);
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// two bf16 values as FP32
+__device__ __forceinline__ uint64_t widen(uint32_t w) { return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+// f / 2 pi modulo one turn, in 2^-64 turns, for a finite f: its 24 bits times 2^96 / 2 pi (94 bits), shifted. Cut, not
+// rounded: off by less than 2^-64 turns. (In integers: a multiprocessor has few units for FP64.)
+__device__ __forceinline__ uint64_t turns_of(float f)
+{
+    constexpr uint64_t kHigh = 0x28be60db9391054aull, kLow = 0x7f09d5f4ull;  // floor(2^96 / 2 pi)
+    const uint32_t bits = __float_as_uint(f), e = bits >> 23 & 0xFFu;
+    const uint64_t m = e ? (bits & 0x7FFFFFu) | 0x800000u : bits & 0x7FFFFFu;  // |f| = m 2^(max(e, 1) - 150)
+    const uint64_t low = m * kLow, mid = m * kHigh;
+    const uint64_t t0 = (mid << 32) + low, t1 = (__umul64hi(m, kHigh) << 32) + (mid >> 32) + (t0 < low);  // m 2^96 / 2 pi
+    const int shift = 32 + 150 - static_cast<int>(e ? e : 1);
+    const uint64_t r = shift >= 128 ? 0 : shift >= 64 ? t1 >> (shift - 64) : shift > 0 ? t0 >> shift | t1 << (64 - shift) : shift > -64 ? t0 << -shift : 0;
+    return bits >> 31 ? 0 - r : r;
+}
+
+enum Kind : int { kQuery, kKey, kValue };
+
+// What a warp knows of its token and its lanes.
+template <int kD>
+struct Token {
+    int64_t place;           // in the cache, -1: none
+    bool turns, low;         // this lane's elements are rotated; they are the first of their pairs (half-split)
+    int partner;             // the lane that holds the others of their pairs
+    uint64_t cos[4], sin[4]; // of this lane's elements, the sine with the sign that its term has
+};
+
+// Passes [first, last) of a token's queries, keys or values (n heads from `from` on; a pass is 32 lanes times 8 elements,
+// whole heads), kN at a time, side by side: their shuffles and roots take turns. x: the first kN's loads, or null.
+template <int kD, bool kE4M3, Kind kKind, int kN>
+__device__ __forceinline__ void heads(const AppendArgs& p, const Token<kD>& k, const uint16_t* from, uint16_t* out, const uint16_t* w, int n,
+                                      int first, int last, const uint4* x0)
+{
+    constexpr int kLanes = kD / 8;
+    const int lane = threadIdx.x % 32, c0 = lane % kLanes * 8, elements = n * kD;
+    const int64_t head_ld = p.c.ld_head;
+    uint64_t wf[4];
+    if (kKind != kValue && w) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(w + c0));
+        const uint64_t off = pair(p.w_offset, p.w_offset), one = pair(1.0f, 1.0f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) wf[j] = fma2(widen(word(v, j)), one, off);
+    }
+    auto load = [&](int pass) {
+        const int e = pass * 256 + lane * 8;
+        return pass < last && e < elements ? *reinterpret_cast<const uint4*>(from + e) : make_uint4(0, 0, 0, 0);
+    };
+    uint4 next[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) next[i] = x0 ? x0[i] : load(first + i);
+    for (int pass = first; pass < last; pass += kN) {
+        uint4 x[kN];
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            x[i] = next[i];
+            next[i] = load(pass + kN + i);
+        }
+        uint64_t f[kN][4];
+        if constexpr (kKind != kValue || kE4M3) {
+#pragma unroll
+            for (int i = 0; i < kN; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[i][j] = widen(word(x[i], j));
+        }
+        if constexpr (kKind != kValue) {
+            if (w) {
+                float sum[kN];
+#pragma unroll
+                for (int i = 0; i < kN; ++i) {
+                    uint64_t s = mul2(f[i][0], f[i][0]);
+#pragma unroll
+                    for (int j = 1; j < 4; ++j) s = fma2(f[i][j], f[i][j], s);
+                    sum[i] = lo_of(s) + hi_of(s);
+                }
+#pragma unroll
+                for (int o = kLanes / 2; o > 0; o >>= 1)
+#pragma unroll
+                    for (int i = 0; i < kN; ++i) sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], o);
+#pragma unroll
+                for (int i = 0; i < kN; ++i) {
+                    const float r = rsqrtf(sum[i] * (1.0f / kD) + p.eps);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) f[i][j] = mul2(mul2(f[i][j], pair(r, r)), wf[j]);
+                }
+            }
+            if (p.rot) {
+#pragma unroll
+                for (int i = 0; i < kN; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float a = lo_of(f[i][j]), b = hi_of(f[i][j]);
+                        const uint64_t other = p.interleaved ? pair(b, a)
+                                                             : pair(__shfl_sync(0xFFFFFFFFu, a, k.partner), __shfl_sync(0xFFFFFFFFu, b, k.partner));
+                        const uint64_t turned = fma2(f[i][j], k.cos[j], mul2(other, k.sin[j]));
+                        f[i][j] = k.turns ? turned : f[i][j];
+                    }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const int e = (pass + i) * 256 + lane * 8, head = e / kD;
+            if (pass + i >= last || e >= elements || (kKind != kQuery && k.place < 0)) continue;
+            const int64_t at = k.place + head * head_ld + c0;
+            if constexpr (kKind != kQuery && kE4M3) {
+                const float* sc = kKind == kValue ? p.c.v_scale : p.c.k_scale;
+                const float d = sc ? __ldg(sc + head) : 1.0f;
+                uint32_t b[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) b[j] = ptx::cvt_e4m3x2(__fdiv_rn(lo_of(f[i][j]), d), __fdiv_rn(hi_of(f[i][j]), d));
+                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(kKind == kValue ? p.c.v : p.c.k) + at) = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+            } else {
+                uint4 v = x[i];
+                if constexpr (kKind != kValue)
+                    v = make_uint4(pack_bf16x2(lo_of(f[i][0]), hi_of(f[i][0])), pack_bf16x2(lo_of(f[i][1]), hi_of(f[i][1])),
+                                   pack_bf16x2(lo_of(f[i][2]), hi_of(f[i][2])), pack_bf16x2(lo_of(f[i][3]), hi_of(f[i][3])));
+                uint16_t* const to = kKind == kQuery ? out + e : static_cast<uint16_t*>(kKind == kValue ? p.c.v : p.c.k) + at;
+                *reinterpret_cast<uint4*>(to) = v;
+            }
+        }
+    }
 }
 
 template <int kD, bool kE4M3>
-__global__ void __launch_bounds__(kThreads) k_cache_append(const __grid_constant__ AppendArgs p, int heads_per_cta)
+__global__ void __launch_bounds__(kWarps * 32) k_cache_append(const __grid_constant__ AppendArgs p, int passes, int chunks)
 {
-    constexpr int kLanes = kD / 8, kHeads = kThreads / kLanes;  // lanes a head, heads a pass
-    __shared__ float2 turn[kD / 2];
-    const int tid = threadIdx.x, at = tid % kLanes, c0 = at * 8, half = p.rot / 2;
-    const int n_all = p.n_q + 2 * p.c.n_kv;
-    const int64_t t = blockIdx.x;
-    const int h0 = blockIdx.y * heads_per_cta, h1 = min(n_all, h0 + heads_per_cta);
+    constexpr int kLanes = kD / 8, kN = 2;
+    __shared__ float2 turn_of[kWarps][kD / 2];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, at = lane % kLanes, c0 = at * 8, half = p.rot / 2;
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * kWarps + warp, t = id / chunks;
+    const int chunk = static_cast<int>(id - t * chunks);
+    float2* const turn = turn_of[warp];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
 
-    auto load = [&](int h) -> uint4 {
-        if (h >= h1) return make_uint4(0, 0, 0, 0);
-        const uint16_t* x = h < p.n_q                ? p.q + t * p.ld_q + h * kD
-                            : h < p.n_q + p.c.n_kv ? p.k + t * p.ld_k + (h - p.n_q) * kD
-                                                     : p.v + t * p.ld_v + (h - p.n_q - p.c.n_kv) * kD;
-        return *reinterpret_cast<const uint4*>(x + c0);
-    };
-    int h = h0 + tid / kLanes;
-    uint4 x = load(h);
-
     // the requests' rules, by the first CTA
-    if (blockIdx.x == 0 && blockIdx.y == 0)
-        for (int s = tid; s < p.r.S; s += kThreads) {
+    if (blockIdx.x == 0)
+        for (int s = threadIdx.x; s < p.r.S; s += kWarps * 32) {
             bool bad;
             load_request(p.r, s, p.T, p.T, bad);
             if (bad) record_status(p.status, kDevBadRequest);
         }
+    if (t >= p.T) return;
+    // this warp's passes [first, last) of all of the token's: of its queries, then its keys, then its values
+    const int nq = p.n_q * kD, nk = p.c.n_kv * kD, q_passes = (nq + 255) / 256, k_passes = (nk + 255) / 256;
+    const int first = chunk * passes, last = min(q_passes + 2 * k_passes, first + passes);
+    const uint16_t *q = p.q + t * p.ld_q, *k = p.k + t * p.ld_k, *v = p.v + t * p.ld_v;
+    uint4 x[kN];  // the first of them, if queries
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        const int e = (first + i) * 256 + lane * 8;
+        x[i] = first + i < min(last, q_passes) && e < nq ? *reinterpret_cast<const uint4*>(q + e) : make_uint4(0, 0, 0, 0);
+    }
+    uint64_t step[kD / 64];  // turns a position of the frequencies lane, lane + 32, ..
+#pragma unroll
+    for (int i = 0; i < kD / 64; ++i) step[i] = lane + 32 * i < half ? turns_of(__ldg(p.inv_freq + lane + 32 * i)) : 0;
+
     const int s = find_request(p.r.seg_offsets, p.r.S, static_cast<int>(t));
     if (s < 0 || s >= p.r.S) return;  // behind the last request
     bool bad;
     const Request r = load_request(p.r, s, p.T, p.T, bad);
     const int pos = r.len - r.n + static_cast<int>(t - r.beg);
     if (r.n == 0 || t >= r.beg + r.n || pos < 0) return;
-    int64_t page = __ldg(p.r.pages + s * p.r.ld_pages + (pos >> p.c.page_log2));
+    const int page = __ldg(p.r.pages + s * p.r.ld_pages + (pos >> p.c.page_log2));
+#pragma unroll
+    for (int i = 0; i < kD / 64; ++i)
+        if (lane + 32 * i < half) {
+            float sn, cs;
+            sincospif(static_cast<float>(static_cast<int64_t>(step[i] * static_cast<uint64_t>(pos))) * 0x1p-63f, &sn, &cs);
+            turn[lane + 32 * i] = make_float2(cs, sn);
+        }
+    __syncwarp();
+    Token<kD> tok;
+    tok.turns = c0 < p.rot;
+    tok.low = c0 < half;
+    tok.partner = lane - at + (!tok.turns || p.interleaved ? at : tok.low ? at + half / 8 : at - half / 8);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int c = tok.turns ? c0 + 2 * j : 0;
+        const int f0 = p.interleaved ? c / 2 : c < half ? c : c - half, f1 = p.interleaved ? c / 2 : f0 + 1;
+        const float2 a = half ? turn[f0] : make_float2(1.0f, 0.0f), b = half ? turn[f1] : a;
+        tok.cos[j] = pair(a.x, b.x);
+        tok.sin[j] = p.interleaved ? pair(-a.y, b.y) : tok.low ? pair(-a.y, -b.y) : pair(a.y, b.y);
+    }
+    tok.place = page * p.c.ld_page + (pos & ((1 << p.c.page_log2) - 1)) * p.c.ld_slot;
     if (page < 0 || page >= p.c.n_pages) {
-        page = -1;
-        if (tid == 0) record_status(p.status, kDevBadPage);
+        tok.place = -1;
+        if (lane == 0) record_status(p.status, kDevBadPage);
     }
-    const int64_t place = page * p.c.ld_page + (pos & ((1 << p.c.page_log2) - 1)) * p.c.ld_slot;
-
-    if (tid < half) {
-        double f = static_cast<double>(__ldg(p.inv_freq + tid)) * 0.15915494309189533577;  // turns a position
-        f -= floor(f);
-        const uint64_t phase = static_cast<uint64_t>(f * 18446744073709551616.0) * static_cast<uint64_t>(pos);
-        float sn, cs;
-        sincospif(static_cast<float>(static_cast<int64_t>(phase)) * 0x1p-63f, &sn, &cs);
-        turn[tid] = make_float2(cs, sn);
-    }
-    __syncthreads();
-    float2 cs[8];  // of this lane's elements (interleaved: of its four pairs)
-    const bool turns = c0 < p.rot;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int c = c0 + i, f = p.interleaved ? c / 2 : c < half ? c : c - half;
-        cs[i] = turns ? turn[f] : make_float2(1.0f, 0.0f);
-    }
-    const bool low = c0 < half;
-    const int partner = !turns || p.interleaved ? at : low ? at + half / 8 : at - half / 8;
-
-    for (; h - tid / kLanes < h1; h += kHeads) {
-        const uint4 cur = x;
-        x = load(h + kHeads);
-        const bool is_q = h < p.n_q, is_v = h >= p.n_q + p.c.n_kv;
-        float f[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = bf16_at(cur, i);
-        const uint16_t* w = is_q ? p.w_q : p.w_k;
-        float sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum = fmaf(f[i], f[i], sum);
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        if (!is_v && w) {
-            const float rs = rsqrtf(sum * (1.0f / kD) + p.eps);
-            const uint4 wv = __ldg(reinterpret_cast<const uint4*>(w + c0));
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = f[i] * rs * (p.w_offset + bf16_at(wv, i));
-        }
-        float o[8];
-        if (p.interleaved) {
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                o[i] = f[i] * cs[i].x - f[i + 1] * cs[i].y;
-                o[i + 1] = f[i] * cs[i].y + f[i + 1] * cs[i].x;
-            }
-        } else {
-            const int lane = (tid & 31) - at + partner;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float other = __shfl_sync(0xFFFFFFFFu, f[i], lane);
-                o[i] = low ? f[i] * cs[i].x - other * cs[i].y : other * cs[i].y + f[i] * cs[i].x;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (!turns || is_v) o[i] = f[i];
-        if (h >= h1) continue;
-        if (is_q) {
-            const uint4 v = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
-            *reinterpret_cast<uint4*>(p.q_out + t * p.ld_q_out + h * kD + c0) = v;
-        } else if (page >= 0) {
-            const int kv = is_v ? h - p.n_q - p.c.n_kv : h - p.n_q;
-            const int64_t e = place + kv * p.c.ld_head + c0;
-            void* base = is_v ? p.c.v : p.c.k;
-            if constexpr (kE4M3) {
-                const float* sc = is_v ? p.c.v_scale : p.c.k_scale;
-                const float d = sc ? __ldg(sc + kv) : 1.0f;
-                uint32_t b[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) b[i] = ptx::cvt_e4m3x2(__fdiv_rn(o[2 * i], d), __fdiv_rn(o[2 * i + 1], d));
-                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(base) + e) = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
-            } else {
-                const uint4 v = is_v ? cur
-                                     : make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + e) = v;
-            }
-        }
-    }
+    heads<kD, kE4M3, kQuery, kN>(p, tok, q, p.q_out + t * p.ld_q_out, p.w_q, p.n_q, first, min(last, q_passes), x);
+    heads<kD, kE4M3, kKey, kN>(p, tok, k, nullptr, p.w_k, p.c.n_kv, max(first - q_passes, 0), min(last - q_passes, k_passes), nullptr);
+    heads<kD, kE4M3, kValue, kN>(p, tok, v, nullptr, nullptr, p.c.n_kv, max(first - q_passes - k_passes, 0), last - q_passes - k_passes, nullptr);
 }
 
 template <int kD, bool kE4M3>
 cudaError_t launch(const AppendArgs& a, int sms, cudaStream_t stream)
 {
-    constexpr int kHeads = kThreads / (kD / 8);
-    const int n_all = a.n_q + 2 * a.c.n_kv, passes = (n_all + kHeads - 1) / kHeads;
-    // few tokens: their heads over more CTAs, a pass each
-    const int per = a.T * static_cast<int64_t>(passes) <= sms * 4LL ? kHeads : n_all;
-    return launch_pdl(k_cache_append<kD, kE4M3>, dim3(a.T, (n_all + per - 1) / per), dim3(kThreads), 0, stream, a, per);
+    const int passes_all = (a.n_q * kD + 255) / 256 + 2 * ((a.c.n_kv * kD + 255) / 256);
+    // a warp a token; of few tokens as many warps as 16 an SM are, a pass each at the least
+    const int64_t per = static_cast<int64_t>(a.T) * passes_all / (sms * 16LL);
+    const int passes = static_cast<int>(per < 1 ? 1 : per > passes_all ? passes_all : per), chunks = (passes_all + passes - 1) / passes;
+    const int64_t ctas = (static_cast<int64_t>(a.T) * chunks + kWarps - 1) / kWarps;
+    if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    return launch_pdl(k_cache_append<kD, kE4M3>, dim3(static_cast<unsigned>(ctas)), dim3(kWarps * 32), 0, stream, a, passes, chunks);
 }
 
 template <bool kE4M3>
