@@ -35,48 +35,36 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N)
     return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// Warp-wide: this warp's 32 lanes x 32 consecutive 32-bit columns.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-}
-
-// Two FP32 sums by one instruction: acc += v * s.
+// Two FP32 sums by one instruction: acc += v * s. (Volatile: it stays behind the wait for the load of v.)
 __device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) { return static_cast<uint64_t>(hi) << 32 | lo; }
-__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t v, uint64_t s) { asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(s)); }
+__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t v, uint64_t s) { asm volatile("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(s)); }
 __device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
 __device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
 
 // ------------------------------------------------------------------------------------------------
 // many tokens
 // ------------------------------------------------------------------------------------------------
-constexpr int kBigM = 128, kBigN = 256, kBigStages = 4, kBigThreads = 320, kEpiWarps = 8;
+constexpr int kBigM = 128, kBigN = 256, kBigStages = 4, kBigThreads = 320, kEpiWarps = 8, kFirstEpi = 2;
 constexpr int kBigA = kBigM * 128, kBigStage = kBigA + kBigN * 128;
+constexpr int kOutBox = 32 * 128;  // a warp's piece of the output: 32 rows of 128 bytes
 
 struct BigTail {
     uint64_t full[kBigStages], empty[kBigStages], acc_full[2], acc_empty[2], drain;
     uint32_t tmem;
     int abort;
 };
-constexpr size_t kBigSmem = 1024 + static_cast<size_t>(kBigStages) * kBigStage + sizeof(BigTail);
+constexpr size_t kBigSmem = 1024 + static_cast<size_t>(kBigStages) * kBigStage + kEpiWarps * kOutBox + sizeof(BigTail);
 static_assert(kBigSmem <= kSmemMax, "shared memory");
 
 template <bool kF32>
 __global__ void __launch_bounds__(kBigThreads, 1)
-    k_gemm_fp8(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const __grid_constant__ GemmFp8Args p,
-               int n_tiles_n, int n_tiles)
+    k_gemm_fp8(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_out,
+               const __grid_constant__ GemmFp8Args p, int n_tiles_n, int n_tiles)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    BigTail& st = *reinterpret_cast<BigTail*>(smem + kBigStages * kBigStage);
+    uint8_t* obuf = smem + kBigStages * kBigStage;  // [epilogue warp]
+    BigTail& st = *reinterpret_cast<BigTail*>(obuf + kEpiWarps * kOutBox);
     const int tid = threadIdx.x, warp = __reduce_max_sync(0xFFFFFFFFu, tid / 32), lane = tid % 32;
     const int nk = (p.K + 127) / 128;
     if (tid == 0) {
@@ -159,7 +147,7 @@ __global__ void __launch_bounds__(kBigThreads, 1)
             ptx::mbar_wait(&st.drain, 0);
         }
     } else {
-        const int ew = warp - 2, grp = ew / 4, q = warp & 3;
+        const int ew = warp - kFirstEpi, grp = ew / 4, q = warp & 3;
         const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16) + grp * 128;
         uint32_t it = 0;
         bool ok = true;
@@ -171,51 +159,68 @@ __global__ void __launch_bounds__(kBigThreads, 1)
             uint64_t acc[64];
 #pragma unroll
             for (int i = 0; i < 64; ++i) acc[i] = 0;
-            float f = __ldg(sa) * __ldg(sb);
+            // the scales come a block ahead
+            float fa = __ldg(sa), fb = __ldg(sb);
             for (int kb = 0; kb < nk; ++kb, ++it) {
                 const uint32_t buf = it & 1;
-                const uint32_t fb = __float_as_uint(f);
-                const uint64_t ff = pair(fb, fb);
-                if (kb + 1 < nk) f = __ldg(sa + kb + 1) * __ldg(sb + kb + 1);
+                const uint32_t f = __float_as_uint(fa * fb);
+                const uint64_t ff = pair(f, f);
+                if (kb + 1 < nk) {
+                    fa = __ldg(sa + kb + 1);
+                    fb = __ldg(sb + kb + 1);
+                }
                 ok = all(ptx::mbar_wait_near(&st.acc_full[buf], (it >> 1) & 1));
                 if (!ok) break;
                 ptx::tc_fence_after();
+                // 16 columns at a time, the next ones' load in flight while some are scaled and added
+                uint32_t v[2][16];
+                ptx::tmem_ld16(tq + buf * kBigN, v[0]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t v[32];
-                    tmem_ld32(tq + buf * kBigN + c * 32, v);
+                for (int c = 0; c < 8; ++c) {
                     ptx::tmem_ld_wait();
-                    if (c == 3) {
+                    if (c < 7) {
+                        ptx::tmem_ld16(tq + buf * kBigN + (c + 1) * 16, v[(c + 1) & 1]);
+                    } else {
                         ptx::tc_fence_before();
                         __syncwarp();
                         if (lane == 0) ptx::mbar_arrive(&st.acc_empty[buf]);
                     }
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) fma2(acc[c * 16 + i], pair(v[2 * i], v[2 * i + 1]), ff);
+                    for (int i = 0; i < 8; ++i) fma2(acc[c * 8 + i], pair(v[c & 1][2 * i], v[c & 1][2 * i + 1]), ff);
                 }
             }
             if (!ok) break;
-            if (row < p.T) {
-                const int64_t at = static_cast<int64_t>(row) * p.ld_out + col;
-                if constexpr (kF32) {
-                    float* out = static_cast<float*>(p.out) + at;
+            // the rows go out in pieces of 128 bytes, by way of shared memory: one copy of 32 of them, which clips at T and N
+            constexpr int kCols = kF32 ? 32 : 64;  // of a piece
+            const uint32_t ob = ptx::smem_u32(obuf + ew * kOutBox);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (col + 4 * i < p.N)
-                            *reinterpret_cast<float4*>(out + 4 * i) = make_float4(lo_of(acc[2 * i]), hi_of(acc[2 * i]), lo_of(acc[2 * i + 1]), hi_of(acc[2 * i + 1]));
-                } else {
-                    uint16_t* out = static_cast<uint16_t*>(p.out) + at;
+            for (int h = 0; h < 128 / kCols; ++h) {
+                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the copy before has read the buffer
+                __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (col + 8 * i < p.N) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) w[x] = pack_bf16x2(lo_of(acc[4 * i + x]), hi_of(acc[4 * i + x]));
-                            *reinterpret_cast<uint4*>(out + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
+                for (int i = 0; i < 8; ++i) {
+                    uint4 w;
+                    if constexpr (kF32) {
+                        const uint64_t u = acc[h * 16 + 2 * i], v = acc[h * 16 + 2 * i + 1];
+                        w = make_uint4(static_cast<uint32_t>(u), static_cast<uint32_t>(u >> 32), static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32));
+                    } else {
+                        const uint64_t* a = acc + h * 32 + 4 * i;
+                        w = make_uint4(pack_bf16x2(lo_of(a[0]), hi_of(a[0])), pack_bf16x2(lo_of(a[1]), hi_of(a[1])),
+                                       pack_bf16x2(lo_of(a[2]), hi_of(a[2])), pack_bf16x2(lo_of(a[3]), hi_of(a[3])));
+                    }
+                    ptx::shared_store16(ob + lane * 128 + ((i ^ (lane & 7)) << 4), w);  // as the 128-byte swizzle has it
+                }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0 && col + h * kCols < p.N && tm * kBigM + q * 32 < p.T) {
+                    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];"
+                                 ::"l"(reinterpret_cast<uint64_t>(&map_out)), "r"(col + h * kCols), "r"(tm * kBigM + q * 32), "r"(ob)
+                                 : "memory");
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                 }
             }
         }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         if (!ok) fail();
     }
     ptx::tc_fence_before();
@@ -444,12 +449,13 @@ cudaError_t launch_big(const GemmFp8Args& p, int sms, cudaStream_t stream)
         if (e != cudaSuccess) return e;
         set = true;
     }
-    CUtensorMap a, b;
-    if (!maps(p, &a, &b, kBigM, kBigN)) return cudaErrorInvalidValue;
+    CUtensorMap a, b, out;
+    if (!maps(p, &a, &b, kBigM, kBigN) || encode_tmap_2d_out(&out, p.out, kF32, p.N, p.T, p.ld_out, kF32 ? 32 : 64, 32) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
     const int tn = (p.N + kBigN - 1) / kBigN, tm = (p.T + kBigM - 1) / kBigM;
     const int64_t tiles = static_cast<int64_t>(tn) * tm;
     if (tiles > 0x7FFFFFFF - 65536) return cudaErrorInvalidValue;
-    return launch_pdl(k_gemm_fp8<kF32>, dim3(tiles < sms ? static_cast<int>(tiles) : sms), dim3(kBigThreads), kBigSmem, stream, a, b, p, tn,
+    return launch_pdl(k_gemm_fp8<kF32>, dim3(tiles < sms ? static_cast<int>(tiles) : sms), dim3(kBigThreads), kBigSmem, stream, a, b, out, p, tn,
                       static_cast<int>(tiles));
 }
 
@@ -467,7 +473,7 @@ cudaError_t launch_few(const GemmFp8Args& p, int sms, cudaStream_t stream)
     const int tt = (p.T + kN - 1) / kN, tn = (p.N + kFewM - 1) / kFewM, nk = (p.K + 127) / 128;
     const int64_t tiles = static_cast<int64_t>(tt) * tn;
     int cs = 1;
-    while (cs < 8 && tiles * cs * 2 <= sms && cs * 2 <= nk) cs *= 2;
+    while (cs < 8 && tiles * cs * 2 <= sms * (kN == 64 ? 1 : 2) && cs * 2 <= nk) cs *= 2;
     if (tiles * cs > 0x7FFFFFFF) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * cs));
