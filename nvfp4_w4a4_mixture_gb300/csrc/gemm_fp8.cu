@@ -35,12 +35,6 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N)
     return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// Two FP32 sums by one instruction: acc += v * s. (Volatile: it stays behind the wait for the load of v.)
-__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) { return static_cast<uint64_t>(hi) << 32 | lo; }
-__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t v, uint64_t s) { asm volatile("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(s)); }
-__device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
-__device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
-
 // ------------------------------------------------------------------------------------------------
 // many tokens
 // ------------------------------------------------------------------------------------------------
@@ -156,15 +150,14 @@ __global__ void __launch_bounds__(kBigThreads, 1)
             const int row = tm * kBigM + q * 32 + lane, col = tn * kBigN + grp * 128;
             const float* sa = p.a_scale + static_cast<int64_t>(min(row, p.T - 1)) * nk;
             const float* sb = p.b_scale + static_cast<int64_t>(min(col, p.N - 1) / 128) * nk;
-            uint64_t acc[64];
+            float acc[128];
 #pragma unroll
-            for (int i = 0; i < 64; ++i) acc[i] = 0;
+            for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
             // the scales come a block ahead
             float fa = __ldg(sa), fb = __ldg(sb);
             for (int kb = 0; kb < nk; ++kb, ++it) {
                 const uint32_t buf = it & 1;
-                const uint32_t f = __float_as_uint(fa * fb);
-                const uint64_t ff = pair(f, f);
+                const float f = fa * fb;
                 if (kb + 1 < nk) {
                     fa = __ldg(sa + kb + 1);
                     fb = __ldg(sb + kb + 1);
@@ -178,6 +171,8 @@ __global__ void __launch_bounds__(kBigThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(v[c & 1][i]));  // no use of them is moved before the wait
                     if (c < 7) {
                         ptx::tmem_ld16(tq + buf * kBigN + (c + 1) * 16, v[(c + 1) & 1]);
                     } else {
@@ -186,7 +181,7 @@ __global__ void __launch_bounds__(kBigThreads, 1)
                         if (lane == 0) ptx::mbar_arrive(&st.acc_empty[buf]);
                     }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) fma2(acc[c * 8 + i], pair(v[c & 1][2 * i], v[c & 1][2 * i + 1]), ff);
+                    for (int i = 0; i < 16; ++i) acc[c * 16 + i] = fmaf(__uint_as_float(v[c & 1][i]), f, acc[c * 16 + i]);
                 }
             }
             if (!ok) break;
@@ -201,12 +196,11 @@ __global__ void __launch_bounds__(kBigThreads, 1)
                 for (int i = 0; i < 8; ++i) {
                     uint4 w;
                     if constexpr (kF32) {
-                        const uint64_t u = acc[h * 16 + 2 * i], v = acc[h * 16 + 2 * i + 1];
-                        w = make_uint4(static_cast<uint32_t>(u), static_cast<uint32_t>(u >> 32), static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32));
+                        const float* a = acc + h * 32 + 4 * i;
+                        w = make_uint4(__float_as_uint(a[0]), __float_as_uint(a[1]), __float_as_uint(a[2]), __float_as_uint(a[3]));
                     } else {
-                        const uint64_t* a = acc + h * 32 + 4 * i;
-                        w = make_uint4(pack_bf16x2(lo_of(a[0]), hi_of(a[0])), pack_bf16x2(lo_of(a[1]), hi_of(a[1])),
-                                       pack_bf16x2(lo_of(a[2]), hi_of(a[2])), pack_bf16x2(lo_of(a[3]), hi_of(a[3])));
+                        const float* a = acc + h * 64 + 8 * i;
+                        w = make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]), pack_bf16x2(a[6], a[7]));
                     }
                     ptx::shared_store16(ob + lane * 128 + ((i ^ (lane & 7)) << 4), w);  // as the 128-byte swizzle has it
                 }
@@ -242,7 +236,7 @@ struct Few {
     static constexpr int kA = kFewM * 128, kStage = kA + kN * 128;
     static constexpr int kPart = kN * kFewM * 4;      // the parts of this CTA's share of the tokens
     static constexpr int kScales = 2 * kChunk * kN * 4;
-    static constexpr int kStages = kN == 64 ? 6 : 5;
+    static constexpr int kStages = kN == 64 ? 3 : kN == 32 ? 4 : 5;  // two CTAs an SM
     static constexpr uint32_t kCols = kFewBufs * kN;
 };
 template <int kStages>
@@ -397,7 +391,7 @@ __global__ void __launch_bounds__(kFewThreads)
         if (!good) fail();
     }
     __syncwarp();
-    const int share = kN / cs;  // tokens whose parts this CTA adds
+    const int share_log2 = __ffs(kN / cs) - 1, share = 1 << share_log2;  // tokens whose parts this CTA adds (cs: 1, 2, 4 or 8)
     const int row = (warp & 3) * 32 + lane, n = tn * kFewM + row;
     auto store = [&](int c, float v) {
         const int t = tt * kN + c;
@@ -411,7 +405,7 @@ __global__ void __launch_bounds__(kFewThreads)
         if (warp >= 2) {
 #pragma unroll
             for (int c = 0; c < kN; ++c) {
-                const uint32_t to = ptx::cluster_addr(part + (rank * share + c % share) * kFewM + row, c / share);
+                const uint32_t to = ptx::cluster_addr(part + ((rank << share_log2) + (c & (share - 1))) * kFewM + row, c >> share_log2);
                 ptx::cluster_store(to, acc[c]);
             }
         }
@@ -459,6 +453,14 @@ cudaError_t launch_big(const GemmFp8Args& p, int sms, cudaStream_t stream)
                       static_cast<int>(tiles));
 }
 
+// CTAs that share a tile: as many as all fit at the same time, two an SM
+int few_cluster(int64_t tiles, int nk, int sms)
+{
+    int cs = 1;
+    while (cs < 8 && tiles * cs * 2 <= sms * 2 && cs * 2 <= nk) cs *= 2;
+    return cs;
+}
+
 template <int kN, bool kF32>
 cudaError_t launch_few(const GemmFp8Args& p, int sms, cudaStream_t stream)
 {
@@ -472,8 +474,7 @@ cudaError_t launch_few(const GemmFp8Args& p, int sms, cudaStream_t stream)
     if (!maps(p, &a, &b, kN, kFewM)) return cudaErrorInvalidValue;
     const int tt = (p.T + kN - 1) / kN, tn = (p.N + kFewM - 1) / kFewM, nk = (p.K + 127) / 128;
     const int64_t tiles = static_cast<int64_t>(tt) * tn;
-    int cs = 1;
-    while (cs < 8 && tiles * cs * 2 <= sms * (kN == 64 ? 1 : 2) && cs * 2 <= nk) cs *= 2;
+    const int cs = few_cluster(tiles, nk, sms);
     if (tiles * cs > 0x7FFFFFFF) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * cs));
@@ -495,8 +496,16 @@ cudaError_t launch_few(const GemmFp8Args& p, int sms, cudaStream_t stream)
 template <bool kF32>
 cudaError_t launch(const GemmFp8Args& p, int sms, cudaStream_t stream)
 {
-    const int64_t big = static_cast<int64_t>((p.T + kBigM - 1) / kBigM) * ((p.N + kBigN - 1) / kBigN);
-    if (p.T > 64 && big >= sms / 2) return launch_big<kF32>(p, sms, stream);
+    if (p.T > 32) {
+        // A multiprocessor passes a block of K in 0.5 to 0.6 us in either kernel, whatever its tile, and joining a cluster's
+        // parts takes some 2 us: what has fewer rounds of tiles (512 x 4,096 x 2,048: 9 us with the wide tiles, 21 with 64
+        // tokens; 512 x 1,024 x 4,096: 15 and 12; 128 x 1,024 x 4,096: 19 and 8).
+        const int nk = (p.K + 127) / 128;
+        const int64_t wide = static_cast<int64_t>((p.T + kBigM - 1) / kBigM) * ((p.N + kBigN - 1) / kBigN);
+        const int64_t few = static_cast<int64_t>((p.T + 63) / 64) * ((p.N + kFewM - 1) / kFewM);
+        const int cs = few_cluster(few, nk, sms);
+        if ((wide + sms - 1) / sms * nk <= (few * cs + sms - 1) / sms * ((nk + cs - 1) / cs) + (cs > 1 ? 4 : 0)) return launch_big<kF32>(p, sms, stream);
+    }
     if (p.T <= 16) return launch_few<16, kF32>(p, sms, stream);
     if (p.T <= 32) return launch_few<32, kF32>(p, sms, stream);
     return launch_few<64, kF32>(p, sms, stream);
