@@ -303,6 +303,7 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
     // A bounded wait (a waiting warp takes no issue slots). After one that ran out there are no more: the rest runs on
     // whatever is there, to its end.
     auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (ptx::mbar_try_wait(bar, parity)) return;
         if (*reinterpret_cast<volatile int*>(abort) == 0 && !ptx::mbar_wait(bar, parity)) {
             *reinterpret_cast<volatile int*>(abort) = 1;
             record_status(p.status, kDevTimeoutAttention);
@@ -378,13 +379,20 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
         return r != 0;
     };
 
+    // This lane's addresses in a stage, in q and in the weights. A step along a row is an exclusive or: pieces are swapped
+    // within 128 bytes, and what a step adds are bits that the first piece's number does not have.
+    const uint32_t k_lane = ring_a + (kE4M3 ? piece_k8<kRB>(gw * 16 + g, t4) : piece<kRB>(gw * 16 + (lane & 15), lane >> 4));
+    const uint32_t v_lane = ring_a + kTile * kRB + (kE4M3 ? piece<kRB>(lane, gw * (kD / 64)) : piece<kRB>((lane & 7) + (lane >> 4) * 8, gw * (kD / 32) + ((lane >> 3) & 1)));
+    const uint32_t q_lane = qs_a + piece<kQB>(lane & 7, lane >> 3), p_lane = ps_a + piece<128>(lane & 7, lane >> 3);
+    const uint32_t p_mine = ps_a + piece<128>(lane & 7, 2 * gw + ((lane >> 3) & 1));
+
     float o[kMT][kNR][4], m[kNR][2], l[kNR][2];  // rows 8 nr + 2 t4, + 1; columns of v by g
     uint32_t qf[kQReg ? kNR : 1][kQReg ? kKS : 1][2];
     uint32_t stage_off = 0;
     int stage = 0;
     uint32_t phase = 0;
     bool opens = true;
-    int h = 0, row0 = 0, rows = 0, live = 0, first_row = 0, last_row = 0;
+    int h = 0, row0 = 0, rows = 0, live = 0, first_row = 0, before_window = -1;
     float factor = 0.0f;
     bool active = false;  // this group has rows
 
@@ -396,7 +404,8 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
             rows = min(kRows, cu.a.n * p.group - row0);
             live = (rows + 7) / 8;
             first_row = cu.a.len - cu.a.n + row0 / p.group;
-            last_row = cu.a.len - cu.a.n + (row0 + rows - 1) / p.group;
+            // the last token that the last row does not see (rows further down see later ones)
+            before_window = p.window > 0 ? static_cast<int>(max(static_cast<int64_t>(-1), static_cast<int64_t>(cu.a.len) - cu.a.n + (row0 + rows - 1) / p.group - p.window)) : -1;
             factor = p.scale * 1.44269504088896340736f * (kE4M3 && p.c.k_scale ? __ldg(p.c.k_scale + h) : 1.0f);
             active = rg < live;
             constexpr int kQC = kD / 8;
@@ -436,7 +445,7 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
 #pragma unroll
                     for (int ks = 0; ks < kKS; ks += 2) {
                         uint32_t b[4];
-                        ldsm4(qs_a + piece<kQB>(base_of(nr) + (lane & 7), 2 * ks + (lane >> 3)), b);
+                        ldsm4((q_lane ^ (ks * 32)) + base_of(nr) * kQB, b);
                         qf[nr][ks][0] = b[0];
                         qf[nr][ks][1] = b[1];
                         qf[nr][ks + 1][0] = b[2];
@@ -456,10 +465,9 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
         }
 
         wait(full + stage, phase);
-        const uint32_t ks_a = ring_a + stage_off, vs_a = ks_a + kTile * kRB;
+        const uint32_t k_at = k_lane + stage_off, v_at = v_lane + stage_off;
         const int pos0 = cu.a.start + cu.tile * kTile;
-        // some row does not see some token (rows further down see later ones)
-        const bool edge = pos0 + kTile - 1 > first_row || (p.window > 0 && static_cast<int64_t>(pos0) + p.window <= last_row);
+        const bool edge = pos0 + kTile - 1 > first_row || pos0 <= before_window;  // some row does not see some token
         auto sees = [&](int at, int pos) { return pos <= at && (p.window <= 0 || static_cast<int64_t>(pos) + p.window > at); };
         if (active) {
         // ---- S^T = K Q^T of this warp's 16 tokens, two chains of sums
@@ -476,15 +484,15 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
                 b[2] = qf[nr][ks + 1][0];
                 b[3] = qf[nr][ks + 1][1];
             } else {
-                ldsm4(qs_a + piece<kQB>(base_of(nr) + (lane & 7), 2 * ks + (lane >> 3)), b);
+                ldsm4((q_lane ^ (ks * 32)) + base_of(nr) * kQB, b);
             }
         };
         if constexpr (!kE4M3) {
 #pragma unroll
             for (int ks = 0; ks < kKS; ks += 2) {
                 uint32_t a[4], a2[4];
-                ldsm4(ks_a + piece<kRB>(gw * 16 + (lane & 15), 2 * ks + (lane >> 4)), a);
-                ldsm4(ks_a + piece<kRB>(gw * 16 + (lane & 15), 2 * ks + 2 + (lane >> 4)), a2);
+                ldsm4(k_at ^ (ks * 32), a);
+                ldsm4(k_at ^ (ks * 32 + 32), a2);
 #pragma unroll
                 for (int nr = 0; nr < kNR; ++nr) {
                         uint32_t b[4];
@@ -501,7 +509,7 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
                 for (int y = 0; y < 2; ++y)
                     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                                  : "=r"(w[y][0]), "=r"(w[y][1]), "=r"(w[y][2]), "=r"(w[y][3])
-                                 : "r"(ks_a + piece_k8<kRB>(gw * 16 + y * 8 + g, 4 * blk + t4))
+                                 : "r"((k_at ^ (blk * 64)) + y * 8 * kRB)
                                  : "memory");
 #pragma unroll
                 for (int x = 0; x < 4; x += 2) {
@@ -566,7 +574,7 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
 #pragma unroll
                 for (int x = 0; x < 2; ++x) l[nr][x] = l[nr][x] * alpha[nr][x] + (sc[nr][x] + sc[nr][x + 2]);
                 // rows of 64 tokens: this warp's 16 are pieces 2 warp and 2 warp + 1
-                const uint32_t at = ps_a + piece<128>(base_of(nr) + (lane & 7), 2 * gw + ((lane >> 3) & 1));
+                const uint32_t at = p_mine + base_of(nr) * 128;
                 if constexpr (kE4M3) {
                     stsm2t(at, pack_f16x2(sc[nr][0], sc[nr][1]), pack_f16x2(sc[nr][2], sc[nr][3]));
                 } else {
@@ -654,7 +662,7 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
             uint32_t b[kNR][4], bl[kE4M3 ? 1 : kNR][4];
 #pragma unroll
             for (int nr = 0; nr < kNR; ++nr) {
-                    const uint32_t at = ps_a + piece<128>(base_of(nr) + (lane & 7), 2 * kk + (lane >> 3));
+                    const uint32_t at = (p_lane ^ (kk * 32)) + base_of(nr) * 128;
                     ldsm4(at, b[nr]);
                     if constexpr (!kE4M3) ldsm4(at + kRows * kTile * 2, bl[nr]);
                 }
@@ -664,11 +672,11 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
                 if constexpr (!kE4M3) {
 #pragma unroll
                     for (int x = 0; x < 2; ++x)
-                        ldsm4t(vs_a + piece<kRB>((kk + x) * 16 + (lane & 7) + (lane >> 4) * 8, gw * (kD / 32) + 2 * mt + ((lane >> 3) & 1)), a[x]);
+                        ldsm4t((v_at ^ (mt * 32)) + (kk + x) * 16 * kRB, a[x]);
                 } else {
                     // a piece is 16 columns: the transposed load gives the bytes of two columns of two tokens
                     uint32_t w[4];
-                    ldsm4t(vs_a + piece<kRB>(kk * 16 + lane, gw * (kD / 64) + mt), w);
+                    ldsm4t((v_at ^ (mt * 16)) + kk * 16 * kRB, w);
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         e4m3x4_to_f16(__byte_perm(w[x], 0, 0x3120), a[x / 2][x % 2 * 2], a[x / 2][x % 2 * 2 + 1]);
