@@ -764,16 +764,18 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
     }
 }
 
-// ---- the join: a row's parts, in the order of the runs, by the CTA's eight warps (or, of many rows, by one)
+// ---- the join: a row's parts, in the order of the runs. Few rows: 64 columns a CTA, the parts over its eight warps, each with
+// all of its loads in flight; many rows: a warp a row.
 constexpr int kJoinWarps = 8;
 
-template <int kD, bool kE4M3, int kRG, int kNR>
-__global__ void __launch_bounds__(kJoinWarps * 32) k_attention_join(const __grid_constant__ AttentionArgs p, int row_a_warp)
+template <int kD, bool kE4M3, int kRG, int kNR, bool kFew>
+__global__ void __launch_bounds__(kJoinWarps * 32) k_attention_join(const __grid_constant__ AttentionArgs p)
 {
-    constexpr int kRows = 8 * kRG * kNR, kV = kD / 32;  // columns a lane: lane * kV ..
-    __shared__ float sm_o[kJoinWarps][kD], sm_ml[kJoinWarps][2];
+    constexpr int kRows = 8 * kRG * kNR, kCols = kFew ? 64 : kD, kV = kCols / 32;  // columns a CTA, a lane: col0 + lane * kV ..
+    constexpr int kFlight = kFew ? 20 : 8;                                        // parts whose loads are in flight
+    __shared__ float sm_o[kFew ? kJoinWarps : 1][kCols], sm_ml[kJoinWarps][2];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int row = row_a_warp ? static_cast<int>(blockIdx.x) * kJoinWarps + warp : static_cast<int>(blockIdx.x);
+    const int row = kFew ? static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x) * kJoinWarps + warp, col0 = kFew ? blockIdx.y * 64 : 0;
     // (the tables were there before the main launch began)
     const int t = row / p.n_q, head = row - t * p.n_q, s = t < p.T ? find_request(p.r.seg_offsets, p.r.S, t) : -1;
     Span a{};
@@ -796,7 +798,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attention_join(const __grid
 #pragma unroll
     for (int i = 0; i < kV; ++i) o[i] = 0.0f;
     const int per = (n + kJoinWarps - 1) / kJoinWarps;
-    const int b = row_a_warp ? 0 : min(n, warp * per), e = row_a_warp ? n : min(n, b + per);
+    const int b = kFew ? min(n, warp * per) : 0, e = kFew ? min(n, b + per) : n;
     for (int i0 = b; i0 < e; i0 += 32) {
         const int i = i0 + lane;
         float2 ml = make_float2(-INFINITY, 0.0f);
@@ -814,11 +816,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attention_join(const __grid
 #pragma unroll
         for (int x = 0; x < kV; ++x) o[x] *= keep;
         const int in = min(32, e - i0);
-        for (int x0 = 0; x0 < in; x0 += 8) {  // eight parts' loads in flight
-            float v[8][kV];
+        for (int x0 = 0; x0 < in; x0 += kFlight) {
+            float v[kFlight][kV];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                const float* from = p.part + (slot_of(i0 + x0 + x) * kRows + r) * kD + lane * kV;
+            for (int x = 0; x < kFlight; ++x) {
+                const float* from = p.part + (slot_of(i0 + x0 + x) * kRows + r) * kD + col0 + lane * kV;
 #pragma unroll
                 for (int y = 0; y < kV; ++y) v[x][y] = 0.0f;
                 if (x0 + x < in) {
@@ -831,14 +833,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attention_join(const __grid
                 }
             }
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                const float wx = __shfl_sync(0xFFFFFFFFu, w, x0 + x);
+            for (int x = 0; x < kFlight; ++x) {
+                const float wx = __shfl_sync(0xFFFFFFFFu, w, (x0 + x) & 31);  // (past the last part: times zeros)
 #pragma unroll
                 for (int y = 0; y < kV; ++y) o[y] += wx * v[x][y];
             }
         }
     }
-    if (!row_a_warp) {
+    if constexpr (kFew) {
 #pragma unroll
         for (int x = 0; x < kV; ++x) sm_o[warp][lane * kV + x] = o[x];
         if (lane == 0) {
@@ -864,10 +866,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attention_join(const __grid
     }
     float by = sum == 0.0f ? 0.0f : 1.0f / sum;
     if (kE4M3 && p.c.v_scale) by *= __ldg(p.c.v_scale + h);
-    uint16_t* const to = p.out + static_cast<int64_t>(t) * p.ld_out + head * kD + lane * kV;
+    uint16_t* const to = p.out + static_cast<int64_t>(t) * p.ld_out + head * kD + col0 + lane * kV;
 #pragma unroll
     for (int x = 0; x < kV; x += 2) *reinterpret_cast<uint32_t*>(to + x) = pack_bf16x2(o[x] * by, o[x + 1] * by);
-    if (p.lse && lane == 0) p.lse[row] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994530942f;
+    if (p.lse && lane == 0 && col0 == 0) p.lse[row] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994530942f;
 }
 
 template <int kD, bool kE4M3, int kRG, int kNR>
@@ -883,11 +885,11 @@ cudaError_t launch(const AttentionArgs& a, int sms, cudaStream_t stream)
     const int ctas = sms * S::kCtas;
     cudaError_t e = launch_pdl(k_paged_attention<kD, kE4M3, kRG, kNR>, dim3(ctas), dim3(S::kThreads), S::kSmem, stream, a);
     if (e != cudaSuccess) return e;
-    // few rows: a CTA each (a long request's many parts are added by eight warps), else a warp each
     const int64_t n = static_cast<int64_t>(a.T) * a.n_q;
-    const int row_a_warp = n > 512;
-    return launch_pdl(k_attention_join<kD, kE4M3, kRG, kNR>, dim3(static_cast<unsigned>(row_a_warp ? (n + kJoinWarps - 1) / kJoinWarps : n)),
-                      dim3(kJoinWarps * 32), 0, stream, a, row_a_warp);
+    if (n <= 512)
+        return launch_pdl(k_attention_join<kD, kE4M3, kRG, kNR, true>, dim3(static_cast<unsigned>(n), kD / 64), dim3(kJoinWarps * 32), 0, stream, a);
+    return launch_pdl(k_attention_join<kD, kE4M3, kRG, kNR, false>, dim3(static_cast<unsigned>((n + kJoinWarps - 1) / kJoinWarps)), dim3(kJoinWarps * 32),
+                      0, stream, a);
 }
 
 template <int kD, bool kE4M3>
