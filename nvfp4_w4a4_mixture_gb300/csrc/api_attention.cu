@@ -212,6 +212,7 @@ moe_status_t moe_paged_attention(const moe_kv_cache_t* C, const moe_requests_t* 
     a.T = T;
     a.n_q = A->n_q;
     a.group = A->n_q / C->n_kv;
+    a.group_mul = (65536u + a.group - 1) / a.group;
     a.max_new = A->max_new;
     a.window = A->window;
     a.scale = A->scale;

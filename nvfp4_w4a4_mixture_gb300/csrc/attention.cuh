@@ -83,6 +83,7 @@ struct AttentionArgs {
     KvCache c;
     Requests r;
     int T, n_q, group, max_new, window;
+    unsigned group_mul;  // ceil(2^16 / group): (row * group_mul) >> 16 is row / group for row * 63 < 2^16
     float scale;
     const uint16_t* q;
     int64_t ld_q;

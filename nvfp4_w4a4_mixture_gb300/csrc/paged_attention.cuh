@@ -67,6 +67,9 @@ struct Cut {
     __device__ int run(int64_t u) const { return static_cast<int>(u < r * (q + 1) ? quotient(u, q + 1) : r + quotient(u - r * (q + 1), q)); }
 };
 
+// The token of a row of a key head's queries (less than 1,088 of them): row / group, by a multiplication.
+__device__ __forceinline__ int token_of(const AttentionArgs& p, int row) { return static_cast<int>(static_cast<unsigned>(row) * p.group_mul >> 16); }
+
 struct Span {
     int beg, n, len, start, tiles, segs;  // rows; tokens; first token seen; units along the tokens; (head, row block) pairs
     __device__ int64_t cost() const { return static_cast<int64_t>(tiles + (tiles ? kExtra : 0)) * segs; }
@@ -318,11 +321,12 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
         const uint32_t v_even = (kTile + lw * kLoad) * kRB + piece<kRB>(g, t4), v_odd = v_even ^ 64;
         const int mask = (1 << p.c.page_log2) - 1;
         int page = 0, pos = 0;  // of the token lane % kLoad
-        bool in = false;
+        bool in = false, first = true;
         int64_t head_off = 0;
         auto fetch = [&]() {
             pos = cu.a.start + cu.tile * kTile + lw * kLoad + lane % kLoad;
-            head_off = (cu.seg % p.c.n_kv) * p.c.ld_head;
+            if (first || cu.tile == 0) head_off = (cu.seg % p.c.n_kv) * p.c.ld_head;
+            first = false;
             in = pos < cu.a.len && pos >= 0;
             if (in) page = __ldg(p.r.pages + cu.s * p.r.ld_pages + (pos >> p.c.page_log2));
         };
@@ -403,15 +407,15 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
             row0 = cu.seg / p.c.n_kv * kRows;
             rows = min(kRows, cu.a.n * p.group - row0);
             live = (rows + 7) / 8;
-            first_row = cu.a.len - cu.a.n + row0 / p.group;
+            first_row = cu.a.len - cu.a.n + token_of(p, row0);
             // the last token that the last row does not see (rows further down see later ones)
-            before_window = p.window > 0 ? static_cast<int>(max(static_cast<int64_t>(-1), static_cast<int64_t>(cu.a.len) - cu.a.n + (row0 + rows - 1) / p.group - p.window)) : -1;
+            before_window = p.window > 0 ? static_cast<int>(max(static_cast<int64_t>(-1), static_cast<int64_t>(cu.a.len) - cu.a.n + token_of(p, row0 + rows - 1) - p.window)) : -1;
             factor = p.scale * 1.44269504088896340736f * (kE4M3 && p.c.k_scale ? __ldg(p.c.k_scale + h) : 1.0f);
             active = rg < live;
             constexpr int kQC = kD / 8;
 #pragma unroll 4
             for (int i = gt; i < 8 * kNR * kQC; i += kGroup) {
-                const int r = base_of(i / kQC / 8) + i / kQC % 8, c = i % kQC, at = (row0 + r) / p.group;
+                const int r = base_of(i / kQC / 8) + i / kQC % 8, c = i % kQC, at = token_of(p, row0 + r);
                 uint4 v = make_uint4(0, 0, 0, 0);
                 if (r < rows) v = __ldg(reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(cu.a.beg + at) * p.ld_q + (h * p.group + (row0 + r) - at * p.group) * kD + c * 8));
                 if (c == 0) row_pos[r] = cu.a.len - cu.a.n + at;
@@ -727,7 +731,7 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
                     const float sum = (w.x + w.y) + (w.z + w.w);
                     if (r >= rows) continue;
                     if (whole) {
-                        const int at = (row0 + r) / p.group, head = h * p.group + (row0 + r) - at * p.group;
+                        const int at = token_of(p, row0 + r), head = h * p.group + (row0 + r) - at * p.group;
                         const int64_t t = cu.a.beg + at;
                         float by = sum == 0.0f ? 0.0f : 1.0f / sum;
                         if (kE4M3 && p.c.v_scale) by *= __ldg(p.c.v_scale + h);
