@@ -435,7 +435,8 @@ moe_status_t moe_cache_append(const moe_kv_cache_t* C, const moe_requests_t* R, 
  *   last token or outside a row's window takes no part, whatever its bits.
  *   q, out: bf16 [T][n_q][D], ld_*: elements between two tokens, every row on 16 bytes; out may be q (the same
  *   address and row stride), no other overlap. lse: nullable, FP32 [T][n_q]. n_q a multiple of n_kv, n_q / n_kv <= 64.
- *   max_new in [1, 16]: the most rows of a request; a request of more is skipped and reported. window: 0 for none.
+ *   max_new in [1, 16]: the most rows of a request; a request of more, or of more than 2^31 - 65 tokens, is skipped and
+ *   reported. window: 0 for none.
  *   The cache's length is split over the multiprocessors, the parts joined in a second launch in a fixed order.
  *   ws: >= moe_attention_workspace_bytes(S, n_q, n_kv, D, max_new). T = 0 returns MOE_OK after the shape check.
  * ------------------------------------------------------------------------------------------- */

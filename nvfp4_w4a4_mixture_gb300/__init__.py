@@ -241,7 +241,7 @@ def _adapter_workspace():
     """The workspace of moe_adapter_add, moe_cache_append and moe_gemm_fp8 where the caller gives none: its header is all that
     they use, so it is never replaced by a larger one, which would lose its report and leave captured calls with memory
     that was given back."""
-    dev = torch.cuda.current_device()
+    dev = torch._C._cuda_getDevice()
     w = _adapter_ws.get(dev)
     if w is None:
         w = Workspace(4096)
@@ -732,18 +732,24 @@ def _cache_append(q, k, v, k_cache, v_cache, seg_offsets, kv_len, pages, inv_fre
                                   q_ld, k_ptr, k_ld, v_ptr, v_ld, T, o_ptr, o_ld, ws.address, ws.nbytes, _stream())
 
 
-_attention_ws = {}
+_attention_ws, _attention_bytes = {}, {}
 
 
 def _attention_workspace(S, n_q, n_kv, D, max_new):
     """moe_paged_attention's workspace where the caller gives none: one for each stream, since calls on two streams run
     at the same time. A capture's belongs to its graph (the memory is the graph's, its report is lost)."""
-    if not isinstance(max_new, int) or not 0 <= max_new <= _INT_MAX:
-        raise ValueError("max_new is an int of 32 bits")
-    nbytes = _lib.moe_attention_workspace_bytes(S, n_q, n_kv, D, max_new)
-    if torch.cuda.is_current_stream_capturing():
+    dev = torch._C._cuda_getDevice()
+    shape = S, n_q, n_kv, D, max_new, dev
+    nbytes = _attention_bytes.get(shape)
+    if nbytes is None:
+        if not isinstance(max_new, int) or not 0 <= max_new <= _INT_MAX:
+            raise ValueError("max_new is an int of 32 bits")
+        if len(_attention_bytes) > 4096:  # (batches of changing size: a number each)
+            _attention_bytes.clear()
+        nbytes = _attention_bytes[shape] = _lib.moe_attention_workspace_bytes(*shape[:5])
+    if torch._C._cuda_isCurrentStreamCapturing():
         return Workspace(nbytes)
-    key = torch.cuda.current_device(), _stream()
+    key = dev, _stream()
     w = _attention_ws.get(key)
     if w is None or w.nbytes < nbytes:
         old, w = w, Workspace(nbytes)

@@ -1,4 +1,5 @@
 // api_attention.cu -- the C ABI of the attention half of a block (include/moe_nvfp4.h): checks on the host, then the launch.
+#include <algorithm>
 #include <cmath>
 
 #include "api.cuh"
@@ -193,6 +194,7 @@ moe_status_t moe_paged_attention(const moe_kv_cache_t* C, const moe_requests_t* 
     if (T == 0) return MOE_OK;  // an empty batch: nothing is read or written, the pointers may be NULL
     MOE_TRY(check_cache_memory(C));
     MOE_TRY(check_requests(R, C->page_size, T, &a.r));
+    a.r.max_len = std::min<int64_t>(a.r.max_len, 0x7FFFFFFF - 64);  // a unit's positions fit 32 bits
     if (static_cast<int64_t>(T) * A->n_q > 0x7FFFFF00) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "T=%d rows of n_q=%d heads: 2^31 or more", T, A->n_q);
     if (!q || !out) return fail(MOE_ERR_INVALID_ARG, "NULL tensor pointer");
     const int64_t w = static_cast<int64_t>(A->n_q) * C->D;

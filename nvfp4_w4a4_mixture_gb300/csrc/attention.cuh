@@ -96,15 +96,15 @@ struct AttentionArgs {
     int* status;
 };
 namespace attention {
-// the rows of a unit in eights: what max_new tokens of a key head's queries need, at most eight
+// The rows of a unit in eights: what max_new tokens of a key head's queries need, at most eight.
 inline int row_eights(int group, int max_new)
 {
     const int rows = group * max_new;
     return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : rows <= 32 ? 4 : 8;
 }
 
-// most CTAs of the main launch: each has two places for partial sums
-inline int ctas_most(int sms) { return sms * 4; }
+// The most CTAs of the main launch; each has two places for partial sums.
+inline int ctas_most(int sms) { return sms * 3; }
 }  // namespace attention
 size_t attention_workspace_bytes(int S, int n_q, int n_kv, int D, int max_new, int sms);
 cudaError_t launch_paged_attention(AttentionArgs a, void* ws, int sms, cudaStream_t stream);
@@ -123,5 +123,10 @@ struct GemmFp8Args {
     int* status;
 };
 cudaError_t launch_gemm_fp8(const GemmFp8Args& a, int sms, cudaStream_t stream);
+
+// ---- api.cu
+// The map of an output of rows ld elements apart that is stored in boxes (128-byte swizzle).
+CUresult encode_tmap_2d_out(CUtensorMap* map, void* base, bool f32, uint64_t inner, uint64_t outer, uint64_t ld, uint32_t box_inner,
+                            uint32_t box_outer);
 
 }  // namespace moe

@@ -169,9 +169,6 @@ CUresult encode_tmap_2d_bf16(CUtensorMap* map, const void* base, uint64_t inner,
                              uint32_t box_outer);
 CUresult encode_tmap_bf16(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
                           const uint32_t* box, int swizzle_bytes);
-// rows ld elements apart, to be stored in boxes (128-byte swizzle)
-CUresult encode_tmap_2d_out(CUtensorMap* map, void* base, bool f32, uint64_t inner, uint64_t outer, uint64_t ld, uint32_t box_inner,
-                            uint32_t box_outer);
 CUresult encode_tmap_3d_u8(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t box0,
                            uint32_t box1);
 

@@ -1,7 +1,8 @@
 // quantize_fp8.cu -- FP8 encoding of rows with a scale for each 128 elements: s = max |x| / 448, code = E4M3(x / s).
-// A block is in the registers of 16 lanes (16 bytes of bf16 each); its maximum comes by shuffles. Bounded by memory and,
-// with the eight quotients a lane, by instruction issue:
-// x is read once, codes and scales are written once.
+// A block is in the registers of 16 lanes (16 bytes of bf16 each); its maximum comes by shuffles. x is read once, codes
+// and scales are written once; with eight quotients a lane it is bound by instruction issue before memory.
+// Measured: 16,384 x 2,064 26.4 us, 3.9 TB/s; with a division for every quotient 29, with CTAs that stay and the next blocks'
+// loads in flight 34 to 46 (fewer warps); 4 x 2,048 1.7 us.
 #include "attention.cuh"
 
 namespace moe {

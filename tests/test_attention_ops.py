@@ -311,6 +311,46 @@ def test_attention_of_one_buffer_of_keys_and_values(m):
     assert torch.equal(ref, m.moe_paged_attention(q, both[:, 0], both[:, 1], *b.tables(), max_new=2))
 
 
+def test_attention_at_the_last_positions(m):
+    # the longest request, its table's rows one and the same page; a window keeps the work small
+    D, page, W, n = 64, 65536, 100, 3
+    g = gen(30)
+    k, v = (torch.randn(1, page, 1, D, generator=g, device="cuda").to(BF) for _ in range(2))
+    q = torch.randn(n, 2, D, generator=g, device="cuda").to(BF)
+    pages = torch.zeros(1, 32768, dtype=torch.int32, device="cuda")
+    last = 2 ** 31 - 65
+    out = m.moe_paged_attention(q, k, v, ints([0, n]), ints([last]), pages, max_new=n, window=W)
+    m.moe_read_device_status()
+    for i in range(n):
+        p = torch.arange(last - n + i - W + 1, last - n + i + 1, device="cuda") % page
+        z = torch.einsum("hd,td->ht", q[i].double(), k[0, p, 0].double()) * D ** -0.5
+        ref = torch.softmax(z, 1) @ v[0, p, 0].double()
+        assert bool(((out[i].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -14 * 4).all())
+    with pytest.raises(m.MoeError):
+        m.moe_paged_attention(q, k, v, ints([0, n]), ints([last + 1]), pages, max_new=n, window=W)
+        m.moe_read_device_status()
+
+
+@pytest.mark.parametrize("dtype", [BF, E4M3])
+def test_offsets_past_32_bits(m, dtype):
+    # pages 2^28 elements apart in one buffer: the last begins behind 2^32 elements
+    D, page, n_pages = 64, 16, 18
+    buf = torch.zeros(n_pages << 28, dtype=torch.uint8 if dtype is E4M3 else torch.int16, device="cuda").view(dtype)
+    shape, strides = (n_pages, page, 1, D), (1 << 28, D, D, 1)
+    b = Batch(31, [2, 1], [40, 33], 1, D, page, dtype)
+    b.k_cache, b.v_cache = torch.as_strided(buf, shape, strides), torch.as_strided(buf, shape, strides, 1 << 20)
+    b.table = [[17, 3, 16, 0], [5, 17 - 2, 14, 0]]
+    b.pages = ints(b.table)
+    b.fill()
+    q, k, v = (b.normal(3, h, D).to(BF) for h in (4, 1, 1))
+    m.moe_cache_append(None, k, v, b.k_cache, b.v_cache, *b.tables(), k_scale=b.k_scale, v_scale=b.v_scale)
+    for s, rows in ((0, slice(0, 2)), (1, slice(2, 3))):
+        places = range(b.lens[s] - b.new[s], b.lens[s])
+        want = v[rows] if dtype is BF else (v[rows].float() / b.v_scale[:, None]).clamp(-448, 448).to(E4M3)
+        assert torch.equal(b.got(b.v_cache, s, places).float(), want.float())
+    check_attention(m, b, 4, q=q)
+
+
 def test_attention_repeats_itself_and_in_a_graph(m):
     b = Batch(19, [1, 2, 1], [5000, 333, 64], 2, 128, 16).fill()
     q = b.normal(4, 8, 128).to(BF)
