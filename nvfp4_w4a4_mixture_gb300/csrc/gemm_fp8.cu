@@ -9,11 +9,11 @@
 //                    weight once without padding; a cluster of CTAs shares a tile's blocks along K and adds the parts
 //                    through distributed shared memory, in the order of their ranks.
 // TMA fills the ragged ends of K, T and N with zeros.
-// Measured: 16,384 x 4,096 x 2,048 104 us, 2.6 PFLOP/s (70 % of twice the rate of bf16 matrix products); bound by the sums
-// in registers: a block of a 128 x 256 tile is 128 scaled sums a thread, 930 cycles with the loads from tensor memory where
-// its MMAs take 512. Without the sums the same loads and MMAs took 93 us, with a quarter of the MMAs 114 of then 123. Two
-// values an instruction (fma.rn.f32x2) were slower than one (123 us against 105), as was a third of the threads' registers
-// moved to the summing warps for two loads of 32 columns in flight (127). 4 x 5,120 x 2,048 5.1 us (its weights in 1.6).
+// Measured: 16,384 x 4,096 x 2,048 104 us, 2.6 PFLOP/s (70 % of twice the rate of bf16 matrix products). Without the sums
+// in registers it took 95 us, with the loads from tensor memory alone 93: the rest is the MMAs (512 cycles a block at their
+// nominal rate, some 850 here) and the sums' turn between them. Two values an instruction (fma.rn.f32x2: 123 us) and
+// registers moved to the summing warps for two loads of 32 columns in flight (107) were slower. 4 x 5,120 x 2,048 5.1 us
+// (its weights in 1.6).
 #include "attention.cuh"
 #include "ptx_cluster.cuh"
 
