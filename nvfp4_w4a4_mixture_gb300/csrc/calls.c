@@ -238,6 +238,7 @@ static PyObject* select_experts(PyObject* self, PyObject* const* a, Py_ssize_t n
     if (lt < 0 || lt > 1 || !whole(a[0], 2, rows, &l)) return leave();
     d.E = (int)rows[1];
     d.k = as_int(a[1]);
+    if (PyErr_Occurred()) return leave(); /* before any Python code runs, which may clear it */
     out[0] = rows[0];
     out[1] = d.k;
     if (d.k < 1 || dtype_of(a[9]) != 2 || !whole(a[9], 2, out, &ids) || dtype_of(a[10]) != 1 || !whole(a[10], 2, out, &w)) return leave();
