@@ -255,7 +255,8 @@ def _adapter_workspace():
 def moe_set_wait_test_hook(ws, wait_limit_us, ready_extra):
     """Test hook: the expert GEMMs' wait for a token block's intermediate gives up after
     wait_limit_us (0: default) and needs ready_extra more completions (0: none); with more than none,
-    moe_adapter_add's wait for A x (long requests) runs out too. (0, 0) restores."""
+    moe_adapter_add's wait for A x (long requests) and the first waits of moe_gemm_fp8 and moe_paged_attention run out
+    too. (0, 0) restores."""
     _check(lib().moe_set_wait_test_hook(ws.ptr, int(wait_limit_us), int(ready_extra), _stream()))
 
 
@@ -263,7 +264,10 @@ def moe_read_device_status(ws=None):
     """Raises what the calls on the workspace have reported since the last reading (None: the default workspaces)."""
     if ws is None:
         dev = torch.cuda.current_device()
-        for w in [_adapter_ws.get(dev)] + [w for key, w in _attention_ws.items() if key[0] == dev]:
+        of_streams = [w for key, w in _attention_ws.items() if key[0] == dev]
+        if len(of_streams) > 1:  # their calls, too, have to be over
+            torch.cuda.synchronize()
+        for w in [_adapter_ws.get(dev)] + of_streams:
             if w is not None:
                 _check(lib().moe_read_device_status(w.ptr, _stream()))
         ws = _ws(4096)
@@ -774,7 +778,10 @@ def moe_paged_attention(q, k_cache, v_cache, seg_offsets, kv_len, pages, max_new
     status = -1
     if q.is_cuda:
         if ws is None:
-            ws = _attention_workspace(kv_len.shape[0], q.shape[1], k_cache.shape[2], k_cache.shape[3], max_new)
+            try:
+                ws = _attention_workspace(kv_len.shape[0], q.shape[1], k_cache.shape[2], k_cache.shape[3], max_new)
+            except IndexError:
+                raise ValueError("q must have shape [T, n_q, D], k_cache [n_pages, page_size, n_kv, D] and kv_len [S]") from None
         if _calls is not None:
             status = _calls.paged_attention(q, k_cache, v_cache, k_scale, v_scale, seg_offsets, kv_len, pages, max_new, scale, window, out,
                                             lse, ws.address, ws.nbytes, _stream())

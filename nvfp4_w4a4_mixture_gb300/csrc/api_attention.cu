@@ -224,6 +224,7 @@ moe_status_t moe_paged_attention(const moe_kv_cache_t* C, const moe_requests_t* 
     a.ld_out = ld_out;
     a.lse = lse;
     a.status = &static_cast<WsHeader*>(ws)->status;
+    a.hooks = static_cast<const WsHeader*>(ws);
     MOE_CUDA(launch_paged_attention(a, ws, sms, static_cast<cudaStream_t>(stream)), "attention launch");
     return MOE_OK;
 }
@@ -275,6 +276,7 @@ moe_status_t moe_gemm_fp8(const uint8_t* a, const float* a_scale, const uint8_t*
     g.out_f32 = es == 4;
     g.ld_out = T > 1 ? ld_out : N;
     g.status = &static_cast<WsHeader*>(ws)->status;
+    g.hooks = static_cast<const WsHeader*>(ws);
     MOE_CUDA(launch_gemm_fp8(g, device_sm_count(), static_cast<cudaStream_t>(stream)), "FP8 GEMM launch");
     return MOE_OK;
 }

@@ -94,6 +94,7 @@ struct AttentionArgs {
     float* part;      // partial sums (workspace)
     float* part_ml;   // their maxima and weights (workspace)
     int* status;
+    const WsHeader* hooks;  // the workspace header whose test_* fields the first wait reads
 };
 namespace attention {
 // The rows of a unit in eights: what max_new tokens of a key head's queries need, at most eight.
@@ -121,6 +122,7 @@ struct GemmFp8Args {
     bool out_f32;
     int64_t ld_out;
     int* status;
+    const WsHeader* hooks;  // the workspace header whose test_* fields the first wait reads
 };
 cudaError_t launch_gemm_fp8(const GemmFp8Args& a, int sms, cudaStream_t stream);
 
