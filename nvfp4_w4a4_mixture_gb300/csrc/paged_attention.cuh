@@ -2,25 +2,28 @@
 //   out = sum_t softmax_t(scale q . k_t) v_t over the tokens that a row sees, in one pass over keys and values
 // with the running maximum m and sum l of the softmax: o <- o 2^(m - m') + 2^(s - m') v.
 //
-// Work: a unit is 64 cached tokens of one key head against up to kRows rows (new tokens x query heads of that key
-// head). The units of all requests, in order, are cut into equal runs, one a CTA, so ragged lengths balance by
-// themselves. A (request, head) whose units lie in one run is finished there; of the others every run leaves o, m and l
-// in the workspace, and a second launch adds them in the order of the runs.
+// Work: a unit is 64 cached tokens (128 where they have 128 bytes or less) of one key head against up to kRows rows (new
+// tokens x query heads of that key head). The units of all requests, in order, are cut into equal runs, one a CTA, so
+// ragged lengths balance by themselves. A (request, head) whose units lie in one run is finished there; of the others
+// every run leaves o, m and l in the workspace, and a second launch adds them in the order of the runs.
 // A CTA streams K and V through a ring in shared memory: two warps load (cp.async of 16 bytes a lane, addresses from
 // the page table, which is read a unit ahead; a token behind the end is filled with zeros). The rows' eights are dealt to
-// one to four groups of four warps. Of a unit each warp of a group takes 16 tokens of K Q^T, the four exchange maxima and
-// weights through shared memory, and each takes a quarter of the columns of V^T P^T, so the accumulators need no join.
+// one to four groups of four warps. Of a unit each warp of a group takes a quarter of the tokens for K Q^T, the four exchange
+// maxima and weights through shared memory, and each takes a quarter of the columns of V^T P^T, so the accumulators need no
+// join.
 // mma.sync with the tokens (and V's columns) on its M side: rows are padded to eight, not sixteen. The products are 4
 // flops a byte and row, for 8 rows 32 flops a byte: memory bounds them long before the tensor cores do.
 // bf16 cache: the weights are two bf16 values (16 bits; one would add an error of the size of the output's own rounding);
 // E4M3 cache: codes become FP16 (exact), the weights are FP16, and q is scaled to FP16's range by a power of two a row
 // (exact where q is not 2^-30 of the row's largest).
-// Measured: 64 requests of ragged lengths to 8,192, 32 heads on 8 of 128: 164 to 168 us, 6.3 TB/s (94 % of what a copy
-// reaches); one request over 300,001 tokens in 8 bits, 16 heads on 2 of 256: 59 us, 5.2 TB/s, 10 us of it the two launches,
-// the first loads and the join; 200 verify windows of one to three tokens, 14 heads on 2 of 64, window 1,024: 39 us, bound
+// Measured: 64 requests of ragged lengths to 8,192, 32 heads on 8 of 128: 168 us, 6.2 TB/s (93 % of what a copy
+// reaches); one request over 300,001 tokens in 8 bits, 16 heads on 2 of 256: 60 us, 5.1 TB/s, 10 us of it the two launches,
+// the first loads and the join; 200 verify windows of one to three tokens, 14 heads on 2 of 64, window 1,024: 38 us, bound
 // by instruction issue (two thirds of the rows are padding); 4 tokens over 4,100, 16 heads on 2 of 256: 13 us, one unit's
 // chain and the join's.
 #pragma once
+#include <climits>
+
 #include "attention.cuh"
 #include "ptx_cluster.cuh"
 
@@ -28,14 +31,19 @@ namespace moe {
 
 namespace attention {
 
-constexpr int kTile = 64;                       // tokens of a unit
-constexpr int kWarps = 4, kGroup = 32 * kWarps;  // a group of warps that computes, 16 tokens of a unit each
-// Warps that load, and a warp's tokens of a unit. (Four took issue slots: 200 windows of 1,024 61 us against 54.)
-constexpr int kLoaders = 2, kLoad = kTile / kLoaders;
+constexpr int kWarps = 4, kGroup = 32 * kWarps;  // a group of warps that computes
+// Warps that load. (Four took issue slots: 200 windows of 1,024 61 us against 54.)
+constexpr int kLoaders = 2;
 constexpr int kMinUnits = 1;  // a run costs at least so many units
 // What the begin and the end of a (request, head) cost, in units: queries, sums, output. (0, 1, 2, 4 of them: 200 windows of
 // 1,024 49.7, 42.8, 42.6, 43.6 us, 200 requests to 500 with heads of 128 40.8, 34.8, 34.3, 34.8.)
 constexpr int kExtra = 2;
+
+// Tokens of a unit: 16 a warp, or of short rows 32, for what a unit costs besides its products is then for twice as many.
+// (64 and 128 of them, 200 requests, 14 heads on 2 of 64: windows of 1,024 39.8 and 37.7 us, three new tokens over to 4,096
+// 68.9 and 60.2, one over to 2,000 in 8 bits 23.1 and 21.0; against it, one over to 1,024 19.8 and 20.4.)
+template <int kD, bool kE4M3>
+constexpr int tile_of() { return kD * (kE4M3 ? 1 : 2) <= 128 ? 128 : 64; }
 
 // kRG: groups, kNR: a group's rows in eights
 template <int kD, bool kE4M3, int kRG, int kNR>
@@ -43,15 +51,18 @@ struct Shape {
     static constexpr int kThreads = kRG * kGroup + kLoaders * 32;
     static constexpr int kRows = 8 * kRG * kNR;
     static constexpr int kRowBytes = kD * (kE4M3 ? 1 : 2);       // of a cached token's head
+    static constexpr int kTile = tile_of<kD, kE4M3>();
     static constexpr int kStage = 2 * kTile * kRowBytes;         // K, V
     static constexpr int kQ = kRows * kD * 2;
     static constexpr int kP = kRows * kTile * 2 * (kE4M3 ? 1 : 2);
     static constexpr int kFixed = kQ + kP + kRows * (2 * kWarps * 4 + 8) + 512;
-    // as many CTAs an SM as hold three stages each, and as the registers of so many rows allow: one to three
+    // As many CTAs an SM as hold three stages each, and as the registers of so many rows allow: one to three. Two of two
+    // stages are better than one, too (100 requests of 4 new tokens over to 2,000, 32 heads on 4 of 128: 67 us against 77),
+    // but of heads of 256, whose sums two CTAs' registers do not hold (60 such requests, 16 heads on 2, 8 bits: 39.5, 35.2).
     static constexpr int kByRegs = kRG == 4 ? 1 : kRG >= 2 ? 2 : 3;
     // (a multiprocessor's 228 KB less 1 KB a CTA, and 10 KB in which the join's CTAs can wait)
     static constexpr int most(int ctas) { return (218 / ctas - 1) * 1024; }
-    static constexpr int by_smem(int ctas) { return ctas == 1 || (most(ctas) - kFixed) / kStage >= 3 ? ctas : by_smem(ctas - 1); }
+    static constexpr int by_smem(int ctas) { return ctas == 1 || (most(ctas) - kFixed) / kStage >= (ctas == 2 && kD <= 128 ? 2 : 3) ? ctas : by_smem(ctas - 1); }
     static constexpr int kCtas = by_smem(kByRegs);
     static constexpr int kFit = (most(kCtas) - kFixed) / kStage;
     static constexpr int kStages = kFit > 6 ? 6 : kFit;
@@ -84,7 +95,7 @@ struct Span {
     __device__ int64_t cost() const { return static_cast<int64_t>(tiles + (tiles ? kExtra : 0)) * segs; }
 };
 
-template <int kRows>
+template <int kRows, int kTile>
 __device__ __forceinline__ Span span_of(const AttentionArgs& p, int s, bool& bad)
 {
     const Request r = load_request(p.r, s, p.T, p.max_new, bad);
@@ -100,7 +111,7 @@ __device__ __forceinline__ Span span_of(const AttentionArgs& p, int s, bool& bad
 }
 
 // A place in the order of units.
-template <int kRows>
+template <int kRows, int kTile>
 struct Cursor {
     Span a;
     int s, seg, tile;
@@ -112,7 +123,7 @@ struct Cursor {
         if (++seg < a.segs) return;
         seg = 0;
         bool bad;
-        do a = span_of<kRows>(p, ++s, bad);
+        do a = span_of<kRows, kTile>(p, ++s, bad);
         while (a.segs == 0);
     }
 };
@@ -204,7 +215,9 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
 {
     using S = Shape<kD, kE4M3, kRG, kNR>;
     constexpr int kThreads = S::kThreads, kCompute = kRG * kGroup;
-    constexpr int kRows = S::kRows, kRB = S::kRowBytes, kChunks = kRB / 16, kStages = S::kStages;
+    constexpr int kRows = S::kRows, kTile = S::kTile, kRB = S::kRowBytes, kChunks = kRB / 16, kStages = S::kStages;
+    constexpr int kMQ = kTile / 64, kLoad = kTile / kLoaders;  // a warp's tokens in Q K^T in sixteens, in loading
+    constexpr int kPB = kTile * 2;          // bytes of a row of weights
     constexpr int kQB = kD * 2;             // bytes of a row of q
     constexpr int kMT = kD / 64;            // 16-column tiles of a warp's quarter of the columns
     constexpr int kKS = kD / 16;            // steps of Q K^T
@@ -212,13 +225,13 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* const ring = smem;
     uint8_t* const qs = smem + kStages * S::kStage;
-    uint8_t* const ps = qs + S::kQ;         // weights: [kRows][64] 16-bit, bf16: the high parts, then the low ones
+    uint8_t* const ps = qs + S::kQ;         // weights: [kRows][kTile] 16-bit, bf16: the high parts, then the low ones
     float* const wmax = reinterpret_cast<float*>(ps + S::kP);  // [kRows][kWarps]
     float* const wsum = wmax + kRows * kWarps;                 // [kRows][kWarps]
     float* const qscale = wsum + kRows * kWarps;               // [kRows] (E4M3) what the row of q was divided by
     int* const row_pos = reinterpret_cast<int*>(qscale + kRows);  // [kRows] the row's position
     int64_t* const found = reinterpret_cast<int64_t*>(row_pos + kRows);  // a sum a warp, then what the search found
-    Cursor<kRows>* const start = reinterpret_cast<Cursor<kRows>*>(found + 20);
+    Cursor<kRows, kTile>* const start = reinterpret_cast<Cursor<kRows, kTile>*>(found + 20);
     uint64_t* const full = reinterpret_cast<uint64_t*>(found + 30);  // [kStages]
     uint64_t* const empty = full + kStages;                            // [kStages]
     uint64_t* const never = empty + kStages;
@@ -245,7 +258,7 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
     int64_t mine = 0;
     for (int s = sb; s < se; ++s) {
         bool bad;
-        mine += span_of<kRows>(p, s, bad).cost();
+        mine += span_of<kRows, kTile>(p, s, bad).cost();
         if (bad && blockIdx.x == 0) record_status(p.status, kDevBadRequest);
     }
     int64_t incl = mine;
@@ -273,7 +286,7 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
         for (int s = sb; s < se; ++s) {
             bool bad;
             p.prefix[s] = u;
-            u += span_of<kRows>(p, s, bad).cost();
+            u += span_of<kRows, kTile>(p, s, bad).cost();
         }
         if (tid == 0) {
             p.prefix[p.r.S] = total;
@@ -288,10 +301,10 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
     for (int e = 0; e < 2; ++e) {
         if (border[e] < before || border[e] >= before + mine) continue;
         int64_t u = border[e] - before;
-        Cursor<kRows> c;
+        Cursor<kRows, kTile> c;
         for (c.s = sb;; ++c.s) {
             bool bad;
-            c.a = span_of<kRows>(p, c.s, bad);
+            c.a = span_of<kRows, kTile>(p, c.s, bad);
             if (u < c.a.cost()) break;
             u -= c.a.cost();
         }
@@ -301,17 +314,17 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
         start[e] = c;
     }
     __syncthreads();
-    Cursor<kRows> cu = start[0];
+    Cursor<kRows, kTile> cu = start[0];
     // the units between the borders
     int count;
     {
         const bool to_end = border[1] == total;
-        const Cursor<kRows> end = start[1];
+        const Cursor<kRows, kTile> end = start[1];
         const int last_s = to_end ? p.r.S : end.s;
         int64_t n = -(static_cast<int64_t>(cu.seg) * cu.a.tiles + cu.tile) + (to_end ? 0 : static_cast<int64_t>(end.seg) * end.a.tiles + end.tile);
         for (int s = cu.s; s < last_s; ++s) {
             bool bad;
-            const Span a = s == cu.s ? cu.a : span_of<kRows>(p, s, bad);
+            const Span a = s == cu.s ? cu.a : span_of<kRows, kTile>(p, s, bad);
             n += static_cast<int64_t>(a.tiles) * a.segs;
         }
         count = static_cast<int>(n);
@@ -333,25 +346,32 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
         const uint32_t k_even = lw * kLoad * kRB + (kE4M3 ? piece_k8<kRB>(g, t4) : piece<kRB>(g, t4)), k_odd = k_even ^ 64;
         const uint32_t v_even = (kTile + lw * kLoad) * kRB + piece<kRB>(g, t4), v_odd = v_even ^ 64;
         const int mask = (1 << p.c.page_log2) - 1;
-        int page = 0, pos = 0;  // of the token lane % kLoad
-        bool in = false, first = true;
+        int page[kLoad / 32];  // of the tokens lane, lane + 32
+        unsigned pos = 0;      // the first one's position
+        bool first = true;
         int64_t head_off = 0;
         auto fetch = [&]() {
-            pos = cu.a.start + cu.tile * kTile + lw * kLoad + lane % kLoad;
+            const int pos0 = cu.a.start + cu.tile * kTile, left = cu.a.len - pos0;  // (the unit's end may pass 2^31)
+            pos = static_cast<unsigned>(pos0) + lw * kLoad + lane;
             if (first || cu.tile == 0) head_off = (cu.seg % p.c.n_kv) * p.c.ld_head;
             first = false;
-            in = pos < cu.a.len && pos >= 0;
-            if (in) page = __ldg(p.r.pages + cu.s * p.r.ld_pages + (pos >> p.c.page_log2));
+#pragma unroll
+            for (int x = 0; x < kLoad / 32; ++x)  // INT_MIN: no token
+                page[x] = lw * kLoad + lane + x * 32 < left ? __ldg(p.r.pages + cu.s * p.r.ld_pages + ((pos + x * 32) >> p.c.page_log2)) : INT_MIN;
         };
         fetch();
         int s = 0;
         uint32_t ph = 1;
         for (int j = 0; j < count; ++j) {
-            if (in && static_cast<unsigned>(page) >= static_cast<unsigned>(p.c.n_pages)) {
-                in = false;
-                record_status(p.status, kDevBadPage);
+            int64_t mine[kLoad / 32];
+#pragma unroll
+            for (int x = 0; x < kLoad / 32; ++x) {
+                mine[x] = -1;
+                if (static_cast<unsigned>(page[x]) < static_cast<unsigned>(p.c.n_pages))
+                    mine[x] = (page[x] * p.c.ld_page + static_cast<int>((pos + x * 32) & mask) * p.c.ld_slot + head_off) * (kE4M3 ? 1 : 2);
+                else if (page[x] != INT_MIN)
+                    record_status(p.status, kDevBadPage);
             }
-            const int64_t mine = in ? (page * p.c.ld_page + (pos & mask) * p.c.ld_slot + head_off) * (kE4M3 ? 1 : 2) : -1;
             if (j + 1 < count) {
                 cu.next(p);
                 fetch();
@@ -360,7 +380,7 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
             uint8_t* const to = ring + s * S::kStage;
 #pragma unroll
             for (int b = 0; b < kLoad / 8; ++b) {
-                const int64_t off = __shfl_sync(0xFFFFFFFFu, mine, b * 8 + g);
+                const int64_t off = __shfl_sync(0xFFFFFFFFu, mine[b / 4], b % 4 * 8 + g);
                 const bool there = off >= 0;
                 const char* const k = static_cast<const char*>(p.c.k) + (there ? off + t4 * 16 : 0);
                 const char* const v = k + v_from_k;
@@ -405,8 +425,8 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
     // within 128 bytes, and what a step adds are bits that the first piece's number does not have.
     const uint32_t k_lane = ring_a + (kE4M3 ? piece_k8<kRB>(gw * 16 + g, t4) : piece<kRB>(gw * 16 + (lane & 15), lane >> 4));
     const uint32_t v_lane = ring_a + kTile * kRB + (kE4M3 ? piece<kRB>(lane, gw * (kD / 64)) : piece<kRB>((lane & 7) + (lane >> 4) * 8, gw * (kD / 32) + ((lane >> 3) & 1)));
-    const uint32_t q_lane = qs_a + piece<kQB>(lane & 7, lane >> 3), p_lane = ps_a + piece<128>(lane & 7, lane >> 3);
-    const uint32_t p_mine = ps_a + piece<128>(lane & 7, 2 * gw + ((lane >> 3) & 1));
+    const uint32_t q_lane = qs_a + piece<kQB>(lane & 7, lane >> 3), p_lane = ps_a + piece<kPB>(lane & 7, lane >> 3);
+    const uint32_t p_mine = ps_a + piece<kPB>(lane & 7, 2 * gw + ((lane >> 3) & 1));
 
     float o[kMT][kNR][4], m[kNR][2], l[kNR][2];  // rows 8 nr + 2 t4, + 1; columns of v by g
     uint32_t qf[kQReg ? kNR : 1][kQReg ? kKS : 1][2];
@@ -489,81 +509,101 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
         wait(full + stage, phase);
         const uint32_t k_at = k_lane + stage_off, v_at = v_lane + stage_off;
         const int pos0 = cu.a.start + cu.tile * kTile;
-        const bool edge = pos0 + kTile - 1 > first_row || pos0 <= before_window;  // some row does not see some token
-        auto sees = [&](int at, int pos) { return pos <= at && (p.window <= 0 || static_cast<int64_t>(pos) + p.window > at); };
+        const bool edge = pos0 > first_row - (kTile - 1) || pos0 <= before_window;  // some row does not see some token
+        // whether the row at a position sees the unit's token x
+        auto sees = [&](int at, int x) { return x <= at - pos0 && (p.window <= 0 || static_cast<int64_t>(x) + p.window > at - pos0); };
         if (active) {
-        // ---- S^T = K Q^T of this warp's 16 tokens, two chains of sums
-        float sc[kNR][4], sc2[kNR][4];
+            // ---- S^T = K Q^T of this warp's tokens (16 from 16 gw on, and 64 further), each in two chains of sums
+            float sc[kNR][kMQ][4], sc2[kNR][kMQ][4];
 #pragma unroll
-        for (int nr = 0; nr < kNR; ++nr)
+            for (int nr = 0; nr < kNR; ++nr)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) sc[nr][x] = sc2[nr][x] = 0.0f;
-        // q's fragments of steps ks and ks + 1
-        auto q_frag = [&](int nr, int ks, uint32_t (&b)[4]) {
-            if constexpr (kQReg) {
-                b[0] = qf[nr][ks][0];
-                b[1] = qf[nr][ks][1];
-                b[2] = qf[nr][ks + 1][0];
-                b[3] = qf[nr][ks + 1][1];
-            } else {
-                ldsm4((q_lane ^ (ks * 32)) + base_of(nr) * kQB, b);
-            }
-        };
-        if constexpr (!kE4M3) {
+                for (int y = 0; y < kMQ; ++y)
 #pragma unroll
-            for (int ks = 0; ks < kKS; ks += 2) {
-                uint32_t a[4], a2[4];
-                ldsm4(k_at ^ (ks * 32), a);
-                ldsm4(k_at ^ (ks * 32 + 32), a2);
+                    for (int x = 0; x < 4; ++x) sc[nr][y][x] = sc2[nr][y][x] = 0.0f;
+            // q's fragments of steps ks and ks + 1
+            auto q_frag = [&](int nr, int ks, uint32_t (&b)[4]) {
+                if constexpr (kQReg) {
+                    b[0] = qf[nr][ks][0];
+                    b[1] = qf[nr][ks][1];
+                    b[2] = qf[nr][ks + 1][0];
+                    b[3] = qf[nr][ks + 1][1];
+                } else {
+                    ldsm4((q_lane ^ (ks * 32)) + base_of(nr) * kQB, b);
+                }
+            };
+            if constexpr (!kE4M3) {
 #pragma unroll
-                for (int nr = 0; nr < kNR; ++nr) {
-                        uint32_t b[4];
-                        q_frag(nr, ks, b);
-                        mma<false>(sc[nr], a[0], a[1], a[2], a[3], b[0], b[1]);
-                        mma<false>(sc2[nr], a2[0], a2[1], a2[2], a2[3], b[2], b[3]);
+                for (int ks = 0; ks < kKS; ks += 2) {
+                    uint32_t a[kMQ][4], a2[kMQ][4];
+#pragma unroll
+                    for (int y = 0; y < kMQ; ++y) {
+                        ldsm4((k_at ^ (ks * 32)) + y * 64 * kRB, a[y]);
+                        ldsm4((k_at ^ (ks * 32 + 32)) + y * 64 * kRB, a2[y]);
                     }
-            }
-        } else {
-#pragma unroll
-            for (int blk = 0; blk < kD / 64; ++blk) {
-                uint32_t w[2][4];
-#pragma unroll
-                for (int y = 0; y < 2; ++y)
-                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(w[y][0]), "=r"(w[y][1]), "=r"(w[y][2]), "=r"(w[y][3])
-                                 : "r"((k_at ^ (blk * 64)) + y * 8 * kRB)
-                                 : "memory");
-#pragma unroll
-                for (int x = 0; x < 4; x += 2) {
-                    uint32_t a[2][4];
-#pragma unroll
-                    for (int z = 0; z < 2; ++z)
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) e4m3x4_to_f16(w[y][x + z], a[z][y], a[z][2 + y]);
 #pragma unroll
                     for (int nr = 0; nr < kNR; ++nr) {
-                            uint32_t b[4];
-                            q_frag(nr, 4 * blk + x, b);
-                            mma<true>(sc[nr], a[0][0], a[0][1], a[0][2], a[0][3], b[0], b[1]);
-                            mma<true>(sc2[nr], a[1][0], a[1][1], a[1][2], a[1][3], b[2], b[3]);
-                        }
-                }
-            }
-        }
-
-        // ---- scores in powers of two, masks, maxima
+                        uint32_t b[4];
+                        q_frag(nr, ks, b);
 #pragma unroll
-        for (int nr = 0; nr < kNR; ++nr) {
+                        for (int y = 0; y < kMQ; ++y) {
+                            mma<false>(sc[nr][y], a[y][0], a[y][1], a[y][2], a[y][3], b[0], b[1]);
+                            mma<false>(sc2[nr][y], a2[y][0], a2[y][1], a2[y][2], a2[y][3], b[2], b[3]);
+                        }
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int blk = 0; blk < kD / 64; ++blk)
+#pragma unroll
+                    for (int y = 0; y < kMQ; ++y) {
+                        uint32_t w[2][4];
+#pragma unroll
+                        for (int z = 0; z < 2; ++z)
+                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(w[z][0]), "=r"(w[z][1]), "=r"(w[z][2]), "=r"(w[z][3])
+                                         : "r"((k_at ^ (blk * 64)) + (y * 64 + z * 8) * kRB)
+                                         : "memory");
+#pragma unroll
+                        for (int x = 0; x < 4; x += 2) {
+                            uint32_t a[2][4];
+#pragma unroll
+                            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                                for (int z = 0; z < 2; ++z) e4m3x4_to_f16(w[z][x + u], a[u][z], a[u][2 + z]);
+#pragma unroll
+                            for (int nr = 0; nr < kNR; ++nr) {
+                                uint32_t b[4];
+                                q_frag(nr, 4 * blk + x, b);
+                                mma<true>(sc[nr][y], a[0][0], a[0][1], a[0][2], a[0][3], b[0], b[1]);
+                                mma<true>(sc2[nr][y], a[1][0], a[1][1], a[1][2], a[1][3], b[2], b[3]);
+                            }
+                        }
+                    }
+            }
+
+            // ---- scores in powers of two, masks, maxima
+#pragma unroll
+            for (int nr = 0; nr < kNR; ++nr) {
                 const float2 by = kE4M3 ? *reinterpret_cast<const float2*>(qscale + base_of(nr) + 2 * t4) : make_float2(1.0f, 1.0f);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) sc[nr][x] = (sc[nr][x] + sc2[nr][x]) * (kE4M3 ? factor * (x & 1 ? by.y : by.x) : factor);
+                for (int y = 0; y < kMQ; ++y)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) sc[nr][y][x] = (sc[nr][y][x] + sc2[nr][y][x]) * (kE4M3 ? factor * (x & 1 ? by.y : by.x) : factor);
                 if (edge) {
                     const int2 at = *reinterpret_cast<const int2*>(row_pos + base_of(nr) + 2 * t4);
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        if (!sees(x & 1 ? at.y : at.x, pos0 + gw * 16 + g + x / 2 * 8)) sc[nr][x] = -INFINITY;
+                    for (int y = 0; y < kMQ; ++y)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            if (!sees(x & 1 ? at.y : at.x, y * 64 + gw * 16 + g + x / 2 * 8)) sc[nr][y][x] = -INFINITY;
                 }
-                float u = fmaxf(sc[nr][0], sc[nr][2]), v = fmaxf(sc[nr][1], sc[nr][3]);
+                float u = fmaxf(sc[nr][0][0], sc[nr][0][2]), v = fmaxf(sc[nr][0][1], sc[nr][0][3]);
+#pragma unroll
+                for (int y = 1; y < kMQ; ++y) {
+                    u = fmaxf(u, fmaxf(sc[nr][y][0], sc[nr][y][2]));
+                    v = fmaxf(v, fmaxf(sc[nr][y][1], sc[nr][y][3]));
+                }
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) {
                     u = fmaxf(u, __shfl_xor_sync(0xFFFFFFFFu, u, x));
@@ -574,13 +614,13 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
                     wmax[(base_of(nr) + 2 * t4 + 1) * kWarps + gw] = v;
                 }
             }
-        sync();  // the maxima are there, and every warp is done with the weights of the unit before
+            sync();  // the maxima are there, and every warp is done with the weights of the unit before
 
-        // ---- weights
-        bool moved = false;
-        float alpha[kNR][2];
+            // ---- weights
+            bool moved = false;
+            float alpha[kNR][2];
 #pragma unroll
-        for (int nr = 0; nr < kNR; ++nr) {
+            for (int nr = 0; nr < kNR; ++nr) {
                 float by[2];
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
@@ -590,36 +630,38 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
                     by[x] = to == -INFINITY ? 0.0f : to;  // a row that has seen nothing yet
                     alpha[nr][x] = exp2_fast(m[nr][x] - by[x]);
                     m[nr][x] = to;
+                    l[nr][x] *= alpha[nr][x];
                 }
 #pragma unroll
-                for (int x = 0; x < 4; ++x) sc[nr][x] = exp2_fast(sc[nr][x] - by[x & 1]);
+                for (int y = 0; y < kMQ; ++y) {
 #pragma unroll
-                for (int x = 0; x < 2; ++x) l[nr][x] = l[nr][x] * alpha[nr][x] + (sc[nr][x] + sc[nr][x + 2]);
-                // rows of 64 tokens: this warp's 16 are pieces 2 warp and 2 warp + 1
-                const uint32_t at = p_mine + base_of(nr) * 128;
-                if constexpr (kE4M3) {
-                    stsm2t(at, pack_f16x2(sc[nr][0], sc[nr][1]), pack_f16x2(sc[nr][2], sc[nr][3]));
-                } else {
-                    uint32_t high[2], low[2];
+                    for (int x = 0; x < 4; ++x) sc[nr][y][x] = exp2_fast(sc[nr][y][x] - by[x & 1]);
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        high[x] = pack_bf16x2(sc[nr][2 * x], sc[nr][2 * x + 1]);
-                        low[x] = pack_bf16x2(sc[nr][2 * x] - __uint_as_float(high[x] << 16), sc[nr][2 * x + 1] - __uint_as_float(high[x] & 0xFFFF0000u));
+                    for (int x = 0; x < 2; ++x) l[nr][x] += sc[nr][y][x] + sc[nr][y][x + 2];
+                    // rows of kTile tokens: these 16 are two pieces
+                    const uint32_t at = (p_mine ^ (y * 128)) + base_of(nr) * kPB;
+                    if constexpr (kE4M3) {
+                        stsm2t(at, pack_f16x2(sc[nr][y][0], sc[nr][y][1]), pack_f16x2(sc[nr][y][2], sc[nr][y][3]));
+                    } else {
+                        uint32_t high[2], low[2];
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            high[x] = pack_bf16x2(sc[nr][y][2 * x], sc[nr][y][2 * x + 1]);
+                            low[x] = pack_bf16x2(sc[nr][y][2 * x] - __uint_as_float(high[x] << 16), sc[nr][y][2 * x + 1] - __uint_as_float(high[x] & 0xFFFF0000u));
+                        }
+                        stsm2t(at, high[0], high[1]);
+                        stsm2t(at + kRows * kPB, low[0], low[1]);
                     }
-                    stsm2t(at, high[0], high[1]);
-                    stsm2t(at + kRows * kTile * 2, low[0], low[1]);
                 }
             }
-        if (__any_sync(0xFFFFFFFFu, moved)) {
+            if (__any_sync(0xFFFFFFFFu, moved)) {
 #pragma unroll
-            for (int nr = 0; nr < kNR; ++nr) {
+                for (int nr = 0; nr < kNR; ++nr)
 #pragma unroll
                     for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
                         for (int x = 0; x < 4; ++x) o[mt][nr][x] *= alpha[nr][x & 1];
-                }
-        }
-
+            }
         }
 
         // an accumulator's column of v: x / 2 is the lower or upper eight of a tile (E4M3: the even or odd columns)
@@ -638,17 +680,16 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
             if (any_of(odd)) {  // (the weights are there)
 #pragma unroll 1
                 for (int tok = 0; tok < (active ? kTile : 0); ++tok) {
-                    const int pos = pos0 + tok;
 #pragma unroll
                     for (int nr = 0; nr < kNR; ++nr)
 #pragma unroll
                         for (int y = 0; y < 2; ++y) {
                             const int r = base_of(nr) + 2 * t4 + y;
-                            if (!sees(row_pos[r], pos)) continue;
-                            const uint8_t* pp = ps + piece<128>(r, tok / 8) + tok % 8 * 2;
+                            if (!sees(row_pos[r], tok)) continue;
+                            const uint8_t* pp = ps + piece<kPB>(r, tok / 8) + tok % 8 * 2;
                             float wt;
                             if constexpr (kE4M3) wt = f16_to_f32(*reinterpret_cast<const uint16_t*>(pp));
-                            else wt = bf16_to_f32(*reinterpret_cast<const uint16_t*>(pp)) + bf16_to_f32(*reinterpret_cast<const uint16_t*>(pp + kRows * kTile * 2));
+                            else wt = bf16_to_f32(*reinterpret_cast<const uint16_t*>(pp)) + bf16_to_f32(*reinterpret_cast<const uint16_t*>(pp + kRows * kPB));
 #pragma unroll
                             for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
@@ -678,42 +719,39 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
         }
 
         if (active) {
-        // ---- O^T += V^T P^T, this warp's quarter of the columns, 32 tokens at a time
+            // ---- O^T += V^T P^T, this warp's quarter of the columns, 32 tokens at a time
 #pragma unroll 1
-        for (int kk = 0; kk < kTile / 16; kk += 2) {
-            uint32_t b[kNR][4], bl[kE4M3 ? 1 : kNR][4];
-#pragma unroll
-            for (int nr = 0; nr < kNR; ++nr) {
-                    const uint32_t at = (p_lane ^ (kk * 32)) + base_of(nr) * 128;
-                    ldsm4(at, b[nr]);
-                    if constexpr (!kE4M3) ldsm4(at + kRows * kTile * 2, bl[nr]);
-                }
-#pragma unroll
-            for (int mt = 0; mt < kMT; ++mt) {
-                uint32_t a[2][4];  // of both steps
-                if constexpr (!kE4M3) {
-#pragma unroll
-                    for (int x = 0; x < 2; ++x)
-                        ldsm4t((v_at ^ (mt * 32)) + (kk + x) * 16 * kRB, a[x]);
-                } else {
-                    // a piece is 16 columns: the transposed load gives the bytes of two columns of two tokens
-                    uint32_t w[4];
-                    ldsm4t((v_at ^ (mt * 16)) + kk * 16 * kRB, w);
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        e4m3x4_to_f16(__byte_perm(w[x], 0, 0x3120), a[x / 2][x % 2 * 2], a[x / 2][x % 2 * 2 + 1]);
-                    }
-                }
+            for (int kk = 0; kk < kTile / 16; kk += 2) {
+                uint32_t b[kNR][4], bl[kE4M3 ? 1 : kNR][4];
 #pragma unroll
                 for (int nr = 0; nr < kNR; ++nr) {
+                    const uint32_t at = (p_lane ^ (kk * 32)) + base_of(nr) * kPB;
+                    ldsm4(at, b[nr]);
+                    if constexpr (!kE4M3) ldsm4(at + kRows * kPB, bl[nr]);
+                }
+#pragma unroll
+                for (int mt = 0; mt < kMT; ++mt) {
+                    uint32_t a[2][4];  // of both steps
+                    if constexpr (!kE4M3) {
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) ldsm4t((v_at ^ (mt * 32)) + (kk + x) * 16 * kRB, a[x]);
+                    } else {
+                        // a piece is 16 columns: the transposed load gives the bytes of two columns of two tokens
+                        uint32_t w[4];
+                        ldsm4t((v_at ^ (mt * 16)) + kk * 16 * kRB, w);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            e4m3x4_to_f16(__byte_perm(w[x], 0, 0x3120), a[x / 2][x % 2 * 2], a[x / 2][x % 2 * 2 + 1]);
+                    }
+#pragma unroll
+                    for (int nr = 0; nr < kNR; ++nr)
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
                             mma<kE4M3>(o[mt][nr], a[x][0], a[x][1], a[x][2], a[x][3], b[nr][2 * x], b[nr][2 * x + 1]);
                             if constexpr (!kE4M3) mma<false>(o[mt][nr], a[x][0], a[x][1], a[x][2], a[x][3], bl[nr][2 * x], bl[nr][2 * x + 1]);
                         }
-                    }
+                }
             }
-        }
         }
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(empty + stage);
@@ -793,7 +831,7 @@ constexpr int kJoinWarps = 8;
 template <int kD, bool kE4M3, int kRG, int kNR, bool kFew>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_attention_join(const __grid_constant__ AttentionArgs p)
 {
-    constexpr int kRows = 8 * kRG * kNR, kCols = kFew ? 64 : kD, kV = kCols / 32;  // columns a CTA, a lane: col0 + lane * kV ..
+    constexpr int kRows = 8 * kRG * kNR, kTile = tile_of<kD, kE4M3>(), kCols = kFew ? 64 : kD, kV = kCols / 32;  // columns a CTA, a lane: col0 + lane * kV ..
     constexpr int kFlight = kFew ? 20 : 8;                                        // parts whose loads are in flight
     __shared__ float sm_o[kFew ? kJoinWarps : 1][kCols], sm_ml[kJoinWarps][2];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -802,7 +840,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attention_join(const __grid
     const int t = row / p.n_q, head = row - t * p.n_q, s = t < p.T ? find_request(p.r.seg_offsets, p.r.S, t) : -1;
     Span a{};
     bool bad = true;
-    if (s >= 0 && s < p.r.S) a = span_of<kRows>(p, s, bad);
+    if (s >= 0 && s < p.r.S) a = span_of<kRows, kTile>(p, s, bad);
     const bool mine = a.segs != 0 && t < a.beg + a.n;
     const int h = head / p.group, in_seg = (t - a.beg) * p.group + head % p.group, r = in_seg % kRows;
     const int seg = in_seg / kRows * p.c.n_kv + h;
