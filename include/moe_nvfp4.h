@@ -376,8 +376,9 @@ moe_status_t moe_adapter_add(const moe_adapters_t* A, const uint16_t* x, int64_t
  *   seg_offsets[0] = 0, non-decreasing, seg_offsets[S] <= T: rows behind the last request are left as they were.
  *   A row at a negative position (kv_len < n, for example an idle slot of a batch with kv_len 0) has no place in the
  *   cache. What breaks these rules (offsets out of order or past T, kv_len < 0 or past max_pages * page_size) is
- *   skipped, its rows left as they were; moe_read_device_status reports it as MOE_ERR_INVALID_ARG. A page outside
- *   [0, n_pages) is reported likewise; nothing is written there, and its tokens read as zeros.
+ *   skipped, its rows left as they were (of offsets out of order other requests' rows may be left, too);
+ *   moe_read_device_status reports it as MOE_ERR_INVALID_ARG. A page outside [0, n_pages) is reported likewise; nothing
+ *   is written there, and its tokens read as zeros.
  *   All of it is read on the device: a captured call follows what the tables hold when it is replayed.
  * ------------------------------------------------------------------------------------------- */
 typedef struct {

@@ -43,7 +43,8 @@ __device__ __forceinline__ Request load_request(const Requests& r, int s, int T,
     return Request{beg, bad ? 0 : end - beg, len};
 }
 
-// The last request whose rows begin at or before row t (-1: none). Warp-wide; lanes look at 32 offsets at a time.
+// The last request whose rows begin at or before row t (-1: none), where the offsets are in order; else some request, whose
+// rows may begin behind t. Warp-wide; lanes look at 32 offsets at a time.
 __device__ __forceinline__ int find_request(const int32_t* off, int S, int t)
 {
     const int lane = threadIdx.x & 31;

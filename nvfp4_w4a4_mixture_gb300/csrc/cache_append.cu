@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_cache_append(const __grid_const
     bool bad;
     const Request r = load_request(p.r, s, p.T, p.T, bad);
     const int pos = r.len - r.n + static_cast<int>(t - r.beg);
-    if (r.n == 0 || t >= r.beg + r.n || pos < 0) return;
+    if (r.n == 0 || t < r.beg || t >= r.beg + r.n || pos < 0) return;
     const int page = __ldg(p.r.pages + s * p.r.ld_pages + (pos >> p.c.page_log2));
 #pragma unroll
     for (int i = 0; i < kD / 64; ++i)

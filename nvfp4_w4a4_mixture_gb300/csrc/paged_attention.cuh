@@ -841,7 +841,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attention_join(const __grid
     Span a{};
     bool bad = true;
     if (s >= 0 && s < p.r.S) a = span_of<kRows, kTile>(p, s, bad);
-    const bool mine = a.segs != 0 && t < a.beg + a.n;
+    const bool mine = a.segs != 0 && t >= a.beg && t < a.beg + a.n;
     const int h = head / p.group, in_seg = (t - a.beg) * p.group + head % p.group, r = in_seg % kRows;
     const int seg = in_seg / kRows * p.c.n_kv + h;
     ptx::griddep_wait();

@@ -424,6 +424,32 @@ def test_attention_broken_tables_are_reported(m):
     m.moe_read_device_status(ws)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_offsets_out_of_order_take_no_row_behind_their_begin(m, D):
+    """Offsets in which a search for row 4's request ends at one that begins behind it."""
+    b = Batch(57, [5, 1, 1, 0, 1], [300, 290, 280, 16, 270], 1, D, 16).fill()
+    wrong = ints([0, 5, 6, 7, 1, 2])
+    q = b.normal(8, 4, D).to(BF)
+    good = m.moe_paged_attention(q, b.k_cache, b.v_cache, *b.tables(), max_new=5)
+    ws = m.Workspace(m.moe_attention_workspace_bytes(5, 4, 1, D, 5))
+    out = m.moe_paged_attention(q, b.k_cache, b.v_cache, wrong, b.kv_len, b.pages, max_new=5, out=torch.full_like(q, 7.0), ws=ws)
+    with pytest.raises(m.MoeError):
+        m.moe_read_device_status(ws)
+    seven = torch.full_like(q[0], 7.0)
+    for t in (0, 2, 3, 4, 5, 6):  # (row 1 is two requests')
+        assert torch.equal(out[t], good[t]) or torch.equal(out[t], seven), t
+    assert torch.equal(out[7], seven)
+
+    k, v = (b.normal(8, 1, D).to(BF) for _ in range(2))
+    before = [[b.got(c, s, range(b.lens[s] - n)) for c in (b.k_cache, b.v_cache)] for s, n in enumerate(b.new)]
+    m.moe_cache_append(None, k, v, b.k_cache, b.v_cache, wrong, b.kv_len, b.pages, ws=ws)
+    with pytest.raises(m.MoeError):
+        m.moe_read_device_status(ws)
+    for s, n in enumerate(b.new):  # what lies before a request's new tokens stays
+        for c, was in zip((b.k_cache, b.v_cache), before[s]):
+            assert torch.equal(b.got(c, s, range(b.lens[s] - n)), was), s
+
+
 # ------------------------------------------------------------------------------------------------
 # append
 # ------------------------------------------------------------------------------------------------
