@@ -260,7 +260,7 @@ moe_status_t moe_gemm_fp8(const uint8_t* a, const float* a_scale, const uint8_t*
         return fail(MOE_ERR_MISALIGNED, "a and b must be 16-byte, their scales 4-byte aligned");
     const int64_t kb = (K + 127) / 128, nb = (N + 127) / 128, w = static_cast<int64_t>(N) * es;
     if (rows_overlap_bytes(out, ld_out * es, w, T, a, static_cast<int64_t>(T) * K) || rows_overlap_bytes(out, ld_out * es, w, T, b, static_cast<int64_t>(N) * K) ||
-        rows_overlap_bytes(out, ld_out * es, w, T, a_scale, 4 * T * kb) || rows_overlap_bytes(out, ld_out * es, w, T, b_scale, 4 * nb * kb))
+        rows_overlap_bytes(out, ld_out * es, w, T, a_scale, 4LL * T * kb) || rows_overlap_bytes(out, ld_out * es, w, T, b_scale, 4 * nb * kb))
         return fail(MOE_ERR_INVALID_ARG, "out overlaps an input");
     MOE_TRY(check_ws(ws, ws_bytes, sizeof(WsHeader)));
     MOE_TRY(check_device());

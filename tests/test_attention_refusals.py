@@ -140,6 +140,14 @@ def gemm(m, a=MB, sa=2 * MB, b=10 * MB, sb=3 * MB, T=4, N=512, K=2048, out=4 * M
     return m.lib().moe_gemm_fp8(p(a), p(sa), p(b), p(sb), T, N, K, p(out), dt, ld, p(ws), nbytes, None)
 
 
+def test_overlap_of_more_than_two_gigabytes_of_scales(m):
+    """600,000,000 rows: an output over the last of their scales."""
+    T, G = 600_000_000, 1 << 40
+    kw = dict(T=T, K=16, N=8, ld=8, a=G, b=2 * G, sb=3 * G, sa=4 * G)
+    assert gemm(m, out=4 * G + 4 * T - 16, ws=None, **kw) == INVALID and b"overlaps" in m.lib().moe_last_error_detail()
+    assert gemm(m, out=4 * G + 4 * T, ws=None, **kw) == INVALID and b"overlaps" not in m.lib().moe_last_error_detail()
+
+
 def test_fp8_refusals(m):
     for K in (0, 8, 24, -16, 65552):
         assert quant(m, K=K) == SHAPE and gemm(m, K=K) == SHAPE
