@@ -2,6 +2,7 @@
 // attention over that cache, FP8 encoding and products (not part of the C ABI).
 #pragma once
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstdint>
 
 #include "kernels.cuh"
@@ -126,6 +127,17 @@ struct GemmFp8Args {
     const WsHeader* hooks;  // the workspace header whose test_* fields the first wait reads
 };
 cudaError_t launch_gemm_fp8(const GemmFp8Args& a, int sms, cudaStream_t stream);
+
+// Dynamic shared memory beyond 48 KB for a kernel, asked for once on each device. done: a bit for each.
+inline cudaError_t allow_smem(std::atomic<uint64_t>& done, const void* kernel, size_t bytes)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && done.load(std::memory_order_relaxed) >> dev & 1)) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e == cudaSuccess && dev < 64) done.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+    return e;
+}
 
 // ---- api.cu
 // The map of an output of rows ld elements apart that is stored in boxes (128-byte swizzle).

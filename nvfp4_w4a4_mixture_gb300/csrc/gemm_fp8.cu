@@ -445,16 +445,13 @@ bool maps(const GemmFp8Args& p, CUtensorMap* a, CUtensorMap* b, uint32_t rows_a,
 template <bool kF32>
 cudaError_t launch_big(const GemmFp8Args& p, int sms, cudaStream_t stream)
 {
-    static bool set = false;
-    if (!set) {
-        cudaError_t e = cudaFuncSetAttribute(k_gemm_fp8<kF32>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kBigSmem));
-        if (e != cudaSuccess) return e;
-        set = true;
-    }
+    static std::atomic<uint64_t> smem_set{0};
+    cudaError_t e = allow_smem(smem_set, reinterpret_cast<const void*>(k_gemm_fp8<kF32>), kBigSmem);
+    if (e != cudaSuccess) return e;
     CUtensorMap a, b, out;
     if (!maps(p, &a, &b, kBigM, kBigN) || encode_tmap_2d_out(&out, p.out, kF32, p.N, p.T, p.ld_out, kF32 ? 32 : 64, 32) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
-    const int tn = (p.N + kBigN - 1) / kBigN, tm = (p.T + kBigM - 1) / kBigM;
+    const int tn = (p.N + kBigN - 1) / kBigN, tm = (p.T - 1) / kBigM + 1;
     const int64_t tiles = static_cast<int64_t>(tn) * tm;
     if (tiles > 0x7FFFFFFF - 65536) return cudaErrorInvalidValue;
     return launch_pdl(k_gemm_fp8<kF32>, dim3(tiles < sms ? static_cast<int>(tiles) : sms), dim3(kBigThreads), kBigSmem, stream, a, b, out, p, tn,
@@ -472,15 +469,12 @@ int few_cluster(int64_t tiles, int nk, int sms)
 template <int kN, bool kF32>
 cudaError_t launch_few(const GemmFp8Args& p, int sms, cudaStream_t stream)
 {
-    static bool set = false;
-    if (!set) {
-        cudaError_t e = cudaFuncSetAttribute(k_gemm_fp8_few<kN, kF32>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(few_smem<kN>()));
-        if (e != cudaSuccess) return e;
-        set = true;
-    }
+    static std::atomic<uint64_t> smem_set{0};
+    cudaError_t e = allow_smem(smem_set, reinterpret_cast<const void*>(k_gemm_fp8_few<kN, kF32>), few_smem<kN>());
+    if (e != cudaSuccess) return e;
     CUtensorMap a, b;
     if (!maps(p, &a, &b, kN, kFewM)) return cudaErrorInvalidValue;
-    const int tt = (p.T + kN - 1) / kN, tn = (p.N + kFewM - 1) / kFewM, nk = (p.K + 127) / 128;
+    const int tt = (p.T - 1) / kN + 1, tn = (p.N + kFewM - 1) / kFewM, nk = (p.K + 127) / 128;
     const int64_t tiles = static_cast<int64_t>(tt) * tn;
     const int cs = few_cluster(tiles, nk, sms);
     if (tiles * cs > 0x7FFFFFFF) return cudaErrorInvalidValue;
@@ -509,8 +503,8 @@ cudaError_t launch(const GemmFp8Args& p, int sms, cudaStream_t stream)
         // parts takes some 2 us: what has fewer rounds of tiles (512 x 4,096 x 2,048: 9 us with the wide tiles, 21 with 64
         // tokens; 512 x 1,024 x 4,096: 15 and 12; 128 x 1,024 x 4,096: 19 and 8).
         const int nk = (p.K + 127) / 128;
-        const int64_t wide = static_cast<int64_t>((p.T + kBigM - 1) / kBigM) * ((p.N + kBigN - 1) / kBigN);
-        const int64_t few = static_cast<int64_t>((p.T + 63) / 64) * ((p.N + kFewM - 1) / kFewM);
+        const int64_t wide = static_cast<int64_t>((p.T - 1) / kBigM + 1) * ((p.N + kBigN - 1) / kBigN);
+        const int64_t few = static_cast<int64_t>((p.T - 1) / 64 + 1) * ((p.N + kFewM - 1) / kFewM);
         const int cs = few_cluster(few, nk, sms);
         if ((wide + sms - 1) / sms * nk <= (few * cs + sms - 1) / sms * ((nk + cs - 1) / cs) + (cs > 1 ? 4 : 0)) return launch_big<kF32>(p, sms, stream);
     }

@@ -936,14 +936,11 @@ template <int kD, bool kE4M3, int kRG, int kNR>
 cudaError_t launch(const AttentionArgs& a, int sms, cudaStream_t stream)
 {
     using S = Shape<kD, kE4M3, kRG, kNR>;
-    static bool set = false;
-    if (!set) {
-        cudaError_t e = cudaFuncSetAttribute(k_paged_attention<kD, kE4M3, kRG, kNR>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-        if (e != cudaSuccess) return e;
-        set = true;
-    }
+    static std::atomic<uint64_t> smem_set{0};
+    cudaError_t e = allow_smem(smem_set, reinterpret_cast<const void*>(k_paged_attention<kD, kE4M3, kRG, kNR>), S::kSmem);
+    if (e != cudaSuccess) return e;
     const int ctas = sms * S::kCtas;
-    cudaError_t e = launch_pdl(k_paged_attention<kD, kE4M3, kRG, kNR>, dim3(ctas), dim3(S::kThreads), S::kSmem, stream, a);
+    e = launch_pdl(k_paged_attention<kD, kE4M3, kRG, kNR>, dim3(ctas), dim3(S::kThreads), S::kSmem, stream, a);
     if (e != cudaSuccess) return e;
     const int64_t n = static_cast<int64_t>(a.T) * a.n_q;
     if (n <= 512)
