@@ -18,7 +18,7 @@
 // (exact where q is not 2^-30 of the row's largest).
 // Measured: 64 requests of ragged lengths to 8,192, 32 heads on 8 of 128: 168 us, 6.2 TB/s (93 % of what a copy
 // reaches); one request over 300,001 tokens in 8 bits, 16 heads on 2 of 256: 60 us, 5.1 TB/s, 10 us of it the two launches,
-// the first loads and the join; 200 verify windows of one to three tokens, 14 heads on 2 of 64, window 1,024: 38 us, bound
+// the first loads and the join; 200 verify windows of one to three tokens, 14 heads on 2 of 64, window 1,024: 36 us, bound
 // by instruction issue (two thirds of the rows are padding); 4 tokens over 4,100, 16 heads on 2 of 256: 13 us, one unit's
 // chain and the join's.
 #pragma once
@@ -34,7 +34,10 @@ namespace attention {
 constexpr int kWarps = 4, kGroup = 32 * kWarps;  // a group of warps that computes
 // Warps that load. (Four took issue slots: 200 windows of 1,024 61 us against 54.)
 constexpr int kLoaders = 2;
-constexpr int kMinUnits = 1;  // a run costs at least so many units
+// A unit costs so much besides the groups that have rows in it. (2, 4, 5, 7 and 100, where the rows hardly count: 200
+// windows of 1,024 35.9, 35.7, 36.0, 36.8, 38.1 us, 200 requests of one to three tokens over to 4,096 58.1, 55.4, 56.3, 56.2,
+// 61.1.)
+constexpr int kUnit = 4;
 // What the begin and the end of a (request, head) cost, in units: queries, sums, output. (0, 1, 2, 4 of them: 200 windows of
 // 1,024 49.7, 42.8, 42.6, 43.6 us, 200 requests to 500 with heads of 128 40.8, 34.8, 34.3, 34.8.)
 constexpr int kExtra = 2;
@@ -48,7 +51,7 @@ constexpr int tile_of() { return kD * (kE4M3 ? 1 : 2) <= 128 ? 128 : 64; }
 // kRG: groups, kNR: a group's rows in eights
 template <int kD, bool kE4M3, int kRG, int kNR>
 struct Shape {
-    static constexpr int kThreads = kRG * kGroup + kLoaders * 32;
+    static constexpr int kGroups = kRG, kThreads = kRG * kGroup + kLoaders * 32;
     static constexpr int kRows = 8 * kRG * kNR;
     static constexpr int kRowBytes = kD * (kE4M3 ? 1 : 2);       // of a cached token's head
     static constexpr int kTile = tile_of<kD, kE4M3>();
@@ -70,13 +73,9 @@ struct Shape {
     static_assert(kStages >= 2 && kSmem <= most(kCtas), "shared memory");
 };
 
-// ---- the cut into runs of equal cost. A (request, head) of n units costs kExtra + n, its unit i lying at offset kExtra + i:
-// a border inside the extra part is one before its first unit.
-__host__ __device__ __forceinline__ int runs_of(int64_t total, int ctas)
-{
-    const int64_t n = (total + kMinUnits - 1) / kMinUnits;
-    return n < ctas ? static_cast<int>(n) : ctas;
-}
+// ---- the cut into runs of equal cost. A (request, head) of n units that cost w each costs (kExtra + n) w, its unit i lying
+// at offset (kExtra + i) w: a border inside a unit is one before it, a border inside the extra part one before the first
+// unit. No run costs less than a unit, so there is a border in each unit at the most.
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)  // of numbers that mostly fit 32 bits
 {
     return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
@@ -91,27 +90,30 @@ struct Cut {
 __device__ __forceinline__ int token_of(const AttentionArgs& p, int row) { return static_cast<int>(static_cast<unsigned>(row) * p.group_mul >> 16); }
 
 struct Span {
-    int beg, n, len, start, tiles, segs;  // rows; tokens; first token seen; units along the tokens; (head, row block) pairs
-    __device__ int64_t cost() const { return static_cast<int64_t>(tiles + (tiles ? kExtra : 0)) * segs; }
+    int beg, n, len, start, tiles, segs, w;  // rows; tokens; first token seen; units along the tokens; (head, row block) pairs
+    __device__ int64_t each() const { return static_cast<int64_t>(tiles + kExtra) * w; }
+    __device__ int64_t cost() const { return tiles ? each() * segs : 0; }
 };
 
-template <int kRows, int kTile>
+template <class S>
 __device__ __forceinline__ Span span_of(const AttentionArgs& p, int s, bool& bad)
 {
     const Request r = load_request(p.r, s, p.T, p.max_new, bad);
-    Span a{r.beg, r.n, r.len, 0, 0, 0};
+    Span a{r.beg, r.n, r.len, 0, 0, 0, 0};
     if (r.n == 0) return a;
     if (p.window > 0) {
         const int64_t first = static_cast<int64_t>(r.len) - r.n - p.window + 1;
         a.start = first > 0 ? static_cast<int>(first) : 0;
     }
-    a.tiles = max(1, static_cast<int>((static_cast<int64_t>(r.len) - a.start + kTile - 1) / kTile));  // a request that sees nothing has a unit, too
-    a.segs = p.c.n_kv * ((r.n * p.group + kRows - 1) / kRows);
+    // (a request that sees nothing has a unit, too)
+    a.tiles = max(1, static_cast<int>((static_cast<int64_t>(r.len) - a.start + S::kTile - 1) / S::kTile));
+    a.segs = p.c.n_kv * ((r.n * p.group + S::kRows - 1) / S::kRows);
+    a.w = S::kGroups == 1 ? 1 : kUnit + min(S::kGroups, (r.n * p.group + 7) / 8);
     return a;
 }
 
 // A place in the order of units.
-template <int kRows, int kTile>
+template <class S>
 struct Cursor {
     Span a;
     int s, seg, tile;
@@ -123,7 +125,7 @@ struct Cursor {
         if (++seg < a.segs) return;
         seg = 0;
         bool bad;
-        do a = span_of<kRows, kTile>(p, ++s, bad);
+        do a = span_of<S>(p, ++s, bad);
         while (a.segs == 0);
     }
 };
@@ -231,11 +233,12 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
     float* const qscale = wsum + kRows * kWarps;               // [kRows] (E4M3) what the row of q was divided by
     int* const row_pos = reinterpret_cast<int*>(qscale + kRows);  // [kRows] the row's position
     int64_t* const found = reinterpret_cast<int64_t*>(row_pos + kRows);  // a sum a warp, then what the search found
-    Cursor<kRows, kTile>* const start = reinterpret_cast<Cursor<kRows, kTile>*>(found + 20);
+    Cursor<S>* const start = reinterpret_cast<Cursor<S>*>(found + 20);
     uint64_t* const full = reinterpret_cast<uint64_t*>(found + 30);  // [kStages]
     uint64_t* const empty = full + kStages;                            // [kStages]
     uint64_t* const never = empty + kStages;
     int* const abort = reinterpret_cast<int*>(never + 1);
+    int* const costs = abort + 1;  // a number a warp
     const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid / 32, 0), lane = tid % 32, g = lane / 4, t4 = lane % 4;
     const uint32_t ring_a = ptx::smem_u32(ring), qs_a = ptx::smem_u32(qs), ps_a = ptx::smem_u32(ps);
 
@@ -256,9 +259,12 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
     // ---- this CTA's run: the units before each request, a block of requests a thread
     const int block = (p.r.S + kThreads - 1) / kThreads, sb = min(p.r.S, tid * block), se = min(p.r.S, sb + block);
     int64_t mine = 0;
+    int most = 1;  // what a unit costs at the most
     for (int s = sb; s < se; ++s) {
         bool bad;
-        mine += span_of<kRows, kTile>(p, s, bad).cost();
+        const Span a = span_of<S>(p, s, bad);
+        mine += a.cost();
+        if constexpr (kRG > 1) most = max(most, a.w);
         if (bad && blockIdx.x == 0) record_status(p.status, kDevBadRequest);
     }
     int64_t incl = mine;
@@ -267,15 +273,20 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
         const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
         if (lane >= o) incl += v;
     }
-    if (lane == 31) found[warp] = incl;
+    if constexpr (kRG > 1) most = __reduce_max_sync(0xFFFFFFFFu, most);
+    if (lane == 31) {
+        found[warp] = incl;
+        costs[warp] = most;
+    }
     __syncthreads();
     int64_t before = incl - mine, total = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
         if (w < warp) before += found[w];
         total += found[w];
+        if constexpr (kRG > 1) most = max(most, costs[w]);
     }
-    const int runs = runs_of(total, gridDim.x);
+    const int runs = static_cast<int>(min(static_cast<int64_t>(gridDim.x), quotient(total, most)));
     Cut cut{0, 0};
     if (runs) {
         cut.q = quotient(total, runs);
@@ -286,7 +297,7 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
         for (int s = sb; s < se; ++s) {
             bool bad;
             p.prefix[s] = u;
-            u += span_of<kRows, kTile>(p, s, bad).cost();
+            u += span_of<S>(p, s, bad).cost();
         }
         if (tid == 0) {
             p.prefix[p.r.S] = total;
@@ -301,30 +312,30 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
     for (int e = 0; e < 2; ++e) {
         if (border[e] < before || border[e] >= before + mine) continue;
         int64_t u = border[e] - before;
-        Cursor<kRows, kTile> c;
+        Cursor<S> c;
         for (c.s = sb;; ++c.s) {
             bool bad;
-            c.a = span_of<kRows, kTile>(p, c.s, bad);
+            c.a = span_of<S>(p, c.s, bad);
             if (u < c.a.cost()) break;
             u -= c.a.cost();
         }
-        const int each = c.a.tiles + kExtra;
-        c.seg = static_cast<int>(quotient(u, each));
-        c.tile = max(0, static_cast<int>(u - static_cast<int64_t>(c.seg) * each) - kExtra);
+        c.seg = static_cast<int>(quotient(u, c.a.each()));
+        u -= c.seg * c.a.each();
+        c.tile = max(0, static_cast<int>(kRG > 1 ? quotient(u, c.a.w) : u) - kExtra);
         start[e] = c;
     }
     __syncthreads();
-    Cursor<kRows, kTile> cu = start[0];
+    Cursor<S> cu = start[0];
     // the units between the borders
     int count;
     {
         const bool to_end = border[1] == total;
-        const Cursor<kRows, kTile> end = start[1];
+        const Cursor<S> end = start[1];
         const int last_s = to_end ? p.r.S : end.s;
         int64_t n = -(static_cast<int64_t>(cu.seg) * cu.a.tiles + cu.tile) + (to_end ? 0 : static_cast<int64_t>(end.seg) * end.a.tiles + end.tile);
         for (int s = cu.s; s < last_s; ++s) {
             bool bad;
-            const Span a = s == cu.s ? cu.a : span_of<kRows, kTile>(p, s, bad);
+            const Span a = s == cu.s ? cu.a : span_of<S>(p, s, bad);
             n += static_cast<int64_t>(a.tiles) * a.segs;
         }
         count = static_cast<int>(n);
@@ -831,8 +842,9 @@ constexpr int kJoinWarps = 8;
 template <int kD, bool kE4M3, int kRG, int kNR, bool kFew>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_attention_join(const __grid_constant__ AttentionArgs p)
 {
-    constexpr int kRows = 8 * kRG * kNR, kTile = tile_of<kD, kE4M3>(), kCols = kFew ? 64 : kD, kV = kCols / 32;  // columns a CTA, a lane: col0 + lane * kV ..
-    constexpr int kFlight = kFew ? 20 : 8;                                        // parts whose loads are in flight
+    using S = Shape<kD, kE4M3, kRG, kNR>;
+    constexpr int kRows = S::kRows, kCols = kFew ? 64 : kD, kV = kCols / 32;  // columns a CTA, a lane: col0 + lane * kV ..
+    constexpr int kFlight = kFew ? 20 : 8;                                    // parts whose loads are in flight
     __shared__ float sm_o[kFew ? kJoinWarps : 1][kCols], sm_ml[kJoinWarps][2];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int row = kFew ? static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x) * kJoinWarps + warp, col0 = kFew ? blockIdx.y * 64 : 0;
@@ -840,18 +852,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attention_join(const __grid
     const int t = row / p.n_q, head = row - t * p.n_q, s = t < p.T ? find_request(p.r.seg_offsets, p.r.S, t) : -1;
     Span a{};
     bool bad = true;
-    if (s >= 0 && s < p.r.S) a = span_of<kRows, kTile>(p, s, bad);
+    if (s >= 0 && s < p.r.S) a = span_of<S>(p, s, bad);
     const bool mine = a.segs != 0 && t >= a.beg && t < a.beg + a.n;
     const int h = head / p.group, in_seg = (t - a.beg) * p.group + head % p.group, r = in_seg % kRows;
     const int seg = in_seg / kRows * p.c.n_kv + h;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     if (!mine) return;  // the same in all warps of a row
-    const int64_t u0 = p.prefix[s] + static_cast<int64_t>(seg) * (a.tiles + kExtra);
+    const int64_t u0 = p.prefix[s] + seg * a.each() + kExtra * a.w, last = u0 + static_cast<int64_t>(a.tiles) * a.w - 1;  // of its units
     const Cut cut{p.prefix[p.r.S + 1], p.prefix[p.r.S + 2]};
-    const int c0 = cut.run(u0 + kExtra), n = cut.run(u0 + kExtra + a.tiles - 1) - c0 + 1;
+    const int c0 = cut.run(u0 + a.w - 1), n = cut.run(last) - c0 + 1;
     if (n == 1) return;  // finished by its run
-    const bool from_start = cut.first(c0) >= u0;
+    const bool from_start = cut.first(c0) >= u0 - kExtra * a.w;
     auto slot_of = [&](int x) { return static_cast<int64_t>(c0 + x) * 2 + (x == 0 && !from_start ? 1 : 0); };
 
     float mx = -INFINITY, sum = 0.0f, o[kV];
@@ -955,7 +967,10 @@ cudaError_t launch_head_size(const AttentionArgs& a, int sms, cudaStream_t strea
     switch (row_eights(a.group, a.max_new)) {
     case 1: return launch<kD, kE4M3, 1, 1>(a, sms, stream);
     case 2: return launch<kD, kE4M3, 2, 1>(a, sms, stream);
-    case 3: return launch<kD, kE4M3, 3, 1>(a, sms, stream);
+    // (One group reads K and V once for the three eights, three hide one another's waits: 100 requests over to 2,000, 32
+    // heads on 4 of 128, 59.5 and 66.0 us; 60, 16 on 2 of 256, 45.2 and 44.2; 200 over to 4,096, 14 on 2 of 64,
+    // 58.8 and 55.4.)
+    case 3: return launch<kD, kE4M3, kD == 128 && !kE4M3 ? 1 : 3, kD == 128 && !kE4M3 ? 3 : 1>(a, sms, stream);
     case 4: return launch<kD, kE4M3, 2, 2>(a, sms, stream);
     default: return launch<kD, kE4M3, 4, 2>(a, sms, stream);
     }
