@@ -3,8 +3,8 @@
 // with the running maximum m and sum l of the softmax: o <- o 2^(m - m') + 2^(s - m') v.
 //
 // Work: a unit is 64 cached tokens (128 where they have 128 bytes or less) of one key head against up to kRows rows (new
-// tokens x query heads of that key head). The units of all requests, in order, are cut into equal runs, one a CTA, so
-// ragged lengths balance by themselves. A (request, head) whose units lie in one run is finished there; of the others
+// tokens x query heads of that key head). The units of all requests, in order, are cut into runs of equal cost, one a
+// CTA, so ragged lengths balance by themselves. A (request, head) whose units lie in one run is finished there; of the others
 // every run leaves o, m and l in the workspace, and a second launch adds them in the order of the runs.
 // A CTA streams K and V through a ring in shared memory: two warps load (cp.async of 16 bytes a lane, addresses from
 // the page table, which is read a unit ahead; a token behind the end is filled with zeros). The rows' eights are dealt to
