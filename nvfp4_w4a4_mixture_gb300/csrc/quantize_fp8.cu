@@ -84,8 +84,10 @@ __global__ void __launch_bounds__(kThreads, 6) k_quantize_fp8(const uint16_t* __
         // two codes) the two are divided.
         float r;
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));  // off by 2^-23 of it at most
-        // the largest outside [2^-100, 2^100): s or 1 / s may leave FP32's normal numbers, and all is divided
-        const float below = m - 0x0D800000u < 0x64000000u ? r * (1.0f - 0x1p-21f) : __uint_as_float(0x7FC00000u), above = r * (1.0f + 0x1p-21f);
+        // the largest outside [2^-100, 2^100): s or 1 / s may leave FP32's normal numbers, and all is divided: products with
+        // NaN and with 0 differ but of an infinity or a NaN, whose code (of x / inf, or x / NaN) is that of NaN
+        const bool near = m - 0x0D800000u < 0x64000000u;
+        const float below = near ? r * (1.0f - 0x1p-21f) : __uint_as_float(0x7FC00000u), above = near ? r * (1.0f + 0x1p-21f) : 0.0f;
         const uint64_t below2 = pair(below, below), above2 = pair(above, above);
         uint32_t q[4 * kPieces];
 #pragma unroll
