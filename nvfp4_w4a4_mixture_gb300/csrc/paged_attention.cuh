@@ -14,8 +14,8 @@
 // mma.sync with the tokens (and V's columns) on its M side: rows are padded to eight, not sixteen. The products are 4
 // flops a byte and row, for 8 rows 32 flops a byte: memory bounds them long before the tensor cores do.
 // bf16 cache: the weights are two bf16 values (16 bits; one would add an error of the size of the output's own rounding);
-// E4M3 cache: codes become FP16 (exact), the weights are FP16, and q is scaled to FP16's range by a power of two a row
-// (exact where q is not 2^-30 of the row's largest).
+// E4M3 cache: codes become FP16 (exact), the weights are FP16 in parts of 2^-15 of the largest, and q is scaled to FP16's range
+// by a power of two a row (exact where q is not 2^-30 of the row's largest).
 // Measured: 64 requests of ragged lengths to 8,192, 32 heads on 8 of 128: 168 us, 6.2 TB/s (93 % of what a copy
 // reaches); one request over 300,001 tokens in 8 bits, 16 heads on 2 of 256: 60 us, 5.1 TB/s, 10 us of it the two launches,
 // the first loads and the join; 200 verify windows of one to three tokens, 14 heads on 2 of 64, window 1,024: 36 us, bound
@@ -224,6 +224,9 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
     constexpr int kMT = kD / 64;            // 16-column tiles of a warp's quarter of the columns
     constexpr int kKS = kD / 16;            // steps of Q K^T
     constexpr bool kQReg = kNR * kKS <= 8;  // q's fragments stay in registers
+    // m is so far below the largest score: FP16 weights are 2^15 at the most and keep their 11 bits down to 2^-14 (2^-29 of the
+    // largest), 2^-25 of one at the least; with 1 at the most, all that lies 2^-25 below the largest would be lost.
+    constexpr float kLift = kE4M3 ? 15.0f : 0.0f;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* const ring = smem;
     uint8_t* const qs = smem + kStages * S::kStage;
@@ -636,7 +639,7 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const float4 w = *reinterpret_cast<const float4*>(wmax + (base_of(nr) + 2 * t4 + x) * kWarps);
-                    const float to = fmaxf(fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w)), m[nr][x]);
+                    const float to = fmaxf(fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w)) - kLift, m[nr][x]);
                     moved |= to > m[nr][x];
                     by[x] = to == -INFINITY ? 0.0f : to;  // a row that has seen nothing yet
                     alpha[nr][x] = exp2_fast(m[nr][x] - by[x]);
