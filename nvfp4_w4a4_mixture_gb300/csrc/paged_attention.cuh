@@ -657,11 +657,15 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
                     if constexpr (kE4M3) {
                         stsm2t(at, pack_f16x2(sc[nr][y][0], sc[nr][y][1]), pack_f16x2(sc[nr][y][2], sc[nr][y][3]));
                     } else {
+                        // The high parts are cut, the low ones what is left, never 0: both are positive, so an infinite value
+                        // times them is one infinity (rounded high parts leave some low ones negative: infinities of both
+                        // signs, a NaN). 8 bits and 8 more of less than 2^-7: within 2^-16.
                         uint32_t high[2], low[2];
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
-                            high[x] = pack_bf16x2(sc[nr][y][2 * x], sc[nr][y][2 * x + 1]);
-                            low[x] = pack_bf16x2(sc[nr][y][2 * x] - __uint_as_float(high[x] << 16), sc[nr][y][2 * x + 1] - __uint_as_float(high[x] & 0xFFFF0000u));
+                            const uint32_t w0 = __float_as_uint(sc[nr][y][2 * x]) | 1u, w1 = __float_as_uint(sc[nr][y][2 * x + 1]) | 1u;
+                            high[x] = __byte_perm(w0, w1, 0x7632);
+                            low[x] = pack_bf16x2(__uint_as_float(w0) - __uint_as_float(w0 & 0xFFFF0000u), __uint_as_float(w1) - __uint_as_float(w1 & 0xFFFF0000u));
                         }
                         stsm2t(at, high[0], high[1]);
                         stsm2t(at + kRows * kPB, low[0], low[1]);
