@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
                     for (int x = 0; x < 4; ++x) big = max(big, max((w[x] << 16) & 0x7FFF0000u, w[x] & 0x7FFF0000u));
 #pragma unroll
                     for (int x = kQC / 2; x > 0; x >>= 1) big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, x));
-                    const int shift = big ? max(-110, min(100, 14 + 127 - static_cast<int>(big >> 23))) : 0;
+                    const int shift = big ? min(100, 14 + 127 - static_cast<int>(big >> 23)) : 0;  // -114 (infinities) at the least
                     const float by = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
                     if (c == 0) qscale[r] = __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
 #pragma unroll
