@@ -346,11 +346,11 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
     // A bounded wait (a waiting warp takes no issue slots). After one that ran out there are no more: the rest runs on
     // whatever is there, to its end.
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (ptx::mbar_try_wait(bar, parity)) return;
-        if (*reinterpret_cast<volatile int*>(abort) == 0 && !ptx::mbar_wait(bar, parity)) {
+        if (!ptx::mbar_try_wait(bar, parity) && *reinterpret_cast<volatile int*>(abort) == 0 && !ptx::mbar_wait(bar, parity)) {
             *reinterpret_cast<volatile int*>(abort) = 1;
             record_status(p.status, kDevTimeoutAttention);
         }
+        __syncwarp();  // the warp's matrix products take all of its lanes
     };
 
     if (warp >= kRG * kWarps) {
