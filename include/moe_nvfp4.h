@@ -432,8 +432,8 @@ moe_status_t moe_cache_append(const moe_kv_cache_t* C, const moe_requests_t* R, 
  *     out = sum_t softmax_t(scale * q . k_t) v_t    over 0 <= t <= p, with a window over p - window < t <= p
  *     lse = log sum_t exp(scale * q . k_t)          (natural logarithm)
  *   A row that sees nothing (a negative position) has out = 0 and lse = -inf. Sums are FP32; the weights are held in 16
- *   significant bits or more (bf16 cache) or 11 (E4M3; below 2^-29 of the row's largest, steps of 2^-39 of that) for the
- *   second product. What lies behind a request's last token or outside a row's window takes no part, whatever its bits;
+ *   significant bits or more (bf16 cache) or 22 (E4M3; within 2^-40 of the row's largest at the least) for the second
+ *   product. What lies behind a request's last token or outside a row's window takes no part, whatever its bits;
  *   an infinite value that a row sees gives its infinity where its weight is 2^-110 of the row's largest or more (NaN below).
  *   q, out: bf16 [T][n_q][D], ld_*: elements between two tokens, every row on 16 bytes; out may be q (the same
  *   address and row stride), no other overlap. lse: nullable, FP32 [T][n_q]. n_q a multiple of n_kv, n_q / n_kv <= 64.

@@ -13,9 +13,12 @@
 // join.
 // mma.sync with the tokens (and V's columns) on its M side: rows are padded to eight, not sixteen. The products are 4
 // flops a byte and row, for 8 rows 32 flops a byte: memory bounds them long before the tensor cores do.
-// bf16 cache: the weights are two bf16 values (16 bits; one would add an error of the size of the output's own rounding);
-// E4M3 cache: codes become FP16 (exact), the weights are FP16 in parts of 2^-15 of the largest, and q is scaled to FP16's range
-// by a power of two a row (exact where q is not 2^-30 of the row's largest).
+// Weights in the second product: of a bf16 cache two bf16 values (16 bits; one would add an error of the size of the output's
+// own rounding, three took 39.4 us for 36.2 in 200 windows of 1,024 and 133 for 116 with 128 rows a key head, for bits that
+// are 2^-8 of the output's rounding); of an E4M3 cache, whose codes become FP16 exactly, two FP16 values (22 bits) in parts of
+// 2^-15 of the largest. (One, 11 bits, is off by an eighth of the output's rounding: 1 request over 300,001 59.5 us either
+// way, 200 over to 2,000, 14 heads on 2 of 64, 22.0 and 20.8, 100 of four tokens over to 2,000, 32 on 4 of 128, 64.7 and 60.4.)
+// q of an E4M3 cache is scaled to FP16's range by a power of two a row (exact where q is not 2^-30 of the row's largest).
 // Measured: 64 requests of ragged lengths to 8,192, 32 heads on 8 of 128: 168 us, 6.2 TB/s (93 % of what a copy
 // reaches); one request over 300,001 tokens in 8 bits, 16 heads on 2 of 256: 60 us, 5.1 TB/s, 10 us of it the two launches,
 // the first loads and the join; 200 verify windows of one to three tokens, 14 heads on 2 of 64, window 1,024: 36 us, bound
@@ -57,7 +60,8 @@ struct Shape {
     static constexpr int kTile = tile_of<kD, kE4M3>();
     static constexpr int kStage = 2 * kTile * kRowBytes;         // K, V
     static constexpr int kQ = kRows * kD * 2;
-    static constexpr int kP = kRows * kTile * 2 * (kE4M3 ? 1 : 2);
+    static constexpr int kParts = 2;                             // values that hold a weight
+    static constexpr int kP = kRows * kTile * 2 * kParts;
     static constexpr int kFixed = kQ + kP + kRows * (2 * kWarps * 4 + 8) + 512;
     // As many CTAs an SM as hold three stages each, and as the registers of so many rows allow: one to three. Two of two
     // stages are better than one, too (100 requests of 4 new tokens over to 2,000, 32 heads on 4 of 128: 67 us against 77),
@@ -224,13 +228,13 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
     constexpr int kMT = kD / 64;            // 16-column tiles of a warp's quarter of the columns
     constexpr int kKS = kD / 16;            // steps of Q K^T
     constexpr bool kQReg = kNR * kKS <= 8;  // q's fragments stay in registers
-    // m is so far below the largest score: FP16 weights are 2^15 at the most and keep their 11 bits down to 2^-14 (2^-29 of the
-    // largest), 2^-25 of one at the least; with 1 at the most, all that lies 2^-25 below the largest would be lost.
+    // m is so far below the largest score: FP16 weights are 2^15 at the most, and both parts together within 2^-22 of a weight
+    // or 2^-25 (2^-40 of the largest); with 1 at the most, all that lies 2^-25 below the largest would be lost.
     constexpr float kLift = kE4M3 ? 15.0f : 0.0f;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* const ring = smem;
     uint8_t* const qs = smem + kStages * S::kStage;
-    uint8_t* const ps = qs + S::kQ;         // weights: [kRows][kTile] 16-bit, bf16: the high parts, then the low ones
+    uint8_t* const ps = qs + S::kQ;         // weights: [kRows][kTile] 16-bit, the high parts, then the low ones
     float* const wmax = reinterpret_cast<float*>(ps + S::kP);  // [kRows][kWarps]
     float* const wsum = wmax + kRows * kWarps;                 // [kRows][kWarps]
     float* const qscale = wsum + kRows * kWarps;               // [kRows] (E4M3) what the row of q was divided by
@@ -655,7 +659,14 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
                     // rows of kTile tokens: these 16 are two pieces
                     const uint32_t at = (p_mine ^ (y * 128)) + base_of(nr) * kPB;
                     if constexpr (kE4M3) {
-                        stsm2t(at, pack_f16x2(sc[nr][y][0], sc[nr][y][1]), pack_f16x2(sc[nr][y][2], sc[nr][y][3]));
+                        uint32_t high[2], low[2];
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            high[x] = pack_f16x2(sc[nr][y][2 * x], sc[nr][y][2 * x + 1]);
+                            low[x] = pack_f16x2(sc[nr][y][2 * x] - f16_to_f32(high[x] & 0xFFFFu), sc[nr][y][2 * x + 1] - f16_to_f32(high[x] >> 16));
+                        }
+                        stsm2t(at, high[0], high[1]);
+                        stsm2t(at + kRows * kPB, low[0], low[1]);
                     } else {
                         // The high parts are cut, the low ones what is left, never 0: both are positive, so an infinite value
                         // times them is one infinity (rounded high parts leave some low ones negative: infinities of both
@@ -706,7 +717,7 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
                             if (!sees(row_pos[r], tok)) continue;
                             const uint8_t* pp = ps + piece<kPB>(r, tok / 8) + tok % 8 * 2;
                             float wt;
-                            if constexpr (kE4M3) wt = f16_to_f32(*reinterpret_cast<const uint16_t*>(pp));
+                            if constexpr (kE4M3) wt = f16_to_f32(*reinterpret_cast<const uint16_t*>(pp)) + f16_to_f32(*reinterpret_cast<const uint16_t*>(pp + kRows * kPB));
                             else wt = bf16_to_f32(*reinterpret_cast<const uint16_t*>(pp)) + bf16_to_f32(*reinterpret_cast<const uint16_t*>(pp + kRows * kPB));
 #pragma unroll
                             for (int mt = 0; mt < kMT; ++mt)
@@ -740,12 +751,12 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
             // ---- O^T += V^T P^T, this warp's quarter of the columns, 32 tokens at a time
 #pragma unroll 1
             for (int kk = 0; kk < kTile / 16; kk += 2) {
-                uint32_t b[kNR][4], bl[kE4M3 ? 1 : kNR][4];
+                uint32_t b[S::kParts][kNR][4];
 #pragma unroll
                 for (int nr = 0; nr < kNR; ++nr) {
                     const uint32_t at = (p_lane ^ (kk * 32)) + base_of(nr) * kPB;
-                    ldsm4(at, b[nr]);
-                    if constexpr (!kE4M3) ldsm4(at + kRows * kPB, bl[nr]);
+#pragma unroll
+                    for (int z = 0; z < S::kParts; ++z) ldsm4(at + z * kRows * kPB, b[z][nr]);
                 }
 #pragma unroll
                 for (int mt = 0; mt < kMT; ++mt) {
@@ -764,10 +775,9 @@ __global__ void __launch_bounds__(Shape<kD, kE4M3, kRG, kNR>::kThreads, Shape<kD
 #pragma unroll
                     for (int nr = 0; nr < kNR; ++nr)
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            mma<kE4M3>(o[mt][nr], a[x][0], a[x][1], a[x][2], a[x][3], b[nr][2 * x], b[nr][2 * x + 1]);
-                            if constexpr (!kE4M3) mma<false>(o[mt][nr], a[x][0], a[x][1], a[x][2], a[x][3], bl[nr][2 * x], bl[nr][2 * x + 1]);
-                        }
+                        for (int x = 0; x < 2; ++x)
+#pragma unroll
+                            for (int z = 0; z < S::kParts; ++z) mma<kE4M3>(o[mt][nr], a[x][0], a[x][1], a[x][2], a[x][3], b[z][nr][2 * x], b[z][nr][2 * x + 1]);
                 }
             }
         }

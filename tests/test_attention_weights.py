@@ -49,3 +49,31 @@ def test_many_small_weights_beside_a_large_one(m, dtype, S, L, new, below):  # n
             got = out[i::new, j].double()
             assert bool(((got - want).abs() <= tol).all()), float(((got - want).abs() / want.abs()).max())
             assert bool(((lse[i::new, j].double() - torch.logsumexp(z, 0)).abs() <= delta + 2 * (n + 16) * U32 + 8 * U32 * d).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, E4M3])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_weights_keep_their_bits_where_values_cancel(m, dtype, D):  # noqa: F811
+    """Few tokens of weights of one size and values of both signs: the bf16 output shows the weights' own bits where the sum is
+    small beside its terms."""
+    S, L, page = 400, 16, 16
+    b = Batch(43, [1], [L], 1, D, page, dtype).fill()
+    v = torch.where(b.normal(L, 1, D) > 0, 1.0, -1.0) * (1 + torch.randint(8, (L, 1, D), generator=b.g, device="cuda") / 8)
+    b.put(b.v_cache, 0, range(L), (v * 16).to(dtype))
+    if dtype is E4M3:
+        b.v_scale.fill_(1.0 / 16)
+    q = b.normal(S, 4, D, std=0.1).to(BF)
+    out = m.moe_paged_attention(q, b.k_cache, b.v_cache, ints(list(range(S + 1))), ints([L] * S), b.pages.expand(S, -1).contiguous(),
+                                k_scale=b.k_scale, v_scale=b.v_scale)
+    m.moe_read_device_status()
+    kk, vv = (x[:, 0] for x in b.values(0))
+    z = q.double() @ kk.T * D ** -0.5
+    p = torch.softmax(z, 2)
+    want, size = p @ vv, p @ vv.abs()
+    top = float(((q.double().abs() @ kk.abs().T) * D ** -0.5).max())
+    # scores off by their sums' roundings, weights by twice that, the exponential's 2^-22 and their own 2^-16 or 2^-22 (and
+    # 2^-40), sums of 16, the output's rounding
+    delta = 2 * ((D + 8) * U32 * top + 2.0 ** -22)
+    tol = 2.0 ** -8 * want.abs() + (1 + 2.0 ** -8) * size * (2 * delta + (2.0 ** -16 if dtype is BF else 2.0 ** -21) + 2 * 32 * U32)
+    assert bool((want.abs() < 2.0 ** -8 * size).any())
+    assert bool(((out.double() - want).abs() <= tol).all()), float(((out.double() - want).abs() / size).max())
