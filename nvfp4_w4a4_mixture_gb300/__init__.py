@@ -261,13 +261,12 @@ def moe_set_wait_test_hook(ws, wait_limit_us, ready_extra):
 
 
 def moe_read_device_status(ws=None):
-    """Raises what the calls on the workspace have reported since the last reading (None: the default workspaces)."""
+    """Raises what the calls on the workspace have reported since the last reading. None: the default workspaces, after all calls
+    of the device's streams are over; a workspace: after those of the current stream."""
     if ws is None:
         dev = torch.cuda.current_device()
-        of_streams = [w for key, w in _attention_ws.items() if key[0] == dev]
-        if len(of_streams) > 1:  # their calls, too, have to be over
-            torch.cuda.synchronize()
-        for w in [_adapter_ws.get(dev)] + of_streams:
+        torch.cuda.synchronize()  # any stream's calls report to them
+        for w in [_adapter_ws.get(dev)] + [w for key, w in _attention_ws.items() if key[0] == dev]:
             if w is not None:
                 _check(lib().moe_read_device_status(w.ptr, _stream()))
         ws = _ws(4096)

@@ -322,10 +322,10 @@ moe_status_t moe_read_device_status(void* ws, moe_stream_t stream)
 {
     if (!ws) return fail(MOE_ERR_INVALID_ARG, "workspace is NULL");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int status = 0;  // read and cleared in the stream's order, and cleared when this returns
+    MOE_CUDA(cudaMemcpyAsync(&status, ws, sizeof(int), cudaMemcpyDeviceToHost, s), "read status");
+    MOE_CUDA(cudaMemsetAsync(ws, 0, sizeof(int), s), "clear status");
     MOE_CUDA(cudaStreamSynchronize(s), "cudaStreamSynchronize");
-    int status = 0;
-    MOE_CUDA(cudaMemcpy(&status, ws, sizeof(int), cudaMemcpyDeviceToHost), "read status");
-    MOE_CUDA(cudaMemset(ws, 0, sizeof(int)), "clear status");
     if (status & kDevTimeoutGemm) return fail(MOE_ERR_DEVICE_TIMEOUT, "device status 0x%x: grouped GEMM wait timed out", status);
     if (status & kDevTimeoutRouter) return fail(MOE_ERR_DEVICE_TIMEOUT, "device status 0x%x: router wait timed out", status);
     if (status & kDevTimeoutCombine) return fail(MOE_ERR_DEVICE_TIMEOUT, "device status 0x%x: combine wait timed out", status);

@@ -1,0 +1,53 @@
+"""GPU: moe_read_device_status() without a workspace reads what calls on every stream have reported, also those still under way."""
+import pytest
+import torch
+
+from test_attention_ops import Batch, BF, ints, m  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def batch():
+    b = Batch(50, [1, 1], [40, 50], 1, 64, 16).fill()
+    q, k, v = (b.normal(2, 1, 64).to(BF) for _ in range(3))
+    return b, q, k, v
+
+
+@pytest.mark.parametrize("call", ["attention", "append"])
+@pytest.mark.parametrize("others", [0, 2])
+def test_a_call_on_another_stream_is_waited_for(m, call, others):  # noqa: F811
+    b, q, k, v = batch()
+    m._attention_ws.clear()
+    good = m.moe_cache_append if call == "append" else m.moe_paged_attention
+    args = (None, k, v) if call == "append" else (q,)
+    for _ in range(others):  # streams that have called before
+        with torch.cuda.stream(torch.cuda.Stream()):
+            good(*args, b.k_cache, b.v_cache, *b.tables())
+    torch.cuda.synchronize()
+    m.moe_read_device_status()
+    side, bad = torch.cuda.Stream(), ints([40, -1])
+    with torch.cuda.stream(side):
+        good(*args, b.k_cache, b.v_cache, *b.tables())  # (its workspace is there)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+        good(*args, b.k_cache, b.v_cache, b.offsets, bad, b.pages)
+    with pytest.raises(m.MoeError, match="kv_len"):
+        m.moe_read_device_status()
+    m.moe_read_device_status()
+    torch.cuda.synchronize()
+    m.moe_read_device_status()
+
+
+def test_a_reading_clears_before_the_next_call(m):  # noqa: F811
+    """A call on a stream of its own directly after a reading: its report is not cleared by that reading."""
+    b, q, _, _ = batch()
+    bad, side = ints([40, -1]), torch.cuda.Stream()
+    ws = m.Workspace(m.moe_attention_workspace_bytes(2, 1, 1, 64, 1))
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(50):
+            m.moe_paged_attention(q, b.k_cache, b.v_cache, b.offsets, bad, b.pages, ws=ws)
+            with pytest.raises(m.MoeError, match="kv_len"):
+                m.moe_read_device_status(ws)
+        m.moe_read_device_status(ws)
