@@ -440,11 +440,13 @@ moe_status_t moe_cache_append(const moe_kv_cache_t* C, const moe_requests_t* R, 
  *   max_new in [1, 16]: the most rows of a request; a request of more, or of more than 2^31 - 65 tokens, is skipped and
  *   reported. window: 0 for none.
  *   The cache's length is split over the multiprocessors, the parts joined in a second launch in a fixed order.
- *   ws: >= moe_attention_workspace_bytes(S, n_q, n_kv, D, max_new). T = 0 returns MOE_OK after the shape check.
+ *   ws: >= moe_attention_workspace_bytes(S, n_q, n_kv, D, max_new); with report it needs no zeroed header. Calls that may run
+ *   at the same time need a ws each and may share a report. T = 0 returns MOE_OK after the shape check.
  * ------------------------------------------------------------------------------------------- */
 typedef struct {
     int n_q, max_new, window;
     float scale;            /* finite */
+    void* report;           /* nullable: a workspace (>= 256 bytes) whose status word and test hook the call uses in place of ws's */
 } moe_attention_t;
 
 moe_status_t moe_paged_attention(const moe_kv_cache_t* C, const moe_requests_t* R, const moe_attention_t* A,

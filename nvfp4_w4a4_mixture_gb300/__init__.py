@@ -91,7 +91,8 @@ class RotaryDesc(ctypes.Structure):
 
 
 class AttentionDesc(ctypes.Structure):
-    _fields_ = [("n_q", ctypes.c_int), ("max_new", ctypes.c_int), ("window", ctypes.c_int), ("scale", ctypes.c_float)]
+    _fields_ = [("n_q", ctypes.c_int), ("max_new", ctypes.c_int), ("window", ctypes.c_int), ("scale", ctypes.c_float),
+                ("report", ctypes.c_void_p)]
 
 
 _lib = None
@@ -207,14 +208,15 @@ def moe_workspace_bytes_host(H, E, k, I, T):
 
 
 class Workspace:
-    """Device scratch for the library calls (header zeroed once)."""
+    """Device scratch for the library calls (header zeroed once; cleared=False: not, for a call that reports elsewhere)."""
 
-    def __init__(self, nbytes, device="cuda"):
+    def __init__(self, nbytes, device="cuda", cleared=True):
         self.nbytes = int(max(nbytes, 4096))
         self.buf = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=device)
         off = (-self.buf.data_ptr()) % 256
         self.tensor = self.buf[off: off + self.nbytes]
-        self.tensor[:256].zero_()
+        if cleared:
+            self.tensor[:256].zero_()
         self.address = self.tensor.data_ptr()
 
     @property
@@ -238,9 +240,9 @@ _adapter_ws = {}
 
 
 def _adapter_workspace():
-    """The workspace of moe_adapter_add, moe_cache_append and moe_gemm_fp8 where the caller gives none: its header is all that
-    they use, so it is never replaced by a larger one, which would lose its report and leave captured calls with memory
-    that was given back."""
+    """The workspace of moe_adapter_add, moe_cache_append and moe_gemm_fp8 where the caller gives none, and what
+    moe_paged_attention reports to then: its header is all that they use, so it is never replaced by a larger one, which
+    would lose its report and leave captured calls with memory that was given back."""
     dev = torch._C._cuda_getDevice()
     w = _adapter_ws.get(dev)
     if w is None:
@@ -266,9 +268,9 @@ def moe_read_device_status(ws=None):
     if ws is None:
         dev = torch.cuda.current_device()
         torch.cuda.synchronize()  # any stream's calls report to them
-        for w in [_adapter_ws.get(dev)] + [w for key, w in _attention_ws.items() if key[0] == dev]:
-            if w is not None:
-                _check(lib().moe_read_device_status(w.ptr, _stream()))
+        w = _adapter_ws.get(dev)
+        if w is not None:
+            _check(lib().moe_read_device_status(w.ptr, _stream()))
         ws = _ws(4096)
     _check(lib().moe_read_device_status(ws.ptr, _stream()))
 
@@ -739,8 +741,8 @@ _attention_ws, _attention_bytes = {}, {}
 
 
 def _attention_workspace(S, n_q, n_kv, D, max_new):
-    """moe_paged_attention's workspace where the caller gives none: one for each stream, since calls on two streams run
-    at the same time. A capture's belongs to its graph (the memory is the graph's, its report is lost)."""
+    """moe_paged_attention's scratch where the caller gives none: one for each stream, since calls on two streams run at the
+    same time; a capture's belongs to its graph. What calls report goes to _adapter_workspace()."""
     dev = torch._C._cuda_getDevice()
     shape = S, n_q, n_kv, D, max_new, dev
     nbytes = _attention_bytes.get(shape)
@@ -751,14 +753,11 @@ def _attention_workspace(S, n_q, n_kv, D, max_new):
             _attention_bytes.clear()
         nbytes = _attention_bytes[shape] = _lib.moe_attention_workspace_bytes(*shape[:5])
     if torch._C._cuda_isCurrentStreamCapturing():
-        return Workspace(nbytes)
+        return Workspace(nbytes, cleared=False)
     key = dev, _stream()
     w = _attention_ws.get(key)
     if w is None or w.nbytes < nbytes:
-        old, w = w, Workspace(nbytes)
-        if old is not None:  # what its calls have reported stays readable
-            w.tensor[:4].copy_(old.tensor[:4])
-        _attention_ws[key] = w
+        w = _attention_ws[key] = Workspace(nbytes, cleared=False)
     return w
 
 
@@ -774,16 +773,18 @@ def moe_paged_attention(q, k_cache, v_cache, seg_offsets, kv_len, pages, max_new
         out = torch.empty(q.shape, dtype=_BF16, device=q.device)
     if scale is None:
         scale = q.shape[-1] ** -0.5
-    status = -1
+    status, report = -1, None
     if q.is_cuda:
         if ws is None:
+            header = _adapter_workspace()  # (held until the launch: a capture's own is given back then)
+            report = header.address
             try:
                 ws = _attention_workspace(kv_len.shape[0], q.shape[1], k_cache.shape[2], k_cache.shape[3], max_new)
             except IndexError:
                 raise ValueError("q must have shape [T, n_q, D], k_cache [n_pages, page_size, n_kv, D] and kv_len [S]") from None
         if _calls is not None:
             status = _calls.paged_attention(q, k_cache, v_cache, k_scale, v_scale, seg_offsets, kv_len, pages, max_new, scale, window, out,
-                                            lse, ws.address, ws.nbytes, _stream())
+                                            lse, ws.address, ws.nbytes, _stream(), report or 0)
     if status < 0:
         T, n_q, D = q.shape
         if k_cache.shape[3:] != (D,):
@@ -793,7 +794,7 @@ def moe_paged_attention(q, k_cache, v_cache, seg_offsets, kv_len, pages, max_new
         q_ptr, q_ld = _heads(q, "q", _BF16, (T, n_q, D))
         o_ptr, o_ld = _heads(out, "out", _BF16, (T, n_q, D))
         status = lib().moe_paged_attention(_cache_desc(k_cache, v_cache, k_scale, v_scale), _requests_desc(seg_offsets, kv_len, pages),
-                                           AttentionDesc(n_q, max_new, window, scale), q_ptr, q_ld, T, o_ptr, o_ld,
+                                           AttentionDesc(n_q, max_new, window, scale, report), q_ptr, q_ld, T, o_ptr, o_ld,
                                            None if lse is None else _whole(lse, "lse", _F32, (T, n_q)), ws.address, ws.nbytes, _stream())
     if status:
         _check(status)

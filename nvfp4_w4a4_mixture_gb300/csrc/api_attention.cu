@@ -208,6 +208,7 @@ moe_status_t moe_paged_attention(const moe_kv_cache_t* C, const moe_requests_t* 
     if (lse && (rows_overlap(lse, lw, lw, q, ld_q * 2, w * 2, T) || rows_overlap(lse, lw, lw, out, ld_out * 2, w * 2, T) || overlaps_tables(lse, lw, lw, T, R, C)))
         return fail(MOE_ERR_INVALID_ARG, "lse overlaps another argument");
     MOE_TRY(check_ws(ws, ws_bytes, sizeof(WsHeader)));
+    if (A->report) MOE_TRY(check_ws(A->report, sizeof(WsHeader), sizeof(WsHeader)));
     MOE_TRY(check_device());
     const int sms = device_sm_count();
     MOE_TRY(check_ws(ws, ws_bytes, attention_workspace_bytes(R->S, A->n_q, C->n_kv, C->D, A->max_new, sms)));
@@ -223,8 +224,9 @@ moe_status_t moe_paged_attention(const moe_kv_cache_t* C, const moe_requests_t* 
     a.out = out;
     a.ld_out = ld_out;
     a.lse = lse;
-    a.status = &static_cast<WsHeader*>(ws)->status;
-    a.hooks = static_cast<const WsHeader*>(ws);
+    WsHeader* const header = static_cast<WsHeader*>(A->report ? A->report : ws);
+    a.status = &header->status;
+    a.hooks = header;
     MOE_CUDA(launch_paged_attention(a, ws, sms, static_cast<cudaStream_t>(stream)), "attention launch");
     return MOE_OK;
 }

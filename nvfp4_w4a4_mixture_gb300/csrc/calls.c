@@ -365,7 +365,7 @@ static PyObject* cache_append(PyObject* self, PyObject* const* a, Py_ssize_t n)
 }
 
 /* paged_attention(q, k_cache, v_cache, k_scale, v_scale, seg_offsets, kv_len, pages, max_new, scale, window, out, lse, ws, ws_bytes,
- * stream) */
+ * stream, report) */
 static PyObject* paged_attention(PyObject* self, PyObject* const* a, Py_ssize_t n)
 {
     moe_kv_cache_t c;
@@ -376,7 +376,7 @@ static PyObject* paged_attention(PyObject* self, PyObject* const* a, Py_ssize_t 
     size_t ws_bytes;
     moe_status_t s;
     (void)self;
-    if (n != 16 || !f_attention) return leave();
+    if (n != 17 || !f_attention) return leave();
     memset(&c, 0, sizeof c);
     memset(&r, 0, sizeof r);
     if (!heads(a[0], qd, &ld_q, &q)) return leave();
@@ -395,6 +395,7 @@ static PyObject* paged_attention(PyObject* self, PyObject* const* a, Py_ssize_t 
     ws = PyLong_AsVoidPtr(a[13]);
     ws_bytes = PyLong_AsSize_t(a[14]);
     p = PyLong_AsVoidPtr(a[15]);
+    d.report = PyLong_AsVoidPtr(a[16]);
     if (PyErr_Occurred()) return leave();
     Py_BEGIN_ALLOW_THREADS
     s = f_attention(&c, &r, &d, q, ld_q, (int)qd[0], o, ld_o, lse, ws, ws_bytes, p);
