@@ -548,7 +548,8 @@ moe_status_t moe_layer_workspace_view(const moe_layer_t* L, int T, moe_layer_vie
  *   with ready_extra > 0 every down tile of moe_layer_forward times out; the launch stops, frees
  *   its tensor memory and records MOE_ERR_DEVICE_TIMEOUT for moe_read_device_status(). In
  *   moe_adapter_add (requests that go to its tensor-memory kernel) the wait for A x does the same,
- *   in moe_gemm_fp8 and moe_paged_attention the first wait of a CTA.
+ *   in moe_gemm_fp8 and moe_paged_attention the first wait of a CTA; with ready_extra = 2 in moe_gemm_fp8's kernel for few
+ *   tokens that of one of four warps at a later block, the other warps and CTAs going on.
  *   Another call with (0, 0) restores normal operation. The values are written into the workspace header
  *   in stream order (a one-thread kernel on `stream`).
  * ------------------------------------------------------------------------------------------- */
