@@ -309,7 +309,9 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     if (cs > 1) ptx::cluster_arrive_all();  // waited for before the first store to another CTA
     ptx::tc_fence_after();
     const uint32_t tmem = st.tmem;
+    bool failed = false;
     auto fail = [&]() {
+        failed = true;
         if (atomicExch(&st.abort, 1) == 0) record_status(p.status, kDevTimeoutGemmFp8);
     };
     auto all = [&](bool got) { return __all_sync(0xFFFFFFFFu, got) != 0; };
@@ -419,6 +421,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     };
     if (cs > 1) {
         ptx::cluster_wait();
+        // without one CTA's part there is no sum: every CTA of the cluster hears of it
+        if (__any_sync(0xFFFFFFFFu, failed) && lane < cs) ptx::cluster_store(ptx::cluster_addr(&st.abort, lane), __int_as_float(1));
         if (warp >= 2) {
 #pragma unroll
             for (int c = 0; c < kN; ++c) {
