@@ -409,7 +409,7 @@ typedef struct {
  *   q: bf16 [T][n_q][D], k and v: bf16 [T][n_kv][D]; ld_*: elements between two tokens, heads contiguous, every row on
  *   16 bytes (the three may be columns of one buffer). q_out: bf16 [T][n_q][D], may be q (the same address and row
  *   stride), no other overlap. n_q = 0: keys and values alone (q and q_out NULL). rot: a multiple of 16 in [0, D].
- *   1 <= n_kv <= 1024, n_q <= 1024. Two rows with one place in the cache (a page shared by requests that both write
+ *   1 <= n_kv <= 1024, n_q <= 1024. Keys and values share no element (they may lie by turns). Two rows with one place in the cache (a page shared by requests that both write
  *   to it) leave either's values there.
  *   ws: >= 256 bytes (status word). T = 0 returns MOE_OK after the shape check.
  * ------------------------------------------------------------------------------------------- */

@@ -1,6 +1,7 @@
 // api_attention.cu -- the C ABI of the attention half of a block (include/moe_nvfp4.h): checks on the host, then the launch.
 #include <algorithm>
 #include <cmath>
+#include <utility>
 
 #include "api.cuh"
 #include "attention.cuh"
@@ -41,6 +42,46 @@ int64_t cache_span(const moe_kv_cache_t* C)
     return ((C->n_pages - 1) * C->ld_page + (C->page_size - 1) * C->ld_slot + (C->n_kv - 1) * C->ld_head + C->D) * es;
 }
 
+// The cache's dimensions of more than one by their strides, the least first, with the elements from the first to behind the
+// last of what lies below each (extent[n]: of the whole).
+struct Levels {
+    int n;
+    int64_t ld[3], count[3], extent[4];
+};
+
+Levels levels_of(const moe_kv_cache_t* C)
+{
+    Levels l{0, {C->ld_page, C->ld_slot, C->ld_head}, {C->n_pages, C->page_size, C->n_kv}, {C->D}};
+    for (int i = 0; i < 3; ++i) {
+        int at = i;
+        for (int j = i + 1; j < 3; ++j)
+            if (l.ld[j] < l.ld[at]) at = j;
+        std::swap(l.ld[i], l.ld[at]);
+        std::swap(l.count[i], l.count[at]);
+    }
+    for (int i = 0; i < 3; ++i) {
+        if (l.count[i] == 1) continue;
+        l.ld[l.n] = l.ld[i];
+        l.count[l.n] = l.count[i];
+        l.extent[l.n + 1] = l.extent[l.n] + (l.count[i] - 1) * l.ld[i];
+        ++l.n;
+    }
+    return l;
+}
+
+// Whether some element of the lowest `at` levels and one of the same shape that begins d elements behind it are one: d is a
+// difference of their indices times the strides. Of each stride it holds two multiples at the most, since what lies below
+// is no longer than the stride.
+bool meet(const Levels& l, int at, int64_t d)
+{
+    if (d <= -l.extent[at] || d >= l.extent[at]) return false;
+    if (at == 0) return true;
+    const int64_t ld = l.ld[at - 1], down = d >= 0 ? d / ld : -((ld - 1 - d) / ld);
+    for (int64_t i = down; i <= down + 1; ++i)
+        if (i > -l.count[at - 1] && i < l.count[at - 1] && meet(l, at - 1, d - i * ld)) return true;
+    return false;
+}
+
 moe_status_t check_cache_memory(const moe_kv_cache_t* C)
 {
     const int es = C->dtype == MOE_DTYPE_E4M3 ? 1 : 2;
@@ -51,22 +92,10 @@ moe_status_t check_cache_memory(const moe_kv_cache_t* C)
         return fail(MOE_ERR_MISALIGNED, "cache strides %lld, %lld, %lld: every head must start on 16 bytes", (long long)C->ld_page,
                     (long long)C->ld_slot, (long long)C->ld_head);
     // pages, slots and heads do not lie on one another: sorted by stride, each is at least the extent of those below
-    struct {
-        int64_t ld, n;
-    } d[3] = {{C->ld_page, C->n_pages}, {C->ld_slot, C->page_size}, {C->ld_head, C->n_kv}};
-    int64_t extent = C->D;
-    bool used[3] = {false, false, false};
-    for (int k = 0; k < 3; ++k) {
-        int at = -1;
-        for (int i = 0; i < 3; ++i)
-            if (!used[i] && (at < 0 || d[i].ld < d[at].ld)) at = i;
-        used[at] = true;
-        if (d[at].n > 1) {
-            if (d[at].ld < extent) return fail(MOE_ERR_INVALID_ARG, "cache strides %lld, %lld, %lld: heads overlap", (long long)C->ld_page,
+    const Levels l = levels_of(C);
+    for (int i = 0; i < l.n; ++i)
+        if (l.ld[i] < l.extent[i]) return fail(MOE_ERR_INVALID_ARG, "cache strides %lld, %lld, %lld: heads overlap", (long long)C->ld_page,
                                                (long long)C->ld_slot, (long long)C->ld_head);
-            extent += (d[at].n - 1) * d[at].ld;
-        }
-    }
     if ((C->k_scale && !aligned(C->k_scale, 4)) || (C->v_scale && !aligned(C->v_scale, 4)))
         return fail(MOE_ERR_MISALIGNED, "k_scale and v_scale must be 4-byte aligned");
     return MOE_OK;
@@ -142,7 +171,9 @@ moe_status_t moe_cache_append(const moe_kv_cache_t* C, const moe_requests_t* R, 
         if (rows_overlap_bytes(q, ld_q * 2, wq * 2, T, cache, span) || rows_overlap_bytes(k, ld_k * 2, wk * 2, T, cache, span) ||
             rows_overlap_bytes(v, ld_v * 2, wk * 2, T, cache, span))
             return fail(MOE_ERR_INVALID_ARG, "the cache overlaps q, k or v");
-    if (C->k == C->v) return fail(MOE_ERR_INVALID_ARG, "keys and values in one place");
+    const int64_t apart = static_cast<const char*>(C->v) - static_cast<const char*>(C->k);  // (a multiple of 16)
+    const Levels l = levels_of(C);
+    if (meet(l, l.n, apart / (C->dtype == MOE_DTYPE_E4M3 ? 1 : 2))) return fail(MOE_ERR_INVALID_ARG, "keys and values lie on one another");
     MOE_TRY(check_ws(ws, ws_bytes, sizeof(WsHeader)));
     MOE_TRY(check_device());
     a.T = T;
