@@ -7,6 +7,7 @@ the shared library is missing or returns an error.
 import ctypes
 import importlib.machinery
 import importlib.util
+import operator
 import os
 import sysconfig
 
@@ -644,7 +645,11 @@ _E4M3 = torch.float8_e4m3fn
 
 
 def moe_attention_workspace_bytes(S, n_q, n_kv, D, max_new):
-    return int(lib().moe_attention_workspace_bytes(S, n_q, n_kv, D, max_new))
+    """Bytes for moe_paged_attention with these sizes; 0 for sizes that it refuses."""
+    sizes = [operator.index(v) for v in (S, n_q, n_kv, D, max_new)]
+    if any(not -_INT_MAX <= v <= _INT_MAX for v in sizes):
+        return 0
+    return int(lib().moe_attention_workspace_bytes(*sizes))
 
 
 def _heads(t, name, dtype, shape):
@@ -747,11 +752,9 @@ def _attention_workspace(S, n_q, n_kv, D, max_new):
     shape = S, n_q, n_kv, D, max_new, dev
     nbytes = _attention_bytes.get(shape)
     if nbytes is None:
-        if not isinstance(max_new, int) or not 0 <= max_new <= _INT_MAX:
-            raise ValueError("max_new is an int of 32 bits")
         if len(_attention_bytes) > 4096:  # (batches of changing size: a number each)
             _attention_bytes.clear()
-        nbytes = _attention_bytes[shape] = _lib.moe_attention_workspace_bytes(*shape[:5])
+        nbytes = _attention_bytes[shape] = moe_attention_workspace_bytes(*shape[:5])
     if torch._C._cuda_isCurrentStreamCapturing():
         return Workspace(nbytes, cleared=False)
     key = dev, _stream()
@@ -789,6 +792,7 @@ def moe_paged_attention(q, k_cache, v_cache, seg_offsets, kv_len, pages, max_new
         T, n_q, D = q.shape
         if k_cache.shape[3:] != (D,):
             raise ValueError("k_cache of %s for q of %s" % (tuple(k_cache.shape), tuple(q.shape)))
+        max_new, window = operator.index(max_new), operator.index(window)
         if any(not -_INT_MAX <= v <= _INT_MAX for v in (max_new, window)):
             raise ValueError("max_new and window are ints of 32 bits")
         q_ptr, q_ld = _heads(q, "q", _BF16, (T, n_q, D))
