@@ -373,7 +373,7 @@ moe_status_t moe_adapter_add(const moe_adapters_t* A, const uint16_t* x, int64_t
  * moe_requests_t: the T rows of a batch are the requests' new tokens one request after the other: request s has the
  *   rows [seg_offsets[s], seg_offsets[s+1]) (none, one or many) and kv_len[s] tokens with them, so its row i is at
  *   position kv_len[s] - n + i. Position p is in slot p % page_size of page pages[s * ld_pages + p / page_size].
- *   seg_offsets[0] = 0, non-decreasing, seg_offsets[S] <= T: rows behind the last request are left as they were.
+ *   1 <= S <= 2^30. seg_offsets[0] = 0, non-decreasing, seg_offsets[S] <= T: rows behind the last request are left as they were.
  *   A row at a negative position (kv_len < n, for example an idle slot of a batch with kv_len 0) has no place in the
  *   cache. What breaks these rules (offsets out of order or past T, kv_len < 0 or past max_pages * page_size) is
  *   skipped, its rows left as they were (of offsets out of order other requests' rows may be left, too);
@@ -409,8 +409,8 @@ typedef struct {
  *   q: bf16 [T][n_q][D], k and v: bf16 [T][n_kv][D]; ld_*: elements between two tokens, heads contiguous, every row on
  *   16 bytes (the three may be columns of one buffer). q_out: bf16 [T][n_q][D], may be q (the same address and row
  *   stride), no other overlap. n_q = 0: keys and values alone (q and q_out NULL). rot: a multiple of 16 in [0, D].
- *   1 <= n_kv <= 1024, n_q <= 1024. Keys and values share no element (they may lie by turns). Two rows with one place in the cache (a page shared by requests that both write
- *   to it) leave either's values there.
+ *   1 <= n_kv <= 1024, n_q <= 1024. Keys and values share no element (they may lie by turns). Two rows with one place in
+ *   the cache (a page shared by requests that both write to it) leave either's values there.
  *   ws: >= 256 bytes (status word). T = 0 returns MOE_OK after the shape check.
  * ------------------------------------------------------------------------------------------- */
 typedef struct {

@@ -10,6 +10,8 @@ using namespace moe;
 
 namespace {
 
+constexpr int kMaxRequests = 1 << 30;  // so that a search among them and a block of them a thread are counted in 32 bits
+
 moe_status_t check_cache(const moe_kv_cache_t* C, KvCache* c)
 {
     if (C->dtype != MOE_DTYPE_BF16 && C->dtype != MOE_DTYPE_E4M3) return fail(MOE_ERR_INVALID_ARG, "cache dtype=%d", C->dtype);
@@ -104,6 +106,7 @@ moe_status_t check_cache_memory(const moe_kv_cache_t* C)
 moe_status_t check_requests(const moe_requests_t* R, int page_size, int T, Requests* r)
 {
     if (R->S < 1) return fail(MOE_ERR_INVALID_ARG, "S=%d: no request holds the T=%d rows", R->S, T);
+    if (R->S > kMaxRequests) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "S=%d: more than 2^30", R->S);
     if (R->max_pages < 1) return fail(MOE_ERR_INVALID_ARG, "max_pages=%d < 1", R->max_pages);
     if (!R->seg_offsets || !R->kv_len || !R->pages) return fail(MOE_ERR_INVALID_ARG, "NULL table pointer");
     if (R->S > 1 && R->ld_pages < R->max_pages)
@@ -207,7 +210,7 @@ static moe_status_t check_attention(int n_q, int n_kv, int max_new)
 
 size_t moe_attention_workspace_bytes(int S, int n_q, int n_kv, int D, int max_new)
 {
-    if (S < 0 || n_kv < 1 || n_kv > 1024 || (D != 64 && D != 128 && D != 256) || check_attention(n_q, n_kv, max_new) != MOE_OK) return 0;
+    if (S < 0 || S > kMaxRequests || n_kv < 1 || n_kv > 1024 || (D != 64 && D != 128 && D != 256) || check_attention(n_q, n_kv, max_new) != MOE_OK) return 0;
     return attention_workspace_bytes(S, n_q, n_kv, D, max_new, device_sm_count());
 }
 
