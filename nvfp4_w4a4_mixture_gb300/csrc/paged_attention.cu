@@ -1,5 +1,7 @@
 // paged_attention.cu -- moe_paged_attention's workspace and the choice of its kernels (paged_attention.cuh), which are
 // compiled in a file for each type of cache and size of head.
+#include <mutex>
+
 #include "attention.cuh"
 
 namespace moe {
@@ -39,6 +41,10 @@ size_t attention_workspace_bytes(int S, int n_q, int n_kv, int D, int max_new, i
 
 cudaError_t launch_paged_attention(AttentionArgs a, void* ws, int sms, cudaStream_t stream)
 {
+    // Both launches of a call come one after the other: of two host threads that share a stream and a workspace, the join of
+    // one would read the parts of the other.
+    static std::mutex launches;
+    std::lock_guard<std::mutex> lock(launches);
     char* const base = static_cast<char*>(ws);
     const int rows = 8 * attention::row_eights(a.group, a.max_new);
     a.prefix = reinterpret_cast<int64_t*>(base + sizeof(WsHeader));
