@@ -405,10 +405,11 @@ typedef struct {
  *     the rot first elements are turned in pairs (a, b) = (u_i, u_{i + rot/2}), or (u_2i, u_2i+1) with interleaved:
  *     (a cos - b sin, a sin + b cos), angle p * inv_freq[i], i < rot/2; the others stay
  *   in FP32, rounded once: q_out = bf16, keys to the cache's type; values go there as they are. E4M3: the nearest code
- *   of x / scale, saturating at 448. Angles are exact to 2^-30 turns at any position.
+ *   of x / scale, saturating at 448. Angles are within 2^-26 turns at any position.
  *   q: bf16 [T][n_q][D], k and v: bf16 [T][n_kv][D]; ld_*: elements between two tokens, heads contiguous, every row on
  *   16 bytes (the three may be columns of one buffer). q_out: bf16 [T][n_q][D], may be q (the same address and row
- *   stride), no other overlap. n_q = 0: keys and values alone (q and q_out NULL). rot: a multiple of 16 in [0, D].
+ *   stride), no other overlap; of rows without a place in the cache and behind the last request it is not written. n_q = 0:
+ *   keys and values alone (q and q_out NULL). rot: a multiple of 16 in [0, D].
  *   1 <= n_kv <= 1024, n_q <= 1024. Keys and values share no element (they may lie by turns). Two rows with one place in
  *   the cache (a page shared by requests that both write to it) leave either's values there.
  *   ws: >= 256 bytes (status word). T = 0 returns MOE_OK after the shape check.

@@ -698,7 +698,9 @@ def moe_cache_append(q, k, v, k_cache, v_cache, seg_offsets, kv_len, pages, inv_
     v_cache: bf16 or float8_e4m3fn [n_pages, page_size, n_kv, D], strided as they like, heads contiguous; request s has
     the rows seg_offsets[s] .. seg_offsets[s + 1] (int32 [S + 1]), with them kv_len[s] tokens (int32 [S]) in the pages
     pages[s] (int32 [S, max_pages]). inv_freq: fp32 [rot / 2]; w_q, w_k: bf16 [D]; k_scale, v_scale: fp32 [n_kv] of an
-    8-bit cache. out: optional, may be q. Requests that break the rules are reported by moe_read_device_status(ws)."""
+    8-bit cache. out: optional, may be q; rows without a place in the cache (kv_len below the request's rows) and behind the last
+    request stay as they were in it, of an out that is allocated here they hold nothing of meaning. Requests that break the
+    rules are reported by moe_read_device_status(ws)."""
     if _lib is None:
         lib()
     if q is not None and out is None:

@@ -2,9 +2,9 @@
 //   u = x rsqrt(mean(x^2) + eps) (off + w);  (a, b) -> (a cos - b sin, a sin + b cos), angle p inv_freq[i]
 // A warp takes the heads of one token (of few tokens, some of them), 256 elements a pass: a head of D elements is in the
 // registers of D / 8 lanes (16 bytes each) from its load to its store, the norm's sum and the rotation's partner come by
-// shuffles. The angle is a 64-bit fraction of a turn: inv_freq / 2 pi in 2^-64
-// turns (one FP64 product, off by 2^-54 of it), times the position modulo 2^64, which drops whole turns exactly, so the
-// angle of position 2^20 is as good as that of position 1; sine and cosine of what is left are FP32's.
+// shuffles. The angle is a 64-bit fraction of a turn: inv_freq / 2 pi in 2^-64 turns (a product of integers, off by less
+// than one of them), times the position modulo 2^64, which drops whole turns exactly, so the angle of position 2^20 is as
+// good as that of position 1. What is left is rounded to FP32 (2^-26 turns at the most) for FP32's sine and cosine.
 #include "attention.cuh"
 
 namespace moe {
@@ -13,22 +13,6 @@ namespace {
 
 constexpr int kWarps = 4;
 
-// ---- two FP32 values an instruction
-__device__ __forceinline__ uint64_t pair(float lo, float hi) { return static_cast<uint64_t>(__float_as_uint(hi)) << 32 | __float_as_uint(lo); }
-__device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
-__device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
 // two bf16 values as FP32
 __device__ __forceinline__ uint64_t widen(uint32_t w) { return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }

@@ -11,16 +11,9 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ uint64_t pair(float lo, float hi) { return static_cast<uint64_t>(__float_as_uint(hi)) << 32 | __float_as_uint(lo); }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 __device__ __forceinline__ uint32_t codes_of_pair(uint64_t v)
 {
-    return ptx::cvt_e4m3x2(__uint_as_float(static_cast<uint32_t>(v)), __uint_as_float(static_cast<uint32_t>(v >> 32)));
+    return ptx::cvt_e4m3x2(lo_of(v), hi_of(v));
 }
 
 // kLanes lanes (8 or 16) take kBlocks blocks, kGroups apart, whose loads are in flight together; a lane has two pieces or one
