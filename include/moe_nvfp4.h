@@ -473,7 +473,7 @@ moe_status_t moe_quantize_fp8(const uint16_t* x, int64_t ld_x, int T, int K, uin
  *   out[t][n] = sum_b a_scale[t][b] b_scale[n / 128][b] sum_{k in block b} a[t][k] b[n][k]
  *   a: E4M3 [T][K], a_scale: FP32 [T][ceil(K / 128)] (moe_quantize_fp8's outputs); b: E4M3 [N][K], b_scale: FP32
  *   [ceil(N / 128)][ceil(K / 128)]. A block's products are summed in FP32 by the tensor cores, the blocks' sums are
- *   scaled and added in FP32. out: out_dtype (MOE_DTYPE_BF16 or MOE_DTYPE_F32) [T][N], rows ld_out elements apart, every
+ *   scaled by the product of their scales (an FP32 number, which keeps its bits from 2^-126 on) and added in FP32. out: out_dtype (MOE_DTYPE_BF16 or MOE_DTYPE_F32) [T][N], rows ld_out elements apart, every
  *   row on 16 bytes; it overlaps no input. K a multiple of 16 in [16, 65536], N a multiple of 8 in [8, 1048576]; the
  *   last blocks may be short. ws: >= 256 bytes (status word). T = 0 returns MOE_OK after the shape check.
  * ------------------------------------------------------------------------------------------- */

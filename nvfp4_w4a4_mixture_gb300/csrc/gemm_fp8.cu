@@ -9,9 +9,11 @@
 //                    weight once without padding; a cluster of CTAs shares a tile's blocks along K and adds the parts
 //                    through distributed shared memory, in the order of their ranks.
 // TMA fills the ragged ends of K, T and N with zeros.
-// Measured: 16,384 x 4,096 x 2,048 104 us, 2.6 PFLOP/s (70 % of twice the rate of bf16 matrix products). Without the sums
-// in registers it took 95 us, with the loads from tensor memory alone 93: the rest is the MMAs (512 cycles a block at their
-// nominal rate, some 850 here) and the sums' turn between them. Two values an instruction (fma.rn.f32x2: 123 us) and
+// Measured: 16,384 x 4,096 x 2,048 104 us, 2.6 PFLOP/s (70 % of twice the rate of bf16 matrix products), in bursts of some 20
+// calls; in hundreds on end, where the power limit holds the clock at 1.7 GHz instead of 2.07, 115 to 117 us (2.4, 69 % of
+// twice what bf16 sustains there). The variants that follow are bursts, too. Without the sums in registers it took 95 us, with
+// the loads from tensor memory alone 93: the rest is the MMAs (512 cycles a block at their nominal rate, some 850 here) and
+// the sums' turn between them. Two values an instruction (fma.rn.f32x2: 123 us) and
 // registers moved to the summing warps for two loads of 32 columns in flight (107) were slower. Pairs of multiprocessors on
 // one tile (cta_group::2, 256 x 256, half of A and of B each) took 104 to 106, too, with eight or sixteen summing warps and
 // two or four buffers: without the loads 98 to 101, without the sums 86, with neither 78, so the sums are what is left, while

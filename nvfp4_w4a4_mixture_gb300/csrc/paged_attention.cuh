@@ -11,8 +11,11 @@
 // one to four groups of four warps. Of a unit each warp of a group takes a quarter of the tokens for K Q^T, the four exchange
 // maxima and weights through shared memory, and each takes a quarter of the columns of V^T P^T, so the accumulators need no
 // join.
-// mma.sync with the tokens (and V's columns) on its M side: rows are padded to eight, not sixteen. The products are 4
-// flops a byte and row, for 8 rows 32 flops a byte: memory bounds them long before the tensor cores do.
+// mma.sync with the tokens (and V's columns) on its M side: rows are padded to eight, not sixteen. A token's keys and values
+// are 4 D bytes in bf16 (2 D in 8 bits) and take 6 D flops a row, the weights' two parts counted: 12 flops a byte for 8 rows
+// (24), 48 for 32 (96), at the memory's rate 80 to 640 TFLOP/s. More than 64 rows of a key head read K and V again for every 64
+// (16 requests of 16 tokens over to 4,000, 16 heads on 2 of 256: 69 us, their bytes in 11): decode steps and short windows are
+// what this is for.
 // Weights in the second product: of a bf16 cache two bf16 values (16 bits; one would add an error of the size of the output's
 // own rounding, three took 39.4 us for 36.2 in 200 windows of 1,024 and 133 for 116 with 128 rows a key head, for bits that
 // are 2^-8 of the output's rounding); of an E4M3 cache, whose codes become FP16 exactly, two FP16 values (22 bits) in parts of
@@ -20,10 +23,10 @@
 // way, 200 over to 2,000, 14 heads on 2 of 64, 22.0 and 20.8, 100 of four tokens over to 2,000, 32 on 4 of 128, 64.7 and 60.4.)
 // q of an E4M3 cache is scaled to FP16's range by a power of two a row (exact where q is not 2^-30 of the row's largest).
 // Measured: 64 requests of ragged lengths to 8,192, 32 heads on 8 of 128: 168 us, 6.2 TB/s (93 % of what a copy
-// reaches); one request over 300,001 tokens in 8 bits, 16 heads on 2 of 256: 60 us, 5.1 TB/s, 10 us of it the two launches,
-// the first loads and the join; 200 verify windows of one to three tokens, 14 heads on 2 of 64, window 1,024: 36 us, bound
-// by instruction issue (two thirds of the rows are padding); 4 tokens over 4,100, 16 heads on 2 of 256: 13 us, one unit's
-// chain and the join's.
+// reaches); one request over 300,001 tokens in 8 bits, 16 heads on 2 of 256: 58 us, 5.3 TB/s, 10 us of it the two launches,
+// the first loads and the join; 200 verify windows of one to three tokens, 14 heads on 2 of 64, window 1,024: 34 us, bound
+// by its groups' chains, two barriers and two ways through shared memory a unit (49 % of the issue slots and 15 % of the
+// tensor pipe are in use); 4 tokens over 4,100, 16 heads on 2 of 256: 12 us, one unit's chain and the join's.
 #pragma once
 #include <climits>
 
