@@ -250,7 +250,7 @@ def _adapter_workspace():
         w = Workspace(4096)
         if not torch.cuda.is_current_stream_capturing():
             torch.cuda.current_stream().synchronize()  # the header is zero for every stream from here on
-            _adapter_ws[dev] = w
+            w = _adapter_ws.setdefault(dev, w)  # (of two threads' first calls one gives the workspace of both)
         # a capture zeroes the header at each replay: its workspace belongs to the graph, and its report is lost
     return w
 

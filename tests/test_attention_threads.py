@@ -1,6 +1,7 @@
 """GPU: moe_paged_attention from several host threads on one stream, which share its scratch: the two launches of a call stay
 together."""
 import threading
+import time
 
 import pytest
 import torch
@@ -39,3 +40,27 @@ def test_threads_on_one_stream(m, side):  # noqa: F811
     m.moe_read_device_status()
     for _, want, outs in jobs:
         assert len(outs) == 200 and all(torch.equal(o, want) for o in outs)
+
+
+def test_first_calls_of_two_threads_report_to_one_place(m, monkeypatch):  # noqa: F811
+    made = m.Workspace
+
+    class Slow(made):
+        def __init__(self, *a, **kw):
+            super().__init__(*a, **kw)
+            time.sleep(0.05)
+
+    monkeypatch.setattr(m, "Workspace", Slow)
+    monkeypatch.setattr(m, "_adapter_ws", {})
+    got, go = [], threading.Barrier(4)
+
+    def work():
+        go.wait()
+        got.append(m._adapter_workspace())
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(got) == 4 and all(w is got[0] for w in got) and m._adapter_ws == {0: got[0]}
