@@ -123,6 +123,9 @@ __global__ void k_set_wait_hook(WsHeader* hdr, unsigned wait_us, int ready_extra
     hdr->test_ready_extra = ready_extra;
 }
 
+// moe_read_device_status: takes the bits that were read out of the status word; others may have come since
+__global__ void k_clear_status(WsHeader* hdr, int bits) { atomicAnd(&hdr->status, ~bits); }
+
 // one device staging buffer of moe_layer_forward_host: T x H bf16, 256-byte aligned
 size_t host_stage_bytes(int64_t H, int64_t T) { return (static_cast<size_t>(T * H * 2) + 255) & ~size_t(255); }
 
@@ -322,10 +325,14 @@ moe_status_t moe_read_device_status(void* ws, moe_stream_t stream)
 {
     if (!ws) return fail(MOE_ERR_INVALID_ARG, "workspace is NULL");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    int status = 0;  // read and cleared in the stream's order, and cleared when this returns
+    int status = 0;
     MOE_CUDA(cudaMemcpyAsync(&status, ws, sizeof(int), cudaMemcpyDeviceToHost, s), "read status");
-    MOE_CUDA(cudaMemsetAsync(ws, 0, sizeof(int), s), "clear status");
     MOE_CUDA(cudaStreamSynchronize(s), "cudaStreamSynchronize");
+    if (status) {  // cleared when this returns; a call on another stream may report in between
+        k_clear_status<<<1, 1, 0, s>>>(static_cast<WsHeader*>(ws), status);
+        MOE_CUDA(cudaGetLastError(), "clear status");
+        MOE_CUDA(cudaStreamSynchronize(s), "cudaStreamSynchronize");
+    }
     if (status & kDevTimeoutGemm) return fail(MOE_ERR_DEVICE_TIMEOUT, "device status 0x%x: grouped GEMM wait timed out", status);
     if (status & kDevTimeoutRouter) return fail(MOE_ERR_DEVICE_TIMEOUT, "device status 0x%x: router wait timed out", status);
     if (status & kDevTimeoutCombine) return fail(MOE_ERR_DEVICE_TIMEOUT, "device status 0x%x: combine wait timed out", status);
