@@ -442,7 +442,8 @@ moe_status_t moe_cache_append(const moe_kv_cache_t* C, const moe_requests_t* R, 
  *   reported. window: 0 for none.
  *   The cache's length is split over the multiprocessors, the parts joined in a second launch in a fixed order.
  *   ws: >= moe_attention_workspace_bytes(S, n_q, n_kv, D, max_new); with report it needs no zeroed header. Calls that may run
- *   at the same time need a ws each and may share a report; those of one stream may share a ws, also from several threads. T = 0 returns MOE_OK after the shape check.
+ *   at the same time need a ws each and may share a report (ws itself, or outside of it); those of one stream may share a
+ *   ws, also from several threads. T = 0 returns MOE_OK after the shape check.
  * ------------------------------------------------------------------------------------------- */
 typedef struct {
     int n_q, max_new, window;

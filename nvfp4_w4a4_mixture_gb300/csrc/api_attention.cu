@@ -243,6 +243,8 @@ moe_status_t moe_paged_attention(const moe_kv_cache_t* C, const moe_requests_t* 
         return fail(MOE_ERR_INVALID_ARG, "lse overlaps another argument");
     MOE_TRY(check_ws(ws, ws_bytes, sizeof(WsHeader)));
     if (A->report) MOE_TRY(check_ws(A->report, sizeof(WsHeader), sizeof(WsHeader)));
+    if (A->report != ws && rows_overlap_bytes(A->report, sizeof(WsHeader), sizeof(WsHeader), 1, ws, static_cast<int64_t>(ws_bytes)))
+        return fail(MOE_ERR_INVALID_ARG, "report lies in ws");
     MOE_TRY(check_device());
     const int sms = device_sm_count();
     MOE_TRY(check_ws(ws, ws_bytes, attention_workspace_bytes(R->S, A->n_q, C->n_kv, C->D, A->max_new, sms)));
